@@ -519,6 +519,167 @@ int tile_frag_mma(const void* a_image, const void* b_image, const float* c_image
 int tile_gemm_atom_select(int64_t M, int64_t N, int64_t K, int dtype, int transA, int transB,
                           int* shape);
 
+/* ---------------------------------------------------------------------------------------
+ * Operators of a transformer layer around the products: the product with scales, bias,
+ * activation and residual in its epilogue, its backward pass, the root-mean-square norm with
+ * the residual's addition (16-bit result, or 8 bits with scales for the products above and
+ * below) and its backward pass.  Conventions as for every entry point; in addition:
+ *   - leading dimensions count elements, 0 means packed; at least the row length, at most 2^40;
+ *   - pointers need only their element's alignment (16-byte aligned operands whose rows are
+ *     multiples of 16 bytes take the faster loads);
+ *   - outputs must not overlap inputs or each other except where a line below allows exactly the
+ *     same matrix (TG_E_ALIAS); two slices of one wider matrix (same leading dimension, disjoint
+ *     columns) do not overlap;
+ *   - workspaces are the caller's, need no initialisation, hold nothing between calls, and must
+ *     stay untouched until the call's work on `stream` is done.
+ * ------------------------------------------------------------------------------------- */
+typedef enum tg_act {
+  TG_ACT_NONE = 0,
+  TG_ACT_RELU = 1,       /* max(z, 0) */
+  TG_ACT_GELU = 2,       /* z·Phi(z), Phi the normal distribution (erf form) */
+  TG_ACT_GELU_TANH = 3,  /* z/2·(1 + tanh(sqrt(2/pi)·(z + 0.044715·z^3))) */
+  TG_ACT_SILU = 4        /* z/(1 + e^-z) */
+} tg_act;
+
+typedef struct tg_epilogue {
+  const void* bias;         /* [N] of bias_dtype, or NULL */
+  const void* residual;     /* [M,N] of d_dtype, leading dimension ld_residual, or NULL; may be
+                               exactly D */
+  void* Z;                  /* [M,N] of d_dtype, leading dimension ld_z: receives the
+                               activation's argument, or NULL */
+  const float* row_scale;   /* [M], or NULL */
+  const float* col_scale;   /* [N], or NULL */
+  int64_t ld_residual, ld_z;
+  int32_t bias_dtype;       /* TG_F16, TG_BF16 or TG_F32; read only with a bias */
+  int32_t act;              /* tg_act */
+} tg_epilogue;
+
+/* Kernel choice of tile_gemm_ep, reported by tile_gemm_ep_plan. */
+typedef enum tg_ep_kernel {
+  TG_EP_NONE = 0,     /* nothing to launch (M == 0 or N == 0) */
+  TG_EP_DIRECT = 1,   /* blocks, operands global -> LDS directly */
+  TG_EP_STAGED = 2,   /* blocks, operands through registers (any alignment) */
+  TG_EP_JOIN = 3,     /* K == 0: the epilogue of a zero product */
+  TG_EP_TOKENS = 4    /* few rows against a stream of weights */
+} tg_ep_kernel;
+
+typedef struct tg_ep_plan {
+  int32_t kernel;           /* tg_ep_kernel */
+  int32_t block_m, block_n, block_k;
+  int32_t splits;           /* parts of K summed by different workgroups (1: none) */
+  int32_t k_per_split;
+  int64_t grid;             /* workgroups */
+  int64_t workspace_bytes;  /* of the workspace this plan uses */
+} tg_ep_plan;
+
+/*
+ * tile_gemm_ep — D = act(Z) + residual,  Z[m][n] = row_scale[m]·col_scale[n]·(A·B)[m][n] + bias[n].
+ *
+ *   A, B    device, stored as tile_gemm's (transA, transB) with leading dimensions lda, ldb.
+ *           16-bit: a_dtype == b_dtype, TG_F16 or TG_BF16, any orientation.  fp8: each
+ *           TG_FP8_E4M3 or TG_FP8_E5M2, transA == 0 and transB == 1 (else TG_E_LAYOUT).
+ *   D       device [M,N] of d_dtype (TG_F16, TG_BF16 or TG_F32), leading dimension ldd.
+ *   M,N,K   any, 0 .. 2^30.  M == 0 or N == 0 is a no-op; K == 0 has A·B = 0.
+ *   ep      the epilogue, or NULL for none of it.
+ *   workspace, workspace_bytes   device, 16-byte aligned, or NULL and 0: problems with few output
+ *           tiles and a long K sum parts of K in different workgroups when the parts' fp32
+ *           sums fit here.  tile_gemm_ep_workspace says how much the best plan uses; with
+ *           less, fewer parts are made.
+ * The sum over K is held in fp32 (fp8: in the groups tile_gemm_fp8 describes), parts are added
+ * in their order, and Z and D are each rounded once from the fp32 value, so a call gives the same
+ * bits every time.  Returns TG_OK or a tg_status; asynchronous on `stream`.
+ */
+int tile_gemm_ep(const void* A, const void* B, void* D, int64_t M, int64_t N, int64_t K,
+                 int64_t lda, int64_t ldb, int64_t ldd, int transA, int transB, int a_dtype,
+                 int b_dtype, int d_dtype, const tg_epilogue* ep, void* workspace,
+                 int64_t workspace_bytes, void* stream);
+
+/* tile_gemm_ep_plan — host-only validation and kernel choice of tile_gemm_ep.  Needs no GPU. */
+int tile_gemm_ep_plan(const void* A, const void* B, const void* D, int64_t M, int64_t N, int64_t K,
+                      int64_t lda, int64_t ldb, int64_t ldd, int transA, int transB, int a_dtype,
+                      int b_dtype, int d_dtype, const tg_epilogue* ep, const void* workspace,
+                      int64_t workspace_bytes, tg_ep_plan* out);
+
+/* tile_gemm_ep_workspace — host-only: bytes of workspace the best plan of a problem uses (0: none,
+ * also for arguments tile_gemm_ep refuses). */
+int64_t tile_gemm_ep_workspace(int64_t M, int64_t N, int64_t K, int transA, int transB, int a_dtype);
+
+/*
+ * tile_gemm_ep_bwd — gradients of D = act(A·B + bias) + residual for the gradient dY of D:
+ *
+ *   dZ = dY·act'(Z)    dbias[n] = sum_m dZ[m][n]    dA = dZ·B^T    dB = A^T·dZ
+ *
+ * (the residual's gradient is dY itself).  Each of dA, dB, dbias is computed when not NULL.
+ *   dY      device [M,N] of dtype, leading dimension ld_dy.
+ *   Z       device [M,N] of dtype, leading dimension ld_z: what tile_gemm_ep stored; may be NULL
+ *           when act == TG_ACT_NONE.
+ *   A, B    as given to tile_gemm_ep, 16-bit (dtype TG_F16 or TG_BF16); A is read only for dB, B
+ *           only for dA.
+ *   dZ      device [M,N] of dtype, packed: written, and the operand of both products (rounded to
+ *           dtype as the matrix instructions take it).  May be NULL when act == TG_ACT_NONE: the
+ *           products then read dY.  May be exactly dY or exactly Z when that is packed.
+ *   dA, dB  device, dtype, packed, in A's and B's stored orientation.
+ *   dbias   device fp32 [N]: the sums of dZ before its rounding.
+ *   workspace   as for tile_gemm_ep; also holds the partial sums of dbias
+ *           (tile_gemm_ep_bwd_workspace).  Without one, dbias is summed by fewer workgroups.
+ */
+int tile_gemm_ep_bwd(const void* dY, const void* Z, const void* A, const void* B, void* dZ, void* dA,
+                     void* dB, float* dbias, int64_t M, int64_t N, int64_t K, int64_t ld_dy,
+                     int64_t ld_z, int64_t lda, int64_t ldb, int transA, int transB, int dtype,
+                     int act, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* tile_gemm_ep_bwd_workspace — host-only: bytes of workspace tile_gemm_ep_bwd uses at most. */
+int64_t tile_gemm_ep_bwd_workspace(int64_t M, int64_t N, int64_t K, int transA, int transB, int dtype);
+
+typedef enum tg_scale_kind {
+  TG_SCALE_NONE = 0,   /* Y in X's dtype */
+  TG_SCALE_ROW = 1,    /* Y in 8 bits, fp32 S[row] = max|Y[row]|/qmax: tile_gemm_ep's row_scale */
+  TG_SCALE_BLOCK = 2   /* Y in 8 bits, E8M0 bytes S[row][col/32]: the smallest power of two with
+                          max|Y of the 32 columns|/S <= qmax: tile_gemm_mx's SA */
+} tg_scale_kind;
+
+/*
+ * tile_rmsnorm — H = X + R,  rstd = 1/sqrt(mean(H^2) + eps) per row,  Y = H·rstd·W.
+ *
+ *   X       device [rows, cols] of dtype (TG_F16, TG_BF16 or TG_F32), leading dimension ld_x.
+ *   R       device, as X with ld_r, or NULL (H = X).  The sum is rounded to dtype before the norm
+ *           is taken: the norm is that of the stream that goes on.
+ *   W       device [cols] of w_dtype (dtype or TG_F32).
+ *   H       device, as X with ld_h, or NULL; only with R.  May be exactly X or exactly R.
+ *   Y       device [rows, cols] of y_dtype, leading dimension ld_y.  TG_SCALE_NONE: y_dtype ==
+ *           dtype.  Otherwise TG_FP8_E4M3 or TG_FP8_E5M2 holding Y/S rounded once (qmax 448 or
+ *           57344; nothing saturates), and max|Y| is taken as at least 2^-100.  A row or block
+ *           that holds a NaN or an infinity gets a NaN scale.
+ *   S       device scales, packed (see tg_scale_kind), or NULL for TG_SCALE_NONE.  TG_SCALE_BLOCK
+ *           needs cols % 32 == 0 (TG_E_SHAPE).
+ *   rstd    device fp32 [rows], or NULL: for the backward pass.
+ *   rows, cols   rows 0 .. 2^30, cols 1 .. 2^30 (rows == 0 is a no-op); eps >= 0.
+ */
+int tile_rmsnorm(const void* X, const void* R, const void* W, void* H, void* Y, void* S, float* rstd,
+                 int64_t rows, int64_t cols, int64_t ld_x, int64_t ld_r, int64_t ld_h, int64_t ld_y,
+                 float eps, int dtype, int w_dtype, int y_dtype, int scale_kind, void* stream);
+
+/*
+ * tile_rmsnorm_bwd — gradients of Y = H·rstd·W for the gradient dY of Y, with xh = H·rstd:
+ *
+ *   dX = rstd·(dY·W - xh·mean(dY·W·xh)) + dH     dW[c] = sum_rows dY·xh
+ *
+ *   dY, H, dX   device [rows, cols] of dtype with leading dimensions.  dX is the gradient of X and
+ *           of R; it may be exactly dY or exactly dH.
+ *   dH      device, as dY with ld_dh, or NULL: the gradient that arrives at H by the residual stream.
+ *   W, rstd as for tile_rmsnorm;  dW device fp32 [cols], or NULL.
+ *   workspace   device, 16-byte aligned, tile_rmsnorm_bwd_workspace bytes: partial sums of dW
+ *           (fewer bytes: fewer workgroups).  Rows of fewer than 8 or more than 16384 columns need
+ *           at least 4·rows bytes (TG_E_ARG).
+ */
+int tile_rmsnorm_bwd(const void* dY, const void* H, const void* W, const float* rstd, const void* dH,
+                     void* dX, float* dW, int64_t rows, int64_t cols, int64_t ld_dy, int64_t ld_h,
+                     int64_t ld_dh, int64_t ld_dx, int dtype, int w_dtype, void* workspace,
+                     int64_t workspace_bytes, void* stream);
+
+/* tile_rmsnorm_bwd_workspace — host-only. */
+int64_t tile_rmsnorm_bwd_workspace(int64_t rows, int64_t cols, int dtype);
+
 /* Reason for the last failure on the calling thread ("" after a success): the readable
  * reason a call was refused, as the dispatcher reports why no variant accepts a call
  * ([SYNC-GEMM] 二, the failure reasons of the dispatch; [VEC-AUTO] 接受什么输入).  The
@@ -528,7 +689,8 @@ const char* tile_last_error(void);
 /* Library ABI version (this header: 7; 2 added tile_gemm_fp8 and tile_gemm_fp8_plan, 3 added
  * tile_gemm_mx and tile_gemm_mx_plan, 4 the register fragment calls tile_frag_*, 5
  * tile_copy_async and tile_copy_async_plan, 6 the K = 8 / 16 atoms and tile_mma_select, 7
- * tile_gemm_atom_select and tg_gemm_plan.atom). */
+ * tile_gemm_atom_select and tg_gemm_plan.atom; tile_gemm_ep*, tile_rmsnorm* were added without
+ * changing any earlier call, and are found by their symbols). */
 int tile_abi_version(void);
 
 #ifdef __cplusplus

@@ -37,6 +37,9 @@ TG_GEMM_NONE, TG_GEMM_ATOM, TG_GEMM_TILED, TG_GEMM_FILL = 0, 1, 2, 3
  TG_FRAG_A16_32x32x8, TG_FRAG_B16_32x32x8, TG_FRAG_A16_16x16x16, TG_FRAG_B16_16x16x16) = range(1, 13)
 TG_FRAG_AUTO, TG_FRAG_DIRECT, TG_FRAG_LDS = 0, 1, 2
 TG_MMA_32x32x16, TG_MMA_16x16x32, TG_MMA_32x32x64_F8, TG_MMA_32x32x8, TG_MMA_16x16x16 = 1, 2, 3, 4, 5
+TG_ACT_NONE, TG_ACT_RELU, TG_ACT_GELU, TG_ACT_GELU_TANH, TG_ACT_SILU = 0, 1, 2, 3, 4
+TG_EP_NONE, TG_EP_DIRECT, TG_EP_STAGED, TG_EP_JOIN, TG_EP_TOKENS = 0, 1, 2, 3, 4
+TG_SCALE_NONE, TG_SCALE_ROW, TG_SCALE_BLOCK = 0, 1, 2
 
 STATUS_NAMES = {0: "TG_OK", -1: "TG_E_NULL", -2: "TG_E_SHAPE", -3: "TG_E_DTYPE", -4: "TG_E_BETA",
                 -5: "TG_E_ALIAS", -6: "TG_E_ALIGN", -7: "TG_E_THREADS", -8: "TG_E_LAYOUT",
@@ -99,6 +102,20 @@ class FragPlan(ctypes.Structure):
                 ("lds_bytes", ctypes.c_int32), ("tiles", ctypes.c_int64), ("grid", ctypes.c_int64)]
 
 
+class Epilogue(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("Z", ctypes.c_void_p),
+                ("row_scale", ctypes.c_void_p), ("col_scale", ctypes.c_void_p),
+                ("ld_residual", ctypes.c_int64), ("ld_z", ctypes.c_int64),
+                ("bias_dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
+class EpPlan(ctypes.Structure):
+    _fields_ = [("kernel", ctypes.c_int32), ("block_m", ctypes.c_int32), ("block_n", ctypes.c_int32),
+                ("block_k", ctypes.c_int32), ("splits", ctypes.c_int32),
+                ("k_per_split", ctypes.c_int32), ("grid", ctypes.c_int64),
+                ("workspace_bytes", ctypes.c_int64)]
+
+
 class TileError(RuntimeError):
     """A non-TG_OK status; .status holds the code, str() the library's reason."""
 
@@ -146,6 +163,20 @@ _SIGS = {
     "tile_copy_async_plan": (_INT, [_VP, _VP, ctypes.POINTER(_I64), _INT, ctypes.POINTER(Layout),
                                     ctypes.POINTER(Layout), ctypes.POINTER(AsyncOpts),
                                     ctypes.POINTER(AsyncPlan)]),
+    "tile_gemm_ep": (_INT, [_VP, _VP, _VP, _I64, _I64, _I64, _I64, _I64, _I64, _INT, _INT, _INT, _INT,
+                            _INT, ctypes.POINTER(Epilogue), _VP, _I64, _VP]),
+    "tile_gemm_ep_plan": (_INT, [_VP, _VP, _VP, _I64, _I64, _I64, _I64, _I64, _I64, _INT, _INT, _INT,
+                                 _INT, _INT, ctypes.POINTER(Epilogue), _VP, _I64,
+                                 ctypes.POINTER(EpPlan)]),
+    "tile_gemm_ep_workspace": (_I64, [_I64, _I64, _I64, _INT, _INT, _INT]),
+    "tile_gemm_ep_bwd": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _I64,
+                                _I64, _I64, _INT, _INT, _INT, _INT, _VP, _I64, _VP]),
+    "tile_gemm_ep_bwd_workspace": (_I64, [_I64, _I64, _I64, _INT, _INT, _INT]),
+    "tile_rmsnorm": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _I64, _I64, _F,
+                            _INT, _INT, _INT, _INT, _VP]),
+    "tile_rmsnorm_bwd": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _I64, _I64,
+                                _INT, _INT, _VP, _I64, _VP]),
+    "tile_rmsnorm_bwd_workspace": (_I64, [_I64, _I64, _INT]),
     "tile_last_error": (ctypes.c_char_p, []),
     "tile_abi_version": (_INT, []),
 }
@@ -481,3 +512,393 @@ def tile_gemm_atom_select(M, N, K, dtype, transA, transB):
     out = ctypes.c_int(0)
     _check(lib().tile_gemm_atom_select(M, N, K, int(dtype), int(transA), int(transB), ctypes.byref(out)))
     return out.value
+
+
+# ------------------------------------------------- transformer-layer operators ----
+#
+# The tile_* functions take the C ABI's arguments (leading dimensions given, so operands may be
+# slices of wider tensors); gemm_ep, gemm_ep_backward, rms_norm and rms_norm_backward take
+# tensors, allocate the results and the workspace on the call's stream and are what a model calls.
+
+ACTS = {"none": TG_ACT_NONE, "relu": TG_ACT_RELU, "gelu": TG_ACT_GELU,
+        "gelu_tanh": TG_ACT_GELU_TANH, "silu": TG_ACT_SILU}
+_FP8 = (TG_FP8_E4M3, TG_FP8_E5M2)
+
+
+def _span(rows, cols, ld, esize):
+    """Bytes a matrix with leading dimension `ld` (0: packed) spans from its first element."""
+    rows, cols = int(rows), int(cols)
+    return ((rows - 1) * (int(ld) or cols) + cols) * esize if rows > 0 and cols > 0 else 0
+
+
+def _room(t):
+    """Bytes from a tensor's first element to its last, gaps of a strided view included."""
+    if t.is_contiguous():
+        return t.numel() * t.element_size()
+    return (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+
+
+def _ptr(name, x, esize, nbytes, dev):
+    """Address of a tensor argument after the checks of _checked; a view may have gaps (its leading
+    dimension says so).  Returns (address, device)."""
+    if x is None or isinstance(x, int):
+        return x, dev
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor, an int address or None, got {type(x)}")
+    if not _on_gpu(x):
+        raise TileError(TG_E_ARG, f"{name} is on {x.device}, not on a GPU")
+    if dev is not None and x.device != dev:
+        raise TileError(TG_E_ARG, f"{name} is on {x.device}, the call's other tensors on {dev}")
+    if esize is not None and x.element_size() != esize:
+        raise TileError(TG_E_DTYPE, f"{name} has {x.element_size()}-byte elements, the call expects "
+                                    f"{esize}-byte elements")
+    if _room(x) < nbytes:
+        raise TileError(TG_E_SHAPE, f"{name} holds {_room(x)} bytes, the sizes need {nbytes}")
+    return x.data_ptr() or None, x.device
+
+
+def _ptrs(*args):
+    """Addresses of several tensor arguments: (name, value, element bytes or None, bytes)."""
+    dev, out = None, []
+    for name, x, esize, nbytes in args:
+        p, dev = _ptr(name, x, esize, nbytes, dev)
+        out.append(p)
+    return out
+
+
+def _ep_args(A, B, D, M, N, K, lda, ldb, ldd, transA, transB, a_dtype, b_dtype, d_dtype, bias, bias_dtype,
+             act, residual, ld_residual, Z, ld_z, row_scale, col_scale, workspace, workspace_bytes):
+    ea, eb, ed = ELEM_BYTES.get(int(a_dtype), 1), ELEM_BYTES.get(int(b_dtype), 1), ELEM_BYTES.get(int(d_dtype), 1)
+    if bias_dtype is None:
+        bias_dtype = TORCH_DTYPES.get(bias.dtype, 0) if isinstance(bias, torch.Tensor) else 0
+    if workspace is not None and workspace_bytes is None:
+        if not isinstance(workspace, torch.Tensor):
+            raise TileError(TG_E_ARG, "a workspace given by address needs workspace_bytes")
+        workspace_bytes = _room(workspace)
+    nb = int(workspace_bytes or 0)
+    pa, pb, pd, pbias, pres, pz, prs, pcs, pws = _ptrs(
+        ("A", A, ea, _span(K if transA else M, M if transA else K, lda, ea)),
+        ("B", B, eb, _span(N if transB else K, K if transB else N, ldb, eb)),
+        ("D", D, ed, _span(M, N, ldd, ed)),
+        ("bias", bias, None, max(int(N), 0) * ELEM_BYTES.get(int(bias_dtype), 1)),
+        ("residual", residual, ed, _span(M, N, ld_residual, ed)), ("Z", Z, ed, _span(M, N, ld_z, ed)),
+        ("row_scale", row_scale, 4, max(int(M), 0) * 4), ("col_scale", col_scale, 4, max(int(N), 0) * 4),
+        ("workspace", workspace, None, nb))
+    ep = Epilogue(pbias, pres, pz, prs, pcs, int(ld_residual), int(ld_z), int(bias_dtype), int(act))
+    return (pa, pb, pd, M, N, K, int(lda), int(ldb), int(ldd), int(transA), int(transB), int(a_dtype),
+            int(b_dtype), int(d_dtype), ctypes.byref(ep), pws, nb)
+
+
+def tile_gemm_ep(A, B, D, M, N, K, transA, transB, a_dtype, b_dtype, d_dtype, *, lda=0, ldb=0, ldd=0,
+                 bias=None, bias_dtype=None, act=TG_ACT_NONE, residual=None, ld_residual=0, Z=None, ld_z=0,
+                 row_scale=None, col_scale=None, workspace=None, workspace_bytes=None, stream=None):
+    """D = act(row_scale·col_scale·A·B + bias) + residual (see include/tilegemm.h)."""
+    args = _ep_args(A, B, D, M, N, K, lda, ldb, ldd, transA, transB, a_dtype, b_dtype, d_dtype, bias,
+                    bias_dtype, act, residual, ld_residual, Z, ld_z, row_scale, col_scale, workspace,
+                    workspace_bytes)
+    _check(lib().tile_gemm_ep(*args, _stream(stream)))
+
+
+def tile_gemm_ep_plan(A, B, D, M, N, K, transA, transB, a_dtype, b_dtype, d_dtype, *, lda=0, ldb=0, ldd=0,
+                      bias=None, bias_dtype=None, act=TG_ACT_NONE, residual=None, ld_residual=0, Z=None,
+                      ld_z=0, row_scale=None, col_scale=None, workspace=None, workspace_bytes=None):
+    """Host-only: the kernel tile_gemm_ep would run."""
+    args = _ep_args(A, B, D, M, N, K, lda, ldb, ldd, transA, transB, a_dtype, b_dtype, d_dtype, bias,
+                    bias_dtype, act, residual, ld_residual, Z, ld_z, row_scale, col_scale, workspace,
+                    workspace_bytes)
+    out = EpPlan()
+    _check(lib().tile_gemm_ep_plan(*args, ctypes.byref(out)))
+    return out
+
+
+def tile_gemm_ep_workspace(M, N, K, transA, transB, a_dtype):
+    """Workspace bytes of a problem's best plan."""
+    return lib().tile_gemm_ep_workspace(M, N, K, int(transA), int(transB), int(a_dtype))
+
+
+def tile_gemm_ep_bwd(dY, Z, A, B, dZ, dA, dB, dbias, M, N, K, transA, transB, dtype, act, *, ld_dy=0, ld_z=0,
+                     lda=0, ldb=0, workspace=None, workspace_bytes=None, stream=None):
+    """Gradients of tile_gemm_ep for 16-bit operands (see include/tilegemm.h)."""
+    e = ELEM_BYTES.get(int(dtype), 1)
+    m, n, k = max(int(M), 0), max(int(N), 0), max(int(K), 0)
+    if workspace is not None and workspace_bytes is None:
+        workspace_bytes = _room(workspace)
+    nb = int(workspace_bytes or 0)
+    p = _ptrs(("dY", dY, e, _span(m, n, ld_dy, e)), ("Z", Z, e, _span(m, n, ld_z, e)),
+              ("A", A, e, _span(k if transA else m, m if transA else k, lda, e)),
+              ("B", B, e, _span(n if transB else k, k if transB else n, ldb, e)),
+              ("dZ", dZ, e, m * n * e), ("dA", dA, e, m * k * e), ("dB", dB, e, k * n * e),
+              ("dbias", dbias, 4, n * 4), ("workspace", workspace, None, nb))
+    _check(lib().tile_gemm_ep_bwd(*p[:8], M, N, K, int(ld_dy), int(ld_z), int(lda), int(ldb), int(transA),
+                                  int(transB), int(dtype), int(act), p[8], nb, _stream(stream)))
+
+
+def tile_gemm_ep_bwd_workspace(M, N, K, transA, transB, dtype):
+    return lib().tile_gemm_ep_bwd_workspace(M, N, K, int(transA), int(transB), int(dtype))
+
+
+def tile_rmsnorm(X, R, W, H, Y, S, rstd, rows, cols, eps, dtype, w_dtype, y_dtype, scale_kind, *, ld_x=0,
+                 ld_r=0, ld_h=0, ld_y=0, stream=None):
+    """H = X + R, Y = H·rstd·W, optionally in 8 bits with scales S (see include/tilegemm.h)."""
+    e, ew, ey = ELEM_BYTES.get(int(dtype), 1), ELEM_BYTES.get(int(w_dtype), 1), ELEM_BYTES.get(int(y_dtype), 1)
+    m, n = max(int(rows), 0), max(int(cols), 0)
+    sb = m * 4 if int(scale_kind) == TG_SCALE_ROW else m * (n // 32) if int(scale_kind) == TG_SCALE_BLOCK else 0
+    p = _ptrs(("X", X, e, _span(m, n, ld_x, e)), ("R", R, e, _span(m, n, ld_r, e)), ("W", W, ew, n * ew),
+              ("H", H, e, _span(m, n, ld_h, e)), ("Y", Y, ey, _span(m, n, ld_y, ey)), ("S", S, None, sb),
+              ("rstd", rstd, 4, m * 4))
+    _check(lib().tile_rmsnorm(*p, rows, cols, int(ld_x), int(ld_r), int(ld_h), int(ld_y), float(eps),
+                              int(dtype), int(w_dtype), int(y_dtype), int(scale_kind), _stream(stream)))
+
+
+def tile_rmsnorm_bwd(dY, H, W, rstd, dH, dX, dW, rows, cols, dtype, w_dtype, *, ld_dy=0, ld_h=0, ld_dh=0,
+                     ld_dx=0, workspace=None, workspace_bytes=None, stream=None):
+    """Gradients of tile_rmsnorm (see include/tilegemm.h)."""
+    e, ew = ELEM_BYTES.get(int(dtype), 1), ELEM_BYTES.get(int(w_dtype), 1)
+    m, n = max(int(rows), 0), max(int(cols), 0)
+    if workspace is not None and workspace_bytes is None:
+        workspace_bytes = _room(workspace)
+    nb = int(workspace_bytes or 0)
+    p = _ptrs(("dY", dY, e, _span(m, n, ld_dy, e)), ("H", H, e, _span(m, n, ld_h, e)), ("W", W, ew, n * ew),
+              ("rstd", rstd, 4, m * 4), ("dH", dH, e, _span(m, n, ld_dh, e)),
+              ("dX", dX, e, _span(m, n, ld_dx, e)), ("dW", dW, 4, n * 4), ("workspace", workspace, None, nb))
+    _check(lib().tile_rmsnorm_bwd(*p[:7], rows, cols, int(ld_dy), int(ld_h), int(ld_dh), int(ld_dx),
+                                  int(dtype), int(w_dtype), p[7], nb, _stream(stream)))
+
+
+def tile_rmsnorm_bwd_workspace(rows, cols, dtype):
+    return lib().tile_rmsnorm_bwd_workspace(rows, cols, int(dtype))
+
+
+def _dtype(name, t):
+    code = TORCH_DTYPES.get(t)
+    if code is None:
+        raise TileError(TG_E_DTYPE, f"{name}: unsupported dtype {t}")
+    return code
+
+
+def _mat(name, t, rows=None, cols=None, dtype=None):
+    """Leading dimension of a matrix argument whose rows are contiguous; checks its shape and dtype."""
+    if t.dim() != 2:
+        raise TileError(TG_E_SHAPE, f"{name} must be a matrix, got {t.dim()} dimensions")
+    r, c = t.shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise TileError(TG_E_SHAPE, f"{name} must be ({rows}, {cols}), got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TileError(TG_E_DTYPE, f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise TileError(TG_E_ARG, f"{name} is on {t.device}, not on a GPU")
+    s0, s1 = t.stride()
+    if c > 1 and s1 != 1:
+        raise TileError(TG_E_LAYOUT, f"{name}: elements of a row must be contiguous (strides {(s0, s1)})")
+    if r <= 1:
+        return 0   # one row: the stride says nothing
+    if s0 < c:
+        raise TileError(TG_E_LAYOUT, f"{name}: rows overlap (strides {(s0, s1)})")
+    return s0
+
+
+def _vec(name, t, n, dtypes):
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise TileError(TG_E_SHAPE, f"{name} must be a contiguous vector of {n}, got {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise TileError(TG_E_DTYPE, f"{name} must be one of {dtypes}, got {t.dtype}")
+    if not t.is_cuda:
+        raise TileError(TG_E_ARG, f"{name} is on {t.device}, not on a GPU")
+
+
+def _one_gpu(*tensors):
+    """The GPU of a call's tensors, which has to be the current one: the launch goes there."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise TileError(TG_E_ARG, f"tensors on {dev} and {t.device}")
+    if dev.index != torch.cuda.current_device():
+        raise TileError(TG_E_ARG, f"tensors on {dev}, the current GPU is {torch.cuda.current_device()}")
+    return dev
+
+
+class _On:
+    """Allocations of a call belong to the stream its kernels run on: the caching allocator hands
+    freed workspace only to later work of the same stream."""
+
+    def __init__(self, stream):
+        self.ctx = None
+        if stream is not None:
+            s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+            self.ctx = torch.cuda.stream(s)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+_FLOATS = (torch.float16, torch.bfloat16, torch.float32)
+_F32 = (torch.float32,)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def gemm_ep(A, B, bias=None, act="none", residual=None, row_scale=None, col_scale=None, trans_a=False,
+            trans_b=True, out_dtype=None, keep_z=False, out=None, stream=None):
+    """D = act(row_scale·col_scale·A·B + bias) + residual; returns D, or (D, Z) with keep_z.
+
+    A is [M, K] ([K, M] with trans_a), B [N, K] as a linear layer's weight ([K, N] without trans_b);
+    rows may be slices of wider tensors.  out_dtype: the operands' type by default, bfloat16 for
+    fp8 operands.  residual and out have out_dtype; they may be the same tensor."""
+    ta, tb = bool(trans_a), bool(trans_b)
+    lda, ldb = _mat("A", A), _mat("B", B)
+    (K, M) = A.shape if ta else (A.shape[1], A.shape[0])
+    (N, kb) = B.shape if tb else (B.shape[1], B.shape[0])
+    if kb != K:
+        raise TileError(TG_E_SHAPE, f"A has K = {K}, B has K = {kb}")
+    at, bt = _dtype("A", A.dtype), _dtype("B", B.dtype)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.bfloat16 if at in _FP8 else A.dtype
+    dt = _dtype("out_dtype", out_dtype)
+    if act not in ACTS:
+        raise TileError(TG_E_ARG, f"unknown activation {act!r}")
+    ldr = ldd = 0
+    if bias is not None:
+        _vec("bias", bias, N, _FLOATS)
+    if residual is not None:
+        ldr = _mat("residual", residual, M, N, out_dtype)
+    if row_scale is not None:
+        _vec("row_scale", row_scale, M, _F32)
+    if col_scale is not None:
+        _vec("col_scale", col_scale, N, _F32)
+    if out is not None:
+        ldd = _mat("out", out, M, N, out_dtype)
+    dev = _one_gpu(A, B, bias, residual, row_scale, col_scale, out)
+    L = lib()
+    nb = L.tile_gemm_ep_workspace(M, N, K, ta, tb, at)
+    with _On(stream) as s:
+        if out is None:
+            out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        z = torch.empty((M, N), dtype=out_dtype, device=dev) if keep_z else None
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
+        ep = Epilogue(_address(bias), _address(residual), _address(z), _address(row_scale),
+                      _address(col_scale), ldr, 0, TORCH_DTYPES[bias.dtype] if bias is not None else 0,
+                      ACTS[act])
+        _check(L.tile_gemm_ep(A.data_ptr(), B.data_ptr(), out.data_ptr(), M, N, K, lda, ldb, ldd, ta, tb,
+                              at, bt, dt, ctypes.byref(ep), _address(ws), nb, s))
+    return (out, z) if keep_z else out
+
+
+def gemm_ep_backward(dY, A, B, Z=None, act="none", trans_a=False, trans_b=True, need_dA=True, need_dB=True,
+                     need_dbias=True, stream=None):
+    """Gradients of gemm_ep for 16-bit operands: (dZ, dA, dB, dbias), None for what is not needed.
+
+    Z is what gemm_ep returned with keep_z.  Without an activation dZ is dY itself.  dA and dB have
+    A's and B's stored orientation, dbias is float32; the residual's gradient is dY."""
+    ta, tb = bool(trans_a), bool(trans_b)
+    lda, ldb = _mat("A", A), _mat("B", B, dtype=A.dtype)
+    (K, M) = A.shape if ta else (A.shape[1], A.shape[0])
+    (N, kb) = B.shape if tb else (B.shape[1], B.shape[0])
+    if kb != K:
+        raise TileError(TG_E_SHAPE, f"A has K = {K}, B has K = {kb}")
+    if act not in ACTS:
+        raise TileError(TG_E_ARG, f"unknown activation {act!r}")
+    t = _dtype("A", A.dtype)
+    ldy = _mat("dY", dY, M, N, A.dtype)
+    ldz = 0
+    if act == "none":
+        Z = None
+    elif Z is None:
+        raise TileError(TG_E_NULL, "an activation's gradient needs Z")
+    else:
+        ldz = _mat("Z", Z, M, N, A.dtype)
+    dev = _one_gpu(dY, A, B, Z)
+    L = lib()
+    nb = L.tile_gemm_ep_bwd_workspace(M, N, K, ta, tb, t)
+    with _On(stream) as s:
+        dZ = torch.empty((M, N), dtype=A.dtype, device=dev) if act != "none" else None
+        dA = torch.empty(A.shape, dtype=A.dtype, device=dev) if need_dA else None
+        dB = torch.empty(B.shape, dtype=A.dtype, device=dev) if need_dB else None
+        dbias = torch.empty(N, dtype=torch.float32, device=dev) if need_dbias else None
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
+        _check(L.tile_gemm_ep_bwd(dY.data_ptr(), _address(Z), A.data_ptr(), B.data_ptr(), _address(dZ),
+                                  _address(dA), _address(dB), _address(dbias), M, N, K, ldy, ldz, lda, ldb,
+                                  ta, tb, t, ACTS[act], _address(ws), nb, s))
+    return (dZ if dZ is not None else dY), dA, dB, dbias
+
+
+class Norm:
+    """Result of rms_norm: y, scale (None without scales), rstd, h (the input without a residual)."""
+    __slots__ = ("y", "scale", "rstd", "h")
+
+    def __init__(self, y, scale, rstd, h):
+        self.y, self.scale, self.rstd, self.h = y, scale, rstd, h
+
+
+def rms_norm(X, weight, eps=1e-5, residual=None, out_dtype=None, scales=None, h_out=None, stream=None):
+    """h = X + residual, y = h·rstd·weight; returns a Norm.
+
+    scales None: y in X's dtype.  "row": y in 8 bits (out_dtype, float8_e4m3fn by default) with one
+    float32 scale a row, gemm_ep's row_scale.  "block": with an E8M0 scale per 32 columns,
+    tile_gemm_mx's SA.  h_out may be X or residual (in place)."""
+    ldx = _mat("X", X)
+    rows, cols = X.shape
+    kind = {None: TG_SCALE_NONE, "row": TG_SCALE_ROW, "block": TG_SCALE_BLOCK}.get(scales)
+    if kind is None:
+        raise TileError(TG_E_ARG, f"scales must be None, 'row' or 'block', got {scales!r}")
+    if out_dtype is None:
+        out_dtype = X.dtype if scales is None else torch.float8_e4m3fn
+    t, yt = _dtype("X", X.dtype), _dtype("out_dtype", out_dtype)
+    _vec("weight", weight, cols, (X.dtype, torch.float32))
+    ldr = ldh = 0
+    if residual is not None:
+        ldr = _mat("residual", residual, rows, cols, X.dtype)
+    elif h_out is not None:
+        raise TileError(TG_E_ARG, "h_out is the sum X + residual: it needs a residual")
+    if h_out is not None:
+        ldh = _mat("h_out", h_out, rows, cols, X.dtype)
+    dev = _one_gpu(X, weight, residual, h_out)
+    L = lib()
+    with _On(stream) as s:
+        h = h_out
+        if h is None and residual is not None:
+            h = torch.empty((rows, cols), dtype=X.dtype, device=dev)
+        y = torch.empty((rows, cols), dtype=out_dtype, device=dev)
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+        sc = None
+        if scales == "row":
+            sc = torch.empty(rows, dtype=torch.float32, device=dev)
+        elif scales == "block":
+            sc = torch.empty((rows, cols // 32), dtype=torch.float8_e8m0fnu, device=dev)
+        _check(L.tile_rmsnorm(X.data_ptr(), _address(residual), weight.data_ptr(), _address(h), y.data_ptr(),
+                              _address(sc), rstd.data_ptr(), rows, cols, ldx, ldr, ldh, 0, eps, t,
+                              TORCH_DTYPES[weight.dtype], yt, kind, s))
+    return Norm(y, sc, rstd, X if residual is None else h)
+
+
+def rms_norm_backward(dY, h, weight, rstd, dH=None, need_dw=True, stream=None):
+    """Gradients of rms_norm: (dX, dweight).  dX is the gradient of X and of the residual; dH, if
+    given, is the gradient that arrives at h by the residual stream.  dweight is float32 or None."""
+    ldh = _mat("h", h)
+    rows, cols = h.shape
+    t = _dtype("h", h.dtype)
+    ldy = _mat("dY", dY, rows, cols, h.dtype)
+    _vec("weight", weight, cols, (h.dtype, torch.float32))
+    _vec("rstd", rstd, rows, _F32)
+    ldd = _mat("dH", dH, rows, cols, h.dtype) if dH is not None else 0
+    dev = _one_gpu(dY, h, weight, rstd, dH)
+    L = lib()
+    nb = L.tile_rmsnorm_bwd_workspace(rows, cols, t)
+    with _On(stream) as s:
+        dX = torch.empty((rows, cols), dtype=h.dtype, device=dev)
+        dw = torch.empty(cols, dtype=torch.float32, device=dev) if need_dw else None
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
+        _check(L.tile_rmsnorm_bwd(dY.data_ptr(), h.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
+                                  _address(dH), dX.data_ptr(), _address(dw), rows, cols, ldy, ldh, ldd, 0, t,
+                                  TORCH_DTYPES[weight.dtype], _address(ws), nb, s))
+    return dX, dw

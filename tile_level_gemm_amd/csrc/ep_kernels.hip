@@ -1,0 +1,107 @@
+// The kernels around the product with an epilogue that are not block kernels: the join of a split
+// sum, the activation's gradient with the bias gradient, and the sum of partial rows.
+#include "ep.h"
+
+namespace tg {
+namespace {
+
+// D from `splits` partial sums, added in their order (0 of them: P = 0, the K == 0 product).
+// 8 columns per thread; bound by the partial sums' bytes, which the block kernels have just
+// written.
+__global__ __launch_bounds__(256) void ep_join(EpArgs g, int64_t chunks) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= chunks) return;
+  const int per_row = (g.N + 7) / 8;
+  const int row = (int)(i / per_row), col = (int)(i % per_row) * 8;
+  EpCols cols;
+  ep_cols(g, col, cols);
+  float v[8] = {};
+  const float* p = g.part + (int64_t)row * g.part_ld + col;
+  for (int s = 0; s < g.splits; ++s, p += (int64_t)g.M * g.part_ld) {
+    const float4 a = *(const float4*)p, b = *(const float4*)(p + 4);
+    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+  }
+  ep_finish8(g, row, col, cols, v);
+}
+
+// dZ = dY·act'(Z), and the column sums of dZ (before its rounding) over the workgroup's rows.
+// 256 columns x rows_per rows per workgroup: 32 lanes of 8 columns, 8 rows at a time.  One pass
+// over dY and Z, bound by memory.
+__global__ __launch_bounds__(256) void act_grad(ActGradArgs a) {
+  __shared__ float red[8][256 + 8];
+  const int lane = (int)threadIdx.x & 31, rl = (int)threadIdx.x >> 5;
+  const int col = (int)blockIdx.x * 256 + lane * 8, n = a.N - col;
+  const int64_t r0 = (int64_t)blockIdx.y * a.rows_per;
+  const int64_t r1 = min((int64_t)a.M, r0 + a.rows_per);
+  float sum[8] = {};
+  if (n > 0)
+    for (int64_t r = r0 + rl; r < r1; r += 8) {
+      float dy[8];
+      ep_get8(a.dY, a.t, r * a.ldy + col, n, dy);
+      if (a.act != TG_ACT_NONE) {
+        float z[8];
+        ep_get8(a.Z, a.t, r * a.ldz + col, n, z);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dy[e] *= ep_act_grad(z[e], a.act);
+      }
+      if (a.dZ) ep_put8(a.dZ, a.t, r * a.N + col, n, dy);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += dy[e];
+    }
+  if (!a.sums) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) red[rl][lane * 8 + e] = sum[e];
+  __syncthreads();
+  const int c = (int)threadIdx.x, gc = (int)blockIdx.x * 256 + c;
+  if (gc < a.N) {
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += red[k][c];
+    a.sums[(int64_t)blockIdx.y * a.N + gc] = s;
+  }
+}
+
+// out[n] = sum over g of part[g][n]: 64 columns x 4 interleaved row lanes per workgroup, joined in
+// LDS, always in the same order.
+__global__ __launch_bounds__(256) void sum_rows(const float* part, int64_t G, int64_t N, float* out) {
+  __shared__ float red[4][64];
+  const int c = (int)threadIdx.x & 63, l = (int)threadIdx.x >> 6;
+  const int64_t n = (int64_t)blockIdx.x * 64 + c;
+  float s = 0.0f;
+  if (n < N) {
+    const float* p = part + (int64_t)l * N + n;
+#pragma unroll 8
+    for (int64_t g = l; g < G; g += 4, p += 4 * N) s += *p;
+  }
+  red[l][c] = s;
+  __syncthreads();
+  if (l == 0 && n < N) out[n] = (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
+}
+
+}  // namespace
+
+hipError_t launch_ep_join(const EpArgs& g, hipStream_t s) {
+  const int64_t chunks = (int64_t)g.M * ((g.N + 7) / 8);
+  hipLaunchKernelGGL(ep_join, dim3((unsigned)((chunks + 255) / 256)), dim3(256), 0, s, g, chunks);
+  return hipGetLastError();
+}
+
+hipError_t launch_act_grad(const ActGradArgs& a, int groups, hipStream_t s) {
+  hipLaunchKernelGGL(act_grad, dim3((unsigned)((a.N + 255) / 256), (unsigned)groups), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_sum_rows(const float* part, int64_t G, int64_t N, float* out, hipStream_t s) {
+  hipLaunchKernelGGL(sum_rows, dim3((unsigned)((N + 63) / 64)), dim3(256), 0, s, part, G, N, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_ep_block(const EpArgs& g, int trans_a, int trans_b, int a_dtype, int b_dtype, int bs,
+                           bool staged, hipStream_t s) {
+  if (a_dtype == TG_FP8_E4M3 || a_dtype == TG_FP8_E5M2) return launch_ep_fp8(g, a_dtype, b_dtype, bs, staged, s);
+  if (trans_a) return trans_b ? launch_ep_mk(g, a_dtype, bs, staged, s) : launch_ep_mm(g, a_dtype, bs, staged, s);
+  return trans_b ? launch_ep_kk(g, a_dtype, bs, staged, s) : launch_ep_km(g, a_dtype, bs, staged, s);
+}
+
+}  // namespace tg

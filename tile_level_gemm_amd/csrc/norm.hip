@@ -1,0 +1,434 @@
+// Root-mean-square norm with the residual's addition, and its backward pass.
+//
+//   H = X + R (rounded to X's type: it is the residual stream the next layer reads, and the
+//   norm is taken of what that layer will see)   rstd = 1/sqrt(mean(H²) + eps)   Y = H·rstd·w
+//   8-bit Y: row scale s = max|Y|/qmax, or per 32 columns the smallest power of two s with
+//   max|Y|/s <= qmax, so nothing saturates; Q = Y/s rounded once.  max|Y| is floored at 2^-100.
+//   backward: g = dY·w, xh = H·rstd, dX = rstd·(g − xh·mean(g·xh)) + dH, dw = Σ_rows dY·xh.
+//
+// All of it is bound by memory: one pass, the row kept in registers between the reduction and
+// the result (TPR threads per row x NV chunks of 8 columns).  Rows up to 1024 columns take one
+// wave each and no barrier; longer ones a workgroup.  The sum of squares and max|H·w| (a row
+// scale needs it: max|Y| = rstd·max|H·w|) travel in one reduction.
+// Rows whose length is not a multiple of 8 end in a chunk moved back to the row's last 8
+// columns: every load is a whole vector, the columns another chunk owns (`dup` of them) are left
+// out of the sums, and both owners store the same values.
+#include "ep.h"
+#include "norm.h"
+
+namespace tg {
+namespace {
+
+constexpr float kAmaxFloor = 7.888609052210118e-31f;   // 2^-100
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+  return v;
+}
+// max that keeps NaN: a NaN in the row reaches its scale
+__device__ __forceinline__ float nan_max(float a, float b) { return a != a || a > b ? a : b; }
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v = nan_max(v, __shfl_xor(v, m));
+  return v;
+}
+
+// 8 values to 8-bit floats; |v| <= qmax up to rounding, clamped there; NaN stays NaN
+__device__ __forceinline__ uint2 quant8(const float (&v)[8], int t) {
+  const float q = t == TG_FP8_E4M3 ? 448.0f : 57344.0f;
+  float c[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) c[e] = v[e] != v[e] ? v[e] : fminf(fmaxf(v[e], -q), q);
+  int lo = 0, hi = 0;
+  if (t == TG_FP8_E4M3) {
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], lo, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], lo, true);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(c[4], c[5], hi, false);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(c[6], c[7], hi, true);
+  } else {
+    lo = __builtin_amdgcn_cvt_pk_bf8_f32(c[0], c[1], lo, false);
+    lo = __builtin_amdgcn_cvt_pk_bf8_f32(c[2], c[3], lo, true);
+    hi = __builtin_amdgcn_cvt_pk_bf8_f32(c[4], c[5], hi, false);
+    hi = __builtin_amdgcn_cvt_pk_bf8_f32(c[6], c[7], hi, true);
+  }
+  return uint2{(uint32_t)lo, (uint32_t)hi};
+}
+typedef __attribute__((ext_vector_type(2))) uint32_t ep_u32x2;
+struct __attribute__((packed, aligned(1))) Bytes8 { ep_u32x2 v; };
+
+__device__ __forceinline__ void put_q8(uint8_t* p, int n, uint2 q) {
+  if (n >= 8) {
+    ((Bytes8*)p)->v = ep_u32x2{q.x, q.y};
+  } else {
+    for (int e = 0; e < n; ++e) p[e] = (uint8_t)((e < 4 ? q.x >> (8 * e) : q.y >> (8 * (e - 4))));
+  }
+}
+
+// Exponent e of the smallest power of two with amax/2^e <= 1.75·2^top (448 = 1.75·2^8, 57344 =
+// 1.75·2^15): the exponent of amax less `top`, one more when its fraction is above 1.75.
+__device__ __forceinline__ int block_exp(float amax, int t) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, amax);
+  return (int)((b + 0x1fffffu) >> 23) - 127 - (t == TG_FP8_E4M3 ? 8 : 15);
+}
+
+// Reduce (sum, max) over TPR threads; every thread gets the result.  red: one slot per wave.
+template <int TPR>
+__device__ __forceinline__ void row_reduce(float& s, float& m, bool want_max, float (*red)[2]) {
+  s = wave_sum(s);
+  if (want_max) m = wave_max(m);
+  if constexpr (TPR > 64) {
+    const int w = (int)threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+      red[w][0] = s;
+      red[w][1] = m;
+    }
+    __syncthreads();
+    s = 0.0f;
+    m = red[0][1];
+#pragma unroll
+    for (int i = 0; i < TPR / 64; ++i) {
+      s += red[i][0];
+      if (want_max) m = nan_max(m, red[i][1]);
+    }
+  }
+}
+
+// SC: tg_scale_kind of the result
+template <int DT, int TPR, int NV, int SC>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm(NormArgs a) {
+  __shared__ float red[TPR > 64 ? TPR / 64 : 1][2];
+  const int t = (int)threadIdx.x % TPR;
+  const int64_t row = TPR == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
+  if (TPR == 64 && row >= a.rows) return;
+  const int cols = (int)a.cols;
+  float h[NV][8], w[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) ep_get8(a.X, DT, row * a.ldx + min((j * TPR + t) * 8, cols - 8), 8, h[j]);
+  if (a.R) {
+    float r[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) ep_get8(a.R, DT, row * a.ldr + min((j * TPR + t) * 8, cols - 8), 8, r[j]);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = h[j][e] + r[j][e];
+        if constexpr (DT == TG_BF16) h[j][e] = (float)(__bf16)x;
+        else if constexpr (DT == TG_F16) h[j][e] = (float)(_Float16)x;
+        else h[j][e] = x;
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int col = min((j * TPR + t) * 8, cols - 8);
+    if (a.w_t == TG_F32) ep_get8(a.W, TG_F32, col, 8, w[j]);
+    else ep_get8(a.W, DT, col, 8, w[j]);
+  }
+  float ss = 0.0f, top = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int dup = (j * TPR + t) * 8 - (cols - 8);   // columns another chunk owns (8 or more: all)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = e >= dup ? h[j][e] : 0.0f;
+      ss += x * x;
+      if constexpr (SC == TG_SCALE_ROW) top = nan_max(top, fabsf(h[j][e] * w[j][e]));
+    }
+  }
+  row_reduce<TPR>(ss, top, SC == TG_SCALE_ROW, red);
+  const float rstd = 1.0f / sqrtf(ss / (float)cols + a.eps);
+  float inv = 1.0f;
+  if constexpr (SC == TG_SCALE_ROW) {
+    const float q = a.y_t == TG_FP8_E4M3 ? 448.0f : 57344.0f;
+    const float amax = nan_max(top * rstd, kAmaxFloor);
+    inv = q / amax;
+    if (t == 0) ((float*)a.S)[row] = amax / q;
+  }
+  if (a.rstd && t == 0) a.rstd[row] = rstd;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int at = (j * TPR + t) * 8, col = min(at, cols - 8);
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = h[j][e] * rstd * w[j][e];
+    if constexpr (SC == TG_SCALE_BLOCK) {   // cols % 32 == 0: a block is 4 adjacent lanes' chunks
+      float m = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = nan_max(m, fabsf(y[e]));
+      m = nan_max(m, __shfl_xor(m, 1));
+      m = nan_max(m, __shfl_xor(m, 2));
+      m = nan_max(m, kAmaxFloor);
+      const bool fine = m < __builtin_inff();
+      const int x = block_exp(m, a.y_t);
+      inv = fine ? __builtin_ldexpf(1.0f, -x) : __builtin_nanf("");
+      if (at < cols && (t & 3) == 0) a.S[row * (a.cols / 32) + at / 32] = fine ? (uint8_t)(x + 127) : 255;
+    }
+    if (at >= cols) continue;
+    if (a.H) ep_put8(a.H, DT, row * a.ldh + col, 8, h[j]);
+    if constexpr (SC == TG_SCALE_NONE) {
+      ep_put8(a.Y, DT, row * a.ldy + col, 8, y);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] *= inv;
+      put_q8(a.Y + row * a.ldy + col, 8, quant8(y, a.y_t));
+    }
+  }
+}
+
+// Rows outside 8 .. kNormRegCols columns: one workgroup per row, which reads the row twice (the
+// second time from the caches).
+template <int DT, int SC>
+__global__ __launch_bounds__(1024) void rmsnorm_long(NormArgs a) {
+  __shared__ float red[16][2];
+  const int64_t row = blockIdx.x;
+  auto get = [&](int64_t col, int n, float (&h)[8], float (&w)[8]) {
+    ep_get8(a.X, DT, row * a.ldx + col, n, h);
+    if (a.R) {
+      float r[8];
+      ep_get8(a.R, DT, row * a.ldr + col, n, r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = h[e] + r[e];
+        if constexpr (DT == TG_BF16) h[e] = (float)(__bf16)x;
+        else if constexpr (DT == TG_F16) h[e] = (float)(_Float16)x;
+        else h[e] = x;
+      }
+    }
+    if (a.w_t == TG_F32) ep_get8(a.W, TG_F32, col, n, w);
+    else ep_get8(a.W, DT, col, n, w);
+  };
+  float ss = 0.0f, top = 0.0f, h[8], w[8];
+  for (int64_t col = (int64_t)threadIdx.x * 8; col < a.cols; col += 8192) {
+    get(col, (int)min((int64_t)8, a.cols - col), h, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {   // elements past the row are 0
+      ss += h[e] * h[e];
+      if constexpr (SC == TG_SCALE_ROW) top = nan_max(top, fabsf(h[e] * w[e]));
+    }
+  }
+  row_reduce<1024>(ss, top, SC == TG_SCALE_ROW, red);
+  const float rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
+  float inv = 1.0f;
+  if constexpr (SC == TG_SCALE_ROW) {
+    const float q = a.y_t == TG_FP8_E4M3 ? 448.0f : 57344.0f;
+    const float amax = nan_max(top * rstd, kAmaxFloor);
+    inv = q / amax;
+    if (threadIdx.x == 0) ((float*)a.S)[row] = amax / q;
+  }
+  if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+  // whole waves take the shuffles: the bound is rounded up to a wave's 512 columns
+  for (int64_t col = (int64_t)threadIdx.x * 8; col < (a.cols + 511) / 512 * 512; col += 8192) {
+    const int n = (int)max((int64_t)0, min((int64_t)8, a.cols - col));
+    float y[8] = {};
+    if (n > 0) {
+      get(col, n, h, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = h[e] * rstd * w[e];
+    }
+    if constexpr (SC == TG_SCALE_BLOCK) {
+      float m = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = nan_max(m, fabsf(y[e]));
+      m = nan_max(m, __shfl_xor(m, 1));
+      m = nan_max(m, __shfl_xor(m, 2));
+      m = nan_max(m, kAmaxFloor);
+      const bool fine = m < __builtin_inff();
+      const int x = block_exp(m, a.y_t);
+      inv = fine ? __builtin_ldexpf(1.0f, -x) : __builtin_nanf("");
+      if (n > 0 && (threadIdx.x & 3) == 0)
+        a.S[row * (a.cols / 32) + col / 32] = fine ? (uint8_t)(x + 127) : 255;
+    }
+    if (n == 0) continue;
+    if (a.H) ep_put8(a.H, DT, row * a.ldh + col, n, h);
+    if constexpr (SC == TG_SCALE_NONE) {
+      ep_put8(a.Y, DT, row * a.ldy + col, n, y);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] *= inv;
+      put_q8(a.Y + row * a.ldy + col, n, quant8(y, a.y_t));
+    }
+  }
+}
+
+// ---- backward --------------------------------------------------------------------------------
+// A workgroup walks rows blockIdx.x, + gridDim.x, … (four at a time with one wave per row) and
+// keeps its share of dw in registers; the shares are written once per workgroup and summed by
+// sum_rows, so the order is fixed.
+template <int DT, int TPR, int NV>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_bwd(NormBwdArgs a) {
+  constexpr int RPB = TPR == 64 ? 4 : 1;
+  __shared__ float red[2][TPR > 64 ? TPR / 64 : 1][2];
+  const int t = (int)threadIdx.x % TPR;
+  const int cols = (int)a.cols;
+  float w[NV][8], dw[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int col = min((j * TPR + t) * 8, cols - 8);
+    if (a.w_t == TG_F32) ep_get8(a.W, TG_F32, col, 8, w[j]);
+    else ep_get8(a.W, DT, col, 8, w[j]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[j][e] = 0.0f;
+  }
+  int par = 0;
+  for (int64_t row = (int64_t)blockIdx.x * RPB + (RPB > 1 ? threadIdx.x >> 6 : 0); row < a.rows;
+       row += (int64_t)gridDim.x * RPB, par ^= 1) {
+    float dy[NV][8], h[NV][8], dh[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int col = min((j * TPR + t) * 8, cols - 8);
+      ep_get8(a.dY, DT, row * a.ldy + col, 8, dy[j]);
+      ep_get8(a.H, DT, row * a.ldh + col, 8, h[j]);
+    }
+    if (a.dH) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) ep_get8(a.dH, DT, row * a.ldd + min((j * TPR + t) * 8, cols - 8), 8, dh[j]);
+    }
+    const float rstd = a.rstd[row];
+    float dot = 0.0f, none = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int dup = (j * TPR + t) * 8 - (cols - 8);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = dy[j][e] * (h[j][e] * rstd);   // dY·xh
+        dw[j][e] += x;
+        dot += e >= dup ? x * w[j][e] : 0.0f;
+      }
+    }
+    row_reduce<TPR>(dot, none, false, red[par]);
+    const float c = dot / (float)cols;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int at = (j * TPR + t) * 8, col = min(at, cols - 8);
+      float dx[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        dx[e] = rstd * (dy[j][e] * w[j][e] - h[j][e] * rstd * c);
+        if (a.dH) dx[e] += dh[j][e];
+      }
+      if (at < cols) ep_put8(a.dX, DT, row * a.ldx + col, 8, dx);
+    }
+  }
+  if (!a.dw) return;
+  if constexpr (TPR == 64) {
+    // the four waves' shares, joined in LDS
+    __shared__ float part[4][NV * 512];
+    const int wv = (int)threadIdx.x >> 6;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) part[wv][(j * 8 + e) * 64 + t] = dw[j][e];
+    __syncthreads();
+    if (wv != 0) return;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = (j * 8 + e) * 64 + t;
+        dw[j][e] = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int at = (j * TPR + t) * 8;
+    if (at < cols)   // a moved chunk's duplicated columns hold the same sums as their owner's
+      ep_put8((uint8_t*)a.dw, TG_F32, (int64_t)blockIdx.x * a.cols + min(at, cols - 8), 8, dw[j]);
+  }
+}
+
+// Rows outside the register kernel's range: mean(g·xh) of each row first ...
+template <int DT>
+__global__ __launch_bounds__(1024) void rmsnorm_bwd_dot(NormBwdArgs a) {
+  __shared__ float red[16][2];
+  const int64_t row = blockIdx.x;
+  const float rstd = a.rstd[row];
+  float dot = 0.0f, none = 0.0f;
+  for (int64_t col = (int64_t)threadIdx.x * 8; col < a.cols; col += 8192) {
+    const int n = (int)min((int64_t)8, a.cols - col);
+    float dy[8], h[8], w[8];
+    ep_get8(a.dY, DT, row * a.ldy + col, n, dy);
+    ep_get8(a.H, DT, row * a.ldh + col, n, h);
+    if (a.w_t == TG_F32) ep_get8(a.W, TG_F32, col, n, w);
+    else ep_get8(a.W, DT, col, n, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dot += dy[e] * (h[e] * rstd) * w[e];
+  }
+  row_reduce<1024>(dot, none, false, red);
+  if (threadIdx.x == 0) a.dot[row] = dot / (float)a.cols;
+}
+// ... then dX and dw by panels of 2048 columns (blockIdx.y), rows shared over blockIdx.x.
+template <int DT>
+__global__ __launch_bounds__(256) void rmsnorm_bwd_panel(NormBwdArgs a) {
+  const int64_t col = (int64_t)blockIdx.y * 2048 + threadIdx.x * 8;
+  if (col >= a.cols) return;
+  const int n = (int)min((int64_t)8, a.cols - col);
+  float w[8], dw[8] = {};
+  if (a.w_t == TG_F32) ep_get8(a.W, TG_F32, col, n, w);
+  else ep_get8(a.W, DT, col, n, w);
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const float rstd = a.rstd[row], c = a.dot[row];
+    float dy[8], h[8], dx[8];
+    ep_get8(a.dY, DT, row * a.ldy + col, n, dy);
+    ep_get8(a.H, DT, row * a.ldh + col, n, h);
+    if (a.dH) ep_get8(a.dH, DT, row * a.ldd + col, n, dx);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float xh = h[e] * rstd;
+      dw[e] += dy[e] * xh;
+      dx[e] = rstd * (dy[e] * w[e] - xh * c) + (a.dH ? dx[e] : 0.0f);
+    }
+    ep_put8(a.dX, DT, row * a.ldx + col, n, dx);
+  }
+  if (a.dw) ep_put8((uint8_t*)a.dw, TG_F32, (int64_t)blockIdx.x * a.cols + col, n, dw);
+}
+
+template <int DT, int SC>
+hipError_t go_fwd(const NormArgs& a, hipStream_t s) {
+  const dim3 rows((unsigned)a.rows), waves((unsigned)((a.rows + 3) / 4));
+  if (!norm_in_registers(a.cols)) hipLaunchKernelGGL((rmsnorm_long<DT, SC>), rows, dim3(1024), 0, s, a);
+  else if (a.cols <= 512) hipLaunchKernelGGL((rmsnorm<DT, 64, 1, SC>), waves, dim3(256), 0, s, a);
+  else if (a.cols <= 1024) hipLaunchKernelGGL((rmsnorm<DT, 64, 2, SC>), waves, dim3(256), 0, s, a);
+  else if (a.cols <= 2048) hipLaunchKernelGGL((rmsnorm<DT, 256, 1, SC>), rows, dim3(256), 0, s, a);
+  else if (a.cols <= 4096) hipLaunchKernelGGL((rmsnorm<DT, 256, 2, SC>), rows, dim3(256), 0, s, a);
+  else if (a.cols <= 8192) hipLaunchKernelGGL((rmsnorm<DT, 256, 4, SC>), rows, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((rmsnorm<DT, 1024, 2, SC>), rows, dim3(1024), 0, s, a);
+  return hipGetLastError();
+}
+template <int DT>
+hipError_t go_fwd(const NormArgs& a, int sc, hipStream_t s) {
+  if (sc == TG_SCALE_ROW) return go_fwd<DT, TG_SCALE_ROW>(a, s);
+  if (sc == TG_SCALE_BLOCK) return go_fwd<DT, TG_SCALE_BLOCK>(a, s);
+  return go_fwd<DT, TG_SCALE_NONE>(a, s);
+}
+template <int DT>
+hipError_t go_bwd(const NormBwdArgs& a, int64_t groups, hipStream_t s) {
+  const dim3 g((unsigned)groups);
+  if (!norm_in_registers(a.cols)) {
+    hipLaunchKernelGGL((rmsnorm_bwd_dot<DT>), dim3((unsigned)a.rows), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL((rmsnorm_bwd_panel<DT>), dim3((unsigned)groups, (unsigned)((a.cols + 2047) / 2048)),
+                       dim3(256), 0, s, a);
+  } else if (a.cols <= 512) hipLaunchKernelGGL((rmsnorm_bwd<DT, 64, 1>), g, dim3(256), 0, s, a);
+  else if (a.cols <= 1024) hipLaunchKernelGGL((rmsnorm_bwd<DT, 64, 2>), g, dim3(256), 0, s, a);
+  else if (a.cols <= 2048) hipLaunchKernelGGL((rmsnorm_bwd<DT, 256, 1>), g, dim3(256), 0, s, a);
+  else if (a.cols <= 4096) hipLaunchKernelGGL((rmsnorm_bwd<DT, 256, 2>), g, dim3(256), 0, s, a);
+  else if (a.cols <= 8192) hipLaunchKernelGGL((rmsnorm_bwd<DT, 256, 4>), g, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((rmsnorm_bwd<DT, 1024, 2>), g, dim3(1024), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const NormArgs& a, int dtype, int scale_kind, hipStream_t s) {
+  if (dtype == TG_F32) return go_fwd<TG_F32>(a, scale_kind, s);
+  if (dtype == TG_F16) return go_fwd<TG_F16>(a, scale_kind, s);
+  return go_fwd<TG_BF16>(a, scale_kind, s);
+}
+
+hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int dtype, int64_t groups, hipStream_t s) {
+  if (dtype == TG_F32) return go_bwd<TG_F32>(a, groups, s);
+  if (dtype == TG_F16) return go_bwd<TG_F16>(a, groups, s);
+  return go_bwd<TG_BF16>(a, groups, s);
+}
+
+}  // namespace tg
