@@ -307,7 +307,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_bwd(NormBwdArgs
         dx[e] = rstd * (dy[j][e] * w[j][e] - h[j][e] * rstd * c);
         if (a.dH) dx[e] += dh[j][e];
       }
-      if (at < cols) ep_put8(a.dX, DT, row * a.ldx + col, 8, dx);
+      // dX may be dH, whose loads no barrier waits for: a moved chunk stores only its own columns
+      if (at + 8 <= cols) {
+        ep_put8(a.dX, DT, row * a.ldx + col, 8, dx);
+      } else if (at < cols) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e >= at - col) ep_put(a.dX, DT, row * a.ldx + col + e, dx[e]);
+      }
     }
   }
   if (!a.dw) return;
