@@ -518,7 +518,8 @@ def tile_gemm_atom_select(M, N, K, dtype, transA, transB):
 #
 # The tile_* functions take the C ABI's arguments (leading dimensions given, so operands may be
 # slices of wider tensors); gemm_ep, gemm_ep_backward, rms_norm and rms_norm_backward take
-# tensors, allocate the results and the workspace on the call's stream and are what a model calls.
+# tensors, allocate the results and the workspace on the call's stream and are what a model calls:
+# their checks and allocations are native (csrc/tensor_calls.cpp).
 
 ACTS = {"none": TG_ACT_NONE, "relu": TG_ACT_RELU, "gelu": TG_ACT_GELU,
         "gelu_tanh": TG_ACT_GELU_TANH, "silu": TG_ACT_SILU}
@@ -669,57 +670,6 @@ def tile_rmsnorm_bwd_workspace(rows, cols, dtype):
     return lib().tile_rmsnorm_bwd_workspace(rows, cols, int(dtype))
 
 
-def _dtype(name, t):
-    code = TORCH_DTYPES.get(t)
-    if code is None:
-        raise TileError(TG_E_DTYPE, f"{name}: unsupported dtype {t}")
-    return code
-
-
-def _mat(name, t, rows=None, cols=None, dtype=None):
-    """Leading dimension of a matrix argument whose rows are contiguous; checks its shape and dtype."""
-    if t.dim() != 2:
-        raise TileError(TG_E_SHAPE, f"{name} must be a matrix, got {t.dim()} dimensions")
-    r, c = t.shape
-    if (rows is not None and r != rows) or (cols is not None and c != cols):
-        raise TileError(TG_E_SHAPE, f"{name} must be ({rows}, {cols}), got {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise TileError(TG_E_DTYPE, f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise TileError(TG_E_ARG, f"{name} is on {t.device}, not on a GPU")
-    s0, s1 = t.stride()
-    if c > 1 and s1 != 1:
-        raise TileError(TG_E_LAYOUT, f"{name}: elements of a row must be contiguous (strides {(s0, s1)})")
-    if r <= 1:
-        return 0   # one row: the stride says nothing
-    if s0 < c:
-        raise TileError(TG_E_LAYOUT, f"{name}: rows overlap (strides {(s0, s1)})")
-    return s0
-
-
-def _vec(name, t, n, dtypes):
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise TileError(TG_E_SHAPE, f"{name} must be a contiguous vector of {n}, got {tuple(t.shape)}")
-    if t.dtype not in dtypes:
-        raise TileError(TG_E_DTYPE, f"{name} must be one of {dtypes}, got {t.dtype}")
-    if not t.is_cuda:
-        raise TileError(TG_E_ARG, f"{name} is on {t.device}, not on a GPU")
-
-
-def _one_gpu(*tensors):
-    """The GPU of a call's tensors, which has to be the current one: the launch goes there."""
-    dev = None
-    for t in tensors:
-        if t is not None:
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise TileError(TG_E_ARG, f"tensors on {dev} and {t.device}")
-    if dev.index != torch.cuda.current_device():
-        raise TileError(TG_E_ARG, f"tensors on {dev}, the current GPU is {torch.cuda.current_device()}")
-    return dev
-
-
 class _On:
     """Allocations of a call belong to the stream its kernels run on: the caching allocator hands
     freed workspace only to later work of the same stream."""
@@ -740,12 +690,28 @@ class _On:
             self.ctx.__exit__(*exc)
 
 
-_FLOATS = (torch.float16, torch.bfloat16, torch.float32)
-_F32 = (torch.float32,)
+_calls = None
 
 
-def _address(t):
-    return None if t is None else t.data_ptr()
+def _native():
+    """The tensor calls' native module; raises if it has not been built (no fallback exists)."""
+    global _calls
+    if _calls is None:
+        lib()
+        try:
+            from . import _tensor_calls
+        except ImportError as e:
+            raise ImportError(f"{e}; run `python -m tile_level_gemm_amd.build`") from e
+        _tensor_calls.set_error_class(TileError)
+        _calls = _tensor_calls
+    return _calls
+
+
+def _act(act):
+    code = ACTS.get(act)
+    if code is None:
+        raise TileError(TG_E_ARG, f"unknown activation {act!r}")
+    return code
 
 
 def gemm_ep(A, B, bias=None, act="none", residual=None, row_scale=None, col_scale=None, trans_a=False,
@@ -755,43 +721,11 @@ def gemm_ep(A, B, bias=None, act="none", residual=None, row_scale=None, col_scal
     A is [M, K] ([K, M] with trans_a), B [N, K] as a linear layer's weight ([K, N] without trans_b);
     rows may be slices of wider tensors.  out_dtype: the operands' type by default, bfloat16 for
     fp8 operands.  residual and out have out_dtype; they may be the same tensor."""
-    ta, tb = bool(trans_a), bool(trans_b)
-    lda, ldb = _mat("A", A), _mat("B", B)
-    (K, M) = A.shape if ta else (A.shape[1], A.shape[0])
-    (N, kb) = B.shape if tb else (B.shape[1], B.shape[0])
-    if kb != K:
-        raise TileError(TG_E_SHAPE, f"A has K = {K}, B has K = {kb}")
-    at, bt = _dtype("A", A.dtype), _dtype("B", B.dtype)
-    if out_dtype is None:
-        out_dtype = out.dtype if out is not None else torch.bfloat16 if at in _FP8 else A.dtype
-    dt = _dtype("out_dtype", out_dtype)
-    if act not in ACTS:
-        raise TileError(TG_E_ARG, f"unknown activation {act!r}")
-    ldr = ldd = 0
-    if bias is not None:
-        _vec("bias", bias, N, _FLOATS)
-    if residual is not None:
-        ldr = _mat("residual", residual, M, N, out_dtype)
-    if row_scale is not None:
-        _vec("row_scale", row_scale, M, _F32)
-    if col_scale is not None:
-        _vec("col_scale", col_scale, N, _F32)
-    if out is not None:
-        ldd = _mat("out", out, M, N, out_dtype)
-    dev = _one_gpu(A, B, bias, residual, row_scale, col_scale, out)
-    L = lib()
-    nb = L.tile_gemm_ep_workspace(M, N, K, ta, tb, at)
-    with _On(stream) as s:
-        if out is None:
-            out = torch.empty((M, N), dtype=out_dtype, device=dev)
-        z = torch.empty((M, N), dtype=out_dtype, device=dev) if keep_z else None
-        ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
-        ep = Epilogue(_address(bias), _address(residual), _address(z), _address(row_scale),
-                      _address(col_scale), ldr, 0, TORCH_DTYPES[bias.dtype] if bias is not None else 0,
-                      ACTS[act])
-        _check(L.tile_gemm_ep(A.data_ptr(), B.data_ptr(), out.data_ptr(), M, N, K, lda, ldb, ldd, ta, tb,
-                              at, bt, dt, ctypes.byref(ep), _address(ws), nb, s))
-    return (out, z) if keep_z else out
+    if stream is not None:
+        with _On(stream):
+            return gemm_ep(A, B, bias, act, residual, row_scale, col_scale, trans_a, trans_b, out_dtype, keep_z, out)
+    return (_calls or _native()).gemm_ep(A, B, bias, _act(act), residual, row_scale, col_scale, trans_a, trans_b,
+                                         out_dtype, keep_z, out)
 
 
 def gemm_ep_backward(dY, A, B, Z=None, act="none", trans_a=False, trans_b=True, need_dA=True, need_dB=True,
@@ -800,36 +734,11 @@ def gemm_ep_backward(dY, A, B, Z=None, act="none", trans_a=False, trans_b=True, 
 
     Z is what gemm_ep returned with keep_z.  Without an activation dZ is dY itself.  dA and dB have
     A's and B's stored orientation, dbias is float32; the residual's gradient is dY."""
-    ta, tb = bool(trans_a), bool(trans_b)
-    lda, ldb = _mat("A", A), _mat("B", B, dtype=A.dtype)
-    (K, M) = A.shape if ta else (A.shape[1], A.shape[0])
-    (N, kb) = B.shape if tb else (B.shape[1], B.shape[0])
-    if kb != K:
-        raise TileError(TG_E_SHAPE, f"A has K = {K}, B has K = {kb}")
-    if act not in ACTS:
-        raise TileError(TG_E_ARG, f"unknown activation {act!r}")
-    t = _dtype("A", A.dtype)
-    ldy = _mat("dY", dY, M, N, A.dtype)
-    ldz = 0
-    if act == "none":
-        Z = None
-    elif Z is None:
-        raise TileError(TG_E_NULL, "an activation's gradient needs Z")
-    else:
-        ldz = _mat("Z", Z, M, N, A.dtype)
-    dev = _one_gpu(dY, A, B, Z)
-    L = lib()
-    nb = L.tile_gemm_ep_bwd_workspace(M, N, K, ta, tb, t)
-    with _On(stream) as s:
-        dZ = torch.empty((M, N), dtype=A.dtype, device=dev) if act != "none" else None
-        dA = torch.empty(A.shape, dtype=A.dtype, device=dev) if need_dA else None
-        dB = torch.empty(B.shape, dtype=A.dtype, device=dev) if need_dB else None
-        dbias = torch.empty(N, dtype=torch.float32, device=dev) if need_dbias else None
-        ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
-        _check(L.tile_gemm_ep_bwd(dY.data_ptr(), _address(Z), A.data_ptr(), B.data_ptr(), _address(dZ),
-                                  _address(dA), _address(dB), _address(dbias), M, N, K, ldy, ldz, lda, ldb,
-                                  ta, tb, t, ACTS[act], _address(ws), nb, s))
-    return (dZ if dZ is not None else dY), dA, dB, dbias
+    if stream is not None:
+        with _On(stream):
+            return gemm_ep_backward(dY, A, B, Z, act, trans_a, trans_b, need_dA, need_dB, need_dbias)
+    return (_calls or _native()).gemm_ep_backward(dY, A, B, Z, _act(act), trans_a, trans_b, need_dA, need_dB,
+                                                  need_dbias)
 
 
 class Norm:
@@ -840,65 +749,28 @@ class Norm:
         self.y, self.scale, self.rstd, self.h = y, scale, rstd, h
 
 
+_SCALES = {None: TG_SCALE_NONE, "row": TG_SCALE_ROW, "block": TG_SCALE_BLOCK}
+
+
 def rms_norm(X, weight, eps=1e-5, residual=None, out_dtype=None, scales=None, h_out=None, stream=None):
     """h = X + residual, y = h·rstd·weight; returns a Norm.
 
     scales None: y in X's dtype.  "row": y in 8 bits (out_dtype, float8_e4m3fn by default) with one
     float32 scale a row, gemm_ep's row_scale.  "block": with an E8M0 scale per 32 columns,
     tile_gemm_mx's SA.  h_out may be X or residual (in place)."""
-    ldx = _mat("X", X)
-    rows, cols = X.shape
-    kind = {None: TG_SCALE_NONE, "row": TG_SCALE_ROW, "block": TG_SCALE_BLOCK}.get(scales)
+    if stream is not None:
+        with _On(stream):
+            return rms_norm(X, weight, eps, residual, out_dtype, scales, h_out)
+    kind = _SCALES.get(scales)
     if kind is None:
         raise TileError(TG_E_ARG, f"scales must be None, 'row' or 'block', got {scales!r}")
-    if out_dtype is None:
-        out_dtype = X.dtype if scales is None else torch.float8_e4m3fn
-    t, yt = _dtype("X", X.dtype), _dtype("out_dtype", out_dtype)
-    _vec("weight", weight, cols, (X.dtype, torch.float32))
-    ldr = ldh = 0
-    if residual is not None:
-        ldr = _mat("residual", residual, rows, cols, X.dtype)
-    elif h_out is not None:
-        raise TileError(TG_E_ARG, "h_out is the sum X + residual: it needs a residual")
-    if h_out is not None:
-        ldh = _mat("h_out", h_out, rows, cols, X.dtype)
-    dev = _one_gpu(X, weight, residual, h_out)
-    L = lib()
-    with _On(stream) as s:
-        h = h_out
-        if h is None and residual is not None:
-            h = torch.empty((rows, cols), dtype=X.dtype, device=dev)
-        y = torch.empty((rows, cols), dtype=out_dtype, device=dev)
-        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-        sc = None
-        if scales == "row":
-            sc = torch.empty(rows, dtype=torch.float32, device=dev)
-        elif scales == "block":
-            sc = torch.empty((rows, cols // 32), dtype=torch.float8_e8m0fnu, device=dev)
-        _check(L.tile_rmsnorm(X.data_ptr(), _address(residual), weight.data_ptr(), _address(h), y.data_ptr(),
-                              _address(sc), rstd.data_ptr(), rows, cols, ldx, ldr, ldh, 0, eps, t,
-                              TORCH_DTYPES[weight.dtype], yt, kind, s))
-    return Norm(y, sc, rstd, X if residual is None else h)
+    return Norm(*(_calls or _native()).rms_norm(X, weight, eps, residual, out_dtype, kind, h_out))
 
 
 def rms_norm_backward(dY, h, weight, rstd, dH=None, need_dw=True, stream=None):
     """Gradients of rms_norm: (dX, dweight).  dX is the gradient of X and of the residual; dH, if
     given, is the gradient that arrives at h by the residual stream.  dweight is float32 or None."""
-    ldh = _mat("h", h)
-    rows, cols = h.shape
-    t = _dtype("h", h.dtype)
-    ldy = _mat("dY", dY, rows, cols, h.dtype)
-    _vec("weight", weight, cols, (h.dtype, torch.float32))
-    _vec("rstd", rstd, rows, _F32)
-    ldd = _mat("dH", dH, rows, cols, h.dtype) if dH is not None else 0
-    dev = _one_gpu(dY, h, weight, rstd, dH)
-    L = lib()
-    nb = L.tile_rmsnorm_bwd_workspace(rows, cols, t)
-    with _On(stream) as s:
-        dX = torch.empty((rows, cols), dtype=h.dtype, device=dev)
-        dw = torch.empty(cols, dtype=torch.float32, device=dev) if need_dw else None
-        ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
-        _check(L.tile_rmsnorm_bwd(dY.data_ptr(), h.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
-                                  _address(dH), dX.data_ptr(), _address(dw), rows, cols, ldy, ldh, ldd, 0, t,
-                                  TORCH_DTYPES[weight.dtype], _address(ws), nb, s))
-    return dX, dw
+    if stream is not None:
+        with _On(stream):
+            return rms_norm_backward(dY, h, weight, rstd, dH, need_dw)
+    return (_calls or _native()).rms_norm_backward(dY, h, weight, rstd, dH, need_dw)

@@ -3,18 +3,21 @@
     python -m tile_level_gemm_amd.build
 
 Objects go to tile_level_gemm_amd/_build/ (git-ignored); the library lands next to
-this file so that it travels with the source tree.
+this file so that it travels with the source tree, and so does the module of the tensor calls
+(_tensor_calls.so, host code against torch's headers, linked to the library beside it).
 """
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtilegemm.so")
+CALLS = os.path.join(HERE, "_tensor_calls.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["abi.cpp", "plan.cpp", "copy_kernels.hip", "gemm_kernels.hip", "gemm_direct.hip",
@@ -46,17 +49,41 @@ def _compile(src):
     return obj
 
 
-def build(jobs=8):
-    """Compile every source and link libtilegemm.so; returns the library path."""
-    os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=jobs) as ex:
-        objs = list(ex.map(_compile, SOURCES))
-    tmp = LIB + ".tmp"
-    cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
+def _run(what, cmd):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
+        raise RuntimeError(f"{what} failed:\n{r.stderr}")
+
+
+def _compile_calls():
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    obj = os.path.join(BUILD, "tensor_calls.cpp.o")
+    _run("g++ on tensor_calls.cpp",
+         ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-I", os.path.join(HERE, "..", "include"), "-isystem", sysconfig.get_paths()["include"],
+          "-isystem", os.path.join(root, "include"), "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+          "-isystem", "/opt/rocm/include", "-c", os.path.join(CSRC, "tensor_calls.cpp"), "-o", obj])
+    return obj, os.path.join(root, "lib")
+
+
+def build(jobs=8):
+    """Compile every source, link libtilegemm.so and _tensor_calls.so; returns the library path."""
+    os.makedirs(BUILD, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=jobs) as ex:
+        calls = ex.submit(_compile_calls)
+        objs = list(ex.map(_compile, SOURCES))
+        obj, torch_lib = calls.result()
+    tmp = LIB + ".tmp"
+    _run("link", [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-Wl,-soname,libtilegemm.so", "-o", tmp] + objs)
     os.replace(tmp, LIB)
+    tmp = CALLS + ".tmp"
+    # torch is imported before the module, so its own rpath finds torch's libraries
+    _run("link of _tensor_calls", ["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:libtilegemm.so", "-L", torch_lib,
+                                   "-ltorch_python", "-ltorch_hip", "-ltorch_cpu", "-lc10_hip", "-lc10",
+                                   "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, CALLS)
     return LIB
 
 

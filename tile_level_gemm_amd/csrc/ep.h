@@ -3,11 +3,13 @@
 //   P = A·B (fp32 sums)   Z = row_scale[m]·col_scale[n]·P + bias[n]   D = act(Z) + residual
 //
 // Every kernel that finishes an output element (the block kernels, the token kernels and the join
-// of a split sum) goes through ep_finish, so all of them round once: Z and D are each
+// of a split sum) goes through ep_finish8, so all of them round once: Z and D are each
 // rounded to d_dtype from the fp32 value.  Internal header.
 #pragma once
 
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "tg_internal.h"
 
@@ -71,7 +73,13 @@ typedef __attribute__((ext_vector_type(2))) float ep_f32x2;
 
 struct __attribute__((packed, aligned(1))) Bytes16 { ep_u32x4 v; };
 __device__ __forceinline__ ep_u32x4 load16(const void* p) { return ((const Bytes16*)p)->v; }
-__device__ __forceinline__ void store16(void* p, ep_u32x4 v) { ((Bytes16*)p)->v = v; }
+typedef ep_u32x4 __attribute__((aligned(1))) ep_u32x4_any;
+// NT: a result that nothing here reads again streams past the L2, where the operands stay
+template <bool NT = false>
+__device__ __forceinline__ void store16(void* p, ep_u32x4 v) {
+  if constexpr (NT) __builtin_nontemporal_store(v, (ep_u32x4_any*)p);
+  else ((Bytes16*)p)->v = v;
+}
 
 __device__ __forceinline__ float ep_get(const uint8_t* p, int t, int64_t i) {
   if (t == TG_F32) return ((const float*)p)[i];
@@ -82,6 +90,21 @@ __device__ __forceinline__ void ep_put(uint8_t* p, int t, int64_t i, float v) {
   if (t == TG_F32) ((float*)p)[i] = v;
   else if (t == TG_BF16) ((__bf16*)p)[i] = (__bf16)v;
   else ((_Float16*)p)[i] = (_Float16)v;
+}
+// 8 16-bit elements
+__device__ __forceinline__ void ep_unpack8(int t, ep_u32x4 a, float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t w = a[e];
+    if (t == TG_BF16) {
+      v[2 * e] = __builtin_bit_cast(float, w << 16);
+      v[2 * e + 1] = __builtin_bit_cast(float, w & 0xffff0000u);
+    } else {
+      const ep_f16x2 h = __builtin_bit_cast(ep_f16x2, w);
+      v[2 * e] = (float)h[0];
+      v[2 * e + 1] = (float)h[1];
+    }
+  }
 }
 // n >= 1 valid elements of 8
 __device__ __forceinline__ void ep_get8(const uint8_t* p, int t, int64_t i, int n, float (&v)[8]) {
@@ -94,19 +117,7 @@ __device__ __forceinline__ void ep_get8(const uint8_t* p, int t, int64_t i, int 
         v[4 + e] = __builtin_bit_cast(float, (uint32_t)b[e]);
       }
     } else {
-      const ep_u32x4 a = load16(p + 2 * i);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t w = a[e];
-        if (t == TG_BF16) {
-          v[2 * e] = __builtin_bit_cast(float, w << 16);
-          v[2 * e + 1] = __builtin_bit_cast(float, w & 0xffff0000u);
-        } else {
-          const ep_f16x2 h = __builtin_bit_cast(ep_f16x2, w);
-          v[2 * e] = (float)h[0];
-          v[2 * e + 1] = (float)h[1];
-        }
-      }
+      ep_unpack8(t, load16(p + 2 * i), v);
     }
   } else {
 #pragma unroll
@@ -123,6 +134,7 @@ __device__ __forceinline__ ep_u32x4 ep_pack8(int t, const float (&v)[8]) {
   }
   return o;
 }
+template <bool NT = false>
 __device__ __forceinline__ void ep_put8(uint8_t* p, int t, int64_t i, int n, const float (&v)[8]) {
   if (n >= 8) {
     if (t == TG_F32) {
@@ -132,10 +144,10 @@ __device__ __forceinline__ void ep_put8(uint8_t* p, int t, int64_t i, int n, con
         a[e] = __builtin_bit_cast(uint32_t, v[e]);
         b[e] = __builtin_bit_cast(uint32_t, v[4 + e]);
       }
-      store16(p + 4 * i, a);
-      store16(p + 4 * i + 16, b);
+      store16<NT>(p + 4 * i, a);
+      store16<NT>(p + 4 * i + 16, b);
     } else {
-      store16(p + 2 * i, ep_pack8(t, v));
+      store16<NT>(p + 2 * i, ep_pack8(t, v));
     }
   } else {
 #pragma unroll
@@ -145,40 +157,80 @@ __device__ __forceinline__ void ep_put8(uint8_t* p, int t, int64_t i, int n, con
 }
 
 // ---- activations ------------------------------------------------------------------------------
-// sigmoid(x) = 1/(1 + e^-x): for x -> -inf e^-x overflows to +inf and the quotient is 0.
-__device__ __forceinline__ float ep_sigmoid(float x) { return 1.0f / (1.0f + __expf(-x)); }
+// The sigmoid and the tail of the normal distribution take the unit's own reciprocal (1 ulp) and
+// exp2: an IEEE quotient costs ten instructions more per element, and the epilogue of a 256-wide
+// block does not overlap its products.
 
+// 1/(1 + 2^x): for x -> +inf 2^x is +inf and the quotient 0.
+__device__ __forceinline__ float ep_inv1p2(float x) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x)); }
+
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2/pi)
 constexpr float kGeluA = 0.044715f;
+constexpr float kGeluE = -2.0f * kGeluC * kLog2e;
+
+// sigmoid(x) and sigmoid(2u), 2u = 2c(z + a z^3)
+__device__ __forceinline__ float ep_sigmoid(float x) { return ep_inv1p2(-kLog2e * x); }
+__device__ __forceinline__ float ep_gelu_sigmoid(float z) { return ep_inv1p2(kGeluE * z * (1.0f + kGeluA * z * z)); }
+
+// 0.5·erfc(-z/sqrt(2)) = Phi(z).  erfc by the Chebyshev fit of Press et al., Numerical Recipes
+// (erfcc): t·exp(-x² + p(t)), t = 1/(1 + x/2), within 1.2e-7 of the value for every x >= 0; so
+// small tails keep their relative accuracy.
+__device__ __forceinline__ float ep_phi(float z) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(1.0f + 0.5f * x);
+  float p = 0.17087277f;
+  p = fmaf(p, t, -0.82215223f);
+  p = fmaf(p, t, 1.48851587f);
+  p = fmaf(p, t, -1.13520398f);
+  p = fmaf(p, t, 0.27886807f);
+  p = fmaf(p, t, -0.18628806f);
+  p = fmaf(p, t, 0.09678418f);
+  p = fmaf(p, t, 0.37409196f);
+  p = fmaf(p, t, 1.00002368f);
+  p = fmaf(p, t, -1.26551223f);
+  const float q = 0.5f * t * __builtin_amdgcn_exp2f(kLog2e * (p - 0.5f * z * z));
+  return z > 0.0f ? 1.0f - q : q;
+}
 
 // 0.5 z (1 + tanh u) = z·sigmoid(2u): no difference of near-equal numbers for negative z.
 // gelu = z·Phi(z) with Phi from erfc, for the same reason.
-__device__ __forceinline__ float ep_act(float z, int act) {
-  switch (act) {
-    case TG_ACT_RELU: return z > 0.0f || z != z ? z : 0.0f;
-    case TG_ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
-    case TG_ACT_GELU_TANH: return z * ep_sigmoid(2.0f * kGeluC * (z + kGeluA * z * z * z));
-    case TG_ACT_SILU: return z * ep_sigmoid(z);
-    default: return z;
-  }
+template <int ACT>
+__device__ __forceinline__ float ep_act(float z) {
+  if constexpr (ACT == TG_ACT_RELU) return z > 0.0f || z != z ? z : 0.0f;
+  else if constexpr (ACT == TG_ACT_GELU) return z * ep_phi(z);
+  else if constexpr (ACT == TG_ACT_GELU_TANH) return z * ep_gelu_sigmoid(z);
+  else if constexpr (ACT == TG_ACT_SILU) return z * ep_sigmoid(z);
+  else return z;
 }
 // Derivatives.  The argument is clamped where the derivative has reached 0 or 1 to below half
 // a unit of fp32, so that z² and z³ of large finite z cannot make 0·inf; NaN passes through.
-__device__ __forceinline__ float ep_act_grad(float z, int act) {
+template <int ACT>
+__device__ __forceinline__ float ep_act_grad(float z) {
   const float c = z != z ? z : fminf(fmaxf(z, -100.0f), 100.0f);
+  if constexpr (ACT == TG_ACT_RELU) {
+    return z > 0.0f ? 1.0f : z != z ? z : 0.0f;
+  } else if constexpr (ACT == TG_ACT_GELU) {
+    return ep_phi(c) + c * 0.3989422804014327f * __builtin_amdgcn_exp2f(-0.5f * kLog2e * c * c);
+  } else if constexpr (ACT == TG_ACT_GELU_TANH) {
+    const float s = ep_gelu_sigmoid(c);
+    return s + c * s * (1.0f - s) * 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * c * c);
+  } else if constexpr (ACT == TG_ACT_SILU) {
+    const float s = ep_sigmoid(c);
+    return s * (1.0f + c * (1.0f - s));
+  } else {
+    return 1.0f;
+  }
+}
+// f(activation) with the activation as a compile-time constant
+template <class F>
+__device__ __forceinline__ void ep_with_act(int act, F f) {
   switch (act) {
-    case TG_ACT_RELU: return z > 0.0f ? 1.0f : z != z ? z : 0.0f;
-    case TG_ACT_GELU:
-      return 0.5f * erfcf(-0.70710678118654752f * c) + c * 0.3989422804014327f * __expf(-0.5f * c * c);
-    case TG_ACT_GELU_TANH: {
-      const float s = ep_sigmoid(2.0f * kGeluC * (c + kGeluA * c * c * c));
-      return s + c * s * (1.0f - s) * 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * c * c);
-    }
-    case TG_ACT_SILU: {
-      const float s = ep_sigmoid(c);
-      return s * (1.0f + c * (1.0f - s));
-    }
-    default: return 1.0f;
+    case TG_ACT_RELU: f(std::integral_constant<int, TG_ACT_RELU>{}); break;
+    case TG_ACT_GELU: f(std::integral_constant<int, TG_ACT_GELU>{}); break;
+    case TG_ACT_GELU_TANH: f(std::integral_constant<int, TG_ACT_GELU_TANH>{}); break;
+    case TG_ACT_SILU: f(std::integral_constant<int, TG_ACT_SILU>{}); break;
+    default: f(std::integral_constant<int, TG_ACT_NONE>{}); break;
   }
 }
 
@@ -197,39 +249,56 @@ __device__ __forceinline__ void ep_cols(const EpArgs& g, int col, EpCols& c) {
   if (g.bias) ep_get8(g.bias, g.bias_t, col, n, c.bias);
   if (g.cs) ep_get8((const uint8_t*)g.cs, TG_F32, col, n, c.cs);
 }
+// What one row's 8 columns need besides the sums, loaded ahead of the stores (the residual may be
+// D, so the compiler would not move its load above a store).
+struct EpRow {
+  float rs;
+  ep_u32x4 lo, hi;   // residual bits: lo alone for 16-bit results; part rows hold fp32 in both
+};
+__device__ __forceinline__ void ep_row(const EpArgs& g, int row, int col, EpRow& x) {
+  const int n = g.N - col;
+  x.rs = g.rs ? g.rs[row] : 1.0f;
+  if (!g.res) return;
+  const int64_t i = (int64_t)row * g.ldr + col;
+  if (n >= 8 && g.d_t != TG_F32) {
+    x.lo = load16(g.res + 2 * i);
+  } else {
+    float r[8];
+    ep_get8(g.res, g.d_t, i, n, r);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x.lo[e] = __builtin_bit_cast(uint32_t, r[e]);
+      x.hi[e] = __builtin_bit_cast(uint32_t, r[4 + e]);
+    }
+  }
+}
 // v: the sums P of row `row`, columns col .. col+7 (row < M, col < N)
-__device__ __forceinline__ void ep_finish8(const EpArgs& g, int row, int col, const EpCols& c,
+template <bool NT = false>
+__device__ __forceinline__ void ep_finish8(const EpArgs& g, int row, int col, const EpCols& c, const EpRow& x,
                                            float (&v)[8]) {
   const int n = g.N - col;
-  if (g.rs) {
-    const float r = g.rs[row];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= r;
-  }
+  for (int e = 0; e < 8; ++e) v[e] = v[e] * x.rs * c.cs[e] + c.bias[e];
+  if (g.Z) ep_put8<NT>(g.Z, g.d_t, (int64_t)row * g.ldz + col, n, v);
+  ep_with_act(g.act, [&](auto act) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = v[e] * c.cs[e] + c.bias[e];
-  if (g.Z) ep_put8(g.Z, g.d_t, (int64_t)row * g.ldz + col, n, v);
-  if (g.act != TG_ACT_NONE) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = ep_act(v[e], g.act);
-  }
+    for (int e = 0; e < 8; ++e) v[e] = ep_act<decltype(act)::value>(v[e]);
+  });
   if (g.res) {
     float r[8];
-    ep_get8(g.res, g.d_t, (int64_t)row * g.ldr + col, n, r);
+    if (n >= 8 && g.d_t != TG_F32) {
+      ep_unpack8(g.d_t, x.lo, r);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        r[e] = __builtin_bit_cast(float, (uint32_t)x.lo[e]);
+        r[4 + e] = __builtin_bit_cast(float, (uint32_t)x.hi[e]);
+      }
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += r[e];
   }
-  ep_put8(g.D, g.d_t, (int64_t)row * g.ldd + col, n, v);
-}
-// one element
-__device__ __forceinline__ void ep_finish1(const EpArgs& g, int row, int col, float p) {
-  if (g.rs) p *= g.rs[row];
-  if (g.cs) p *= g.cs[col];
-  if (g.bias) p += ep_get(g.bias, g.bias_t, col);
-  if (g.Z) ep_put(g.Z, g.d_t, (int64_t)row * g.ldz + col, p);
-  p = ep_act(p, g.act);
-  if (g.res) p += ep_get(g.res, g.d_t, (int64_t)row * g.ldr + col);
-  ep_put(g.D, g.d_t, (int64_t)row * g.ldd + col, p);
+  ep_put8<NT>(g.D, g.d_t, (int64_t)row * g.ldd + col, n, v);
 }
 
 }  // namespace

@@ -294,8 +294,16 @@ __device__ __forceinline__ void ep_body(const EpArgs& g) {
   const int col = n0 + wn + bcol;
   EpCols cols;
   if (g.splits == 1) ep_cols(g, col, cols);
+  auto band_step = [&](auto I) {
+    constexpr int i = decltype(I)::value;   // compile-time: the accumulators stay in registers
+    constexpr int NP = 32 / RPP;
+    const int row0 = m0 + wm + 32 * i + brow;
+    EpRow rows[NP];
+    if (g.splits == 1) {
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
+      for (int p = 0; p < NP; ++p)
+        if (row0 + p * RPP < g.M && col < g.N) ep_row(g, row0 + p * RPP, col, rows[p]);
+    }
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
@@ -305,20 +313,26 @@ __device__ __forceinline__ void ep_body(const EpArgs& g) {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll 1
-    for (int p = 0; p < 32; p += RPP) {
-      const int row = m0 + wm + 32 * i + p + brow;
-      const float* src = band + (p + brow) * LDF + bcol;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const float* src = band + (p * RPP + brow) * LDF + bcol;
       const float4 lo = *(const float4*)src, hi = *(const float4*)(src + 4);
       float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      const int row = row0 + p * RPP;
       if (row < g.M && col < g.N) {
-        if (g.splits == 1) ep_finish8(g, row, col, cols, v);
+        if (g.splits == 1) ep_finish8<true>(g, row, col, cols, rows[p], v);
         else ep_put8((uint8_t*)g.part, TG_F32, ((int64_t)split * g.M + row) * g.part_ld + col, 8, v);
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  };
+  band_step(std::integral_constant<int, 0>{});
+  if constexpr (TM > 1) band_step(std::integral_constant<int, 1>{});
+  if constexpr (TM > 2) {
+    band_step(std::integral_constant<int, 2>{});
+    band_step(std::integral_constant<int, 3>{});
   }
 }
 

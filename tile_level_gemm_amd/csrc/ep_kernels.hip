@@ -7,22 +7,37 @@ namespace {
 
 // D from `splits` partial sums, added in their order (0 of them: P = 0, the K == 0 product).
 // 8 columns per thread; bound by the partial sums' bytes, which the block kernels have just
-// written.
+// written.  Four parts' loads are in flight together: one at a time, 16 parts of one row took
+// 7.9 us, nearly all of it waiting.
 __global__ __launch_bounds__(256) void ep_join(EpArgs g, int64_t chunks) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= chunks) return;
   const int per_row = (g.N + 7) / 8;
   const int row = (int)(i / per_row), col = (int)(i % per_row) * 8;
   EpCols cols;
+  EpRow x;
   ep_cols(g, col, cols);
+  ep_row(g, row, col, x);
   float v[8] = {};
   const float* p = g.part + (int64_t)row * g.part_ld + col;
-  for (int s = 0; s < g.splits; ++s, p += (int64_t)g.M * g.part_ld) {
-    const float4 a = *(const float4*)p, b = *(const float4*)(p + 4);
+  const int64_t step = (int64_t)g.M * g.part_ld;
+  auto add = [&](float4 a, float4 b) {
     v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
     v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+  };
+  int s = 0;
+  for (; s + 4 <= g.splits; s += 4, p += 4 * step) {
+    float4 a[4], b[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      a[k] = *(const float4*)(p + k * step);
+      b[k] = *(const float4*)(p + k * step + 4);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) add(a[k], b[k]);
   }
-  ep_finish8(g, row, col, cols, v);
+  for (; s < g.splits; ++s, p += step) add(*(const float4*)p, *(const float4*)(p + 4));
+  ep_finish8(g, row, col, cols, x, v);
 }
 
 // dZ = dY·act'(Z), and the column sums of dZ (before its rounding) over the workgroup's rows.
@@ -42,8 +57,10 @@ __global__ __launch_bounds__(256) void act_grad(ActGradArgs a) {
       if (a.act != TG_ACT_NONE) {
         float z[8];
         ep_get8(a.Z, a.t, r * a.ldz + col, n, z);
+        ep_with_act(a.act, [&](auto act) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dy[e] *= ep_act_grad(z[e], a.act);
+          for (int e = 0; e < 8; ++e) dy[e] *= ep_act_grad<decltype(act)::value>(z[e]);
+        });
       }
       if (a.dZ) ep_put8(a.dZ, a.t, r * a.N + col, n, dy);
 #pragma unroll
