@@ -3,7 +3,7 @@
 //   P = A·B (fp32 sums)   Z = row_scale[m]·col_scale[n]·P + bias[n]   D = act(Z) + residual
 //
 // Every kernel that finishes an output element (the block kernels, the token kernels and the join
-// of a split sum) goes through ep_finish8, so all of them round once: Z and D are each
+// of a split sum) goes through ep_finish8 or its even form, so all of them round once: Z and D are each
 // rounded to d_dtype from the fp32 value.  Internal header.
 #pragma once
 
@@ -249,56 +249,52 @@ __device__ __forceinline__ void ep_cols(const EpArgs& g, int col, EpCols& c) {
   if (g.bias) ep_get8(g.bias, g.bias_t, col, n, c.bias);
   if (g.cs) ep_get8((const uint8_t*)g.cs, TG_F32, col, n, c.cs);
 }
-// What one row's 8 columns need besides the sums, loaded ahead of the stores (the residual may be
-// D, so the compiler would not move its load above a store).
-struct EpRow {
-  float rs;
-  ep_u32x4 lo, hi;   // residual bits: lo alone for 16-bit results; part rows hold fp32 in both
-};
-__device__ __forceinline__ void ep_row(const EpArgs& g, int row, int col, EpRow& x) {
-  const int n = g.N - col;
-  x.rs = g.rs ? g.rs[row] : 1.0f;
-  if (!g.res) return;
-  const int64_t i = (int64_t)row * g.ldr + col;
-  if (n >= 8 && g.d_t != TG_F32) {
-    x.lo = load16(g.res + 2 * i);
-  } else {
-    float r[8];
-    ep_get8(g.res, g.d_t, i, n, r);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x.lo[e] = __builtin_bit_cast(uint32_t, r[e]);
-      x.hi[e] = __builtin_bit_cast(uint32_t, r[4 + e]);
-    }
-  }
-}
-// v: the sums P of row `row`, columns col .. col+7 (row < M, col < N)
+// v: the sums P of row `row`, columns col .. col+7 (row < M, col < N); any type, any number of
+// columns left.
 template <bool NT = false>
-__device__ __forceinline__ void ep_finish8(const EpArgs& g, int row, int col, const EpCols& c, const EpRow& x,
-                                           float (&v)[8]) {
+__device__ __forceinline__ void ep_finish8(const EpArgs& g, int row, int col, const EpCols& c, float (&v)[8]) {
   const int n = g.N - col;
+  const float rs = g.rs ? g.rs[row] : 1.0f;
+  float r[8] = {};
+  if (g.res) ep_get8(g.res, g.d_t, (int64_t)row * g.ldr + col, n, r);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = v[e] * x.rs * c.cs[e] + c.bias[e];
+  for (int e = 0; e < 8; ++e) v[e] = v[e] * rs * c.cs[e] + c.bias[e];
   if (g.Z) ep_put8<NT>(g.Z, g.d_t, (int64_t)row * g.ldz + col, n, v);
   ep_with_act(g.act, [&](auto act) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = ep_act<decltype(act)::value>(v[e]);
   });
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] += r[e];
+  ep_put8<NT>(g.D, g.d_t, (int64_t)row * g.ldd + col, n, v);
+}
+// The same for 16-bit results and N % 8 == 0, in two halves: what a row needs besides its sums is
+// loaded for several rows ahead of their stores (the residual may be D, so the compiler would not move
+// its load above a store), and no code for ragged columns is in the way.
+inline __host__ __device__ bool ep_even(const EpArgs& g) { return g.d_t != TG_F32 && g.N % 8 == 0; }
+struct EpRow {
+  float rs;
+  ep_u32x4 res;
+};
+__device__ __forceinline__ void ep_row(const EpArgs& g, int row, int col, EpRow& x) {
+  x.rs = g.rs ? g.rs[row] : 1.0f;
+  if (g.res) x.res = load16(g.res + 2 * ((int64_t)row * g.ldr + col));
+}
+template <int ACT>
+__device__ __forceinline__ void ep_finish8_even(const EpArgs& g, int row, int col, const EpCols& c, const EpRow& x,
+                                                float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = v[e] * x.rs * c.cs[e] + c.bias[e];
+  if (g.Z) store16<true>(g.Z + 2 * ((int64_t)row * g.ldz + col), ep_pack8(g.d_t, v));
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = ep_act<ACT>(v[e]);
   if (g.res) {
     float r[8];
-    if (n >= 8 && g.d_t != TG_F32) {
-      ep_unpack8(g.d_t, x.lo, r);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        r[e] = __builtin_bit_cast(float, (uint32_t)x.lo[e]);
-        r[4 + e] = __builtin_bit_cast(float, (uint32_t)x.hi[e]);
-      }
-    }
+    ep_unpack8(g.d_t, x.res, r);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += r[e];
   }
-  ep_put8<NT>(g.D, g.d_t, (int64_t)row * g.ldd + col, n, v);
+  store16<true>(g.D + 2 * ((int64_t)row * g.ldd + col), ep_pack8(g.d_t, v));
 }
 
 }  // namespace

@@ -294,45 +294,79 @@ __device__ __forceinline__ void ep_body(const EpArgs& g) {
   const int col = n0 + wn + bcol;
   EpCols cols;
   if (g.splits == 1) ep_cols(g, col, cols);
-  auto band_step = [&](auto I) {
-    constexpr int i = decltype(I)::value;   // compile-time: the accumulators stay in registers
-    constexpr int NP = 32 / RPP;
-    const int row0 = m0 + wm + 32 * i + brow;
-    EpRow rows[NP];
-    if (g.splits == 1) {
-#pragma unroll
-      for (int p = 0; p < NP; ++p)
-        if (row0 + p * RPP < g.M && col < g.N) ep_row(g, row0 + p * RPP, col, rows[p]);
-    }
+  // The bands run in a loop whose only unrolled part is the write from the accumulators: unrolled
+  // whole, the epilogue was 250 KB of code, and fetching it took 16 us a 256-wide block.
+  auto to_band = [&](auto I) {
+    constexpr int i = decltype(I)::value < TM ? decltype(I)::value : 0;   // compile-time: registers
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         *(float4*)(band + (lane & 31) * LDF + 32 * j + 8 * q + 4 * (lane >> 5)) =
             float4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+  };
+  auto from_band = [&](int p, float (&v)[8]) {
+    const float* src = band + (p * RPP + brow) * LDF + bcol;
+    const float4 lo = *(const float4*)src, hi = *(const float4*)(src + 4);
+    v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+    v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+  };
+  constexpr int NP = 32 / RPP;
+  const bool even = ep_even(g), in = col < g.N;
+  // residual and row scales: one band ahead of the one being stored
+  EpRow ahead[NP];
+  auto look = [&](int i) {
+    if (g.splits > 1 || !even) return;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const int row = m0 + wm + 32 * i + brow + p * RPP;
+      if (in && row < g.M) ep_row(g, row, col, ahead[p]);
+    }
+  };
+  look(0);
+#pragma unroll 1
+  for (int i = 0; i < TM; ++i) {
+    const int row0 = m0 + wm + 32 * i + brow;
+    EpRow rows[NP];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) rows[p] = ahead[p];
+    if (i + 1 < TM) look(i + 1);
+    if (i == 0) to_band(std::integral_constant<int, 0>{});
+    else if (i == 1) to_band(std::integral_constant<int, 1>{});
+    else if (i == 2) to_band(std::integral_constant<int, 2>{});
+    else to_band(std::integral_constant<int, 3>{});
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    float v[8];
+    if (g.splits > 1) {
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      const float* src = band + (p * RPP + brow) * LDF + bcol;
-      const float4 lo = *(const float4*)src, hi = *(const float4*)(src + 4);
-      float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-      const int row = row0 + p * RPP;
-      if (row < g.M && col < g.N) {
-        if (g.splits == 1) ep_finish8<true>(g, row, col, cols, rows[p], v);
-        else ep_put8((uint8_t*)g.part, TG_F32, ((int64_t)split * g.M + row) * g.part_ld + col, 8, v);
+      for (int p = 0; p < NP; ++p) {
+        from_band(p, v);
+        const int row = row0 + p * RPP;
+        if (in && row < g.M)
+          ep_put8((uint8_t*)g.part, TG_F32, ((int64_t)split * g.M + row) * g.part_ld + col, 8, v);
+      }
+    } else if (even) {
+      ep_with_act(g.act, [&](auto act) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          from_band(p, v);
+          const int row = row0 + p * RPP;
+          if (in && row < g.M) ep_finish8_even<decltype(act)::value>(g, row, col, cols, rows[p], v);
+        }
+      });
+    } else {
+#pragma unroll 1
+      for (int p = 0; p < NP; ++p) {
+        from_band(p, v);
+        const int row = row0 + p * RPP;
+        if (in && row < g.M) ep_finish8(g, row, col, cols, v);   // fp32 or ragged: the L2 joins the pieces
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  };
-  band_step(std::integral_constant<int, 0>{});
-  if constexpr (TM > 1) band_step(std::integral_constant<int, 1>{});
-  if constexpr (TM > 2) {
-    band_step(std::integral_constant<int, 2>{});
-    band_step(std::integral_constant<int, 3>{});
   }
 }
 

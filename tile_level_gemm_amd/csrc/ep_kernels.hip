@@ -15,9 +15,7 @@ __global__ __launch_bounds__(256) void ep_join(EpArgs g, int64_t chunks) {
   const int per_row = (g.N + 7) / 8;
   const int row = (int)(i / per_row), col = (int)(i % per_row) * 8;
   EpCols cols;
-  EpRow x;
   ep_cols(g, col, cols);
-  ep_row(g, row, col, x);
   float v[8] = {};
   const float* p = g.part + (int64_t)row * g.part_ld + col;
   const int64_t step = (int64_t)g.M * g.part_ld;
@@ -37,7 +35,7 @@ __global__ __launch_bounds__(256) void ep_join(EpArgs g, int64_t chunks) {
     for (int k = 0; k < 4; ++k) add(a[k], b[k]);
   }
   for (; s < g.splits; ++s, p += step) add(*(const float4*)p, *(const float4*)(p + 4));
-  ep_finish8(g, row, col, cols, x, v);
+  ep_finish8(g, row, col, cols, v);
 }
 
 // dZ = dY·act'(Z), and the column sums of dZ (before its rounding) over the workgroup's rows.
