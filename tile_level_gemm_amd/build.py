@@ -26,7 +26,7 @@ SOURCES = ["abi.cpp", "plan.cpp", "copy_kernels.hip", "gemm_kernels.hip", "gemm_
            "gemm_mx_kk.hip", "gemm_mx_km.hip", "gemm_mx_mk.hip", "gemm_mx_mm.hip", "gemm_mx_packed.hip", "gemm_mx_fp4.hip", "gemm_mx_fp6.hip",
            "frag.cpp", "frag_kernels.hip", "async_copy.hip",
            "layer_abi.cpp", "ep_gemm_kk.hip", "ep_gemm_km.hip", "ep_gemm_mk.hip", "ep_gemm_mm.hip",
-           "ep_gemm_fp8.hip", "ep_kernels.hip", "norm.hip"]
+           "ep_gemm_fp8.hip", "ep_tokens.hip", "ep_kernels.hip", "norm.hip"]
 
 # -packed-fp32-ops: no v_pk_*_f32 in generated code (the device pass honours it; the
 # host pass warns that it does not know the feature).

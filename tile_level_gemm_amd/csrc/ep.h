@@ -22,6 +22,7 @@ struct EpArgs {
   int64_t lda, ldb, ldd;       // elements
   int32_t M, N, K;
   int32_t tiles_m, tiles_n;
+  int32_t waves;               // few rows: waves of a workgroup
   int32_t splits, k_per_split; // the sum over K in `splits` parts of k_per_split (the last one shorter)
   float* part;                 // splits > 1: fp32 sums [splits][M][part_ld]
   int64_t part_ld;             // N rounded up to 8: rows stay 32-byte aligned
@@ -37,6 +38,10 @@ struct EpArgs {
 // Kernel families of tile_gemm_ep (tg_ep_plan.kernel).
 hipError_t launch_ep_block(const EpArgs& g, int trans_a, int trans_b, int a_dtype, int b_dtype, int bs,
                            bool staged, hipStream_t s);
+// M <= kTokenRows; `waves` (1 .. 8) waves share K
+constexpr int64_t kTokenRows = 32;
+hipError_t launch_ep_tokens(const EpArgs& g, int trans_a, int trans_b, int a_dtype, int b_dtype, int waves,
+                            hipStream_t s);
 hipError_t launch_ep_join(const EpArgs& g, hipStream_t s);
 
 // dZ = dY·act'(Z) ([M][N] packed, may be NULL) and column sums [groups][N] (may be NULL).
@@ -268,7 +273,18 @@ __device__ __forceinline__ void ep_finish8(const EpArgs& g, int row, int col, co
   for (int e = 0; e < 8; ++e) v[e] += r[e];
   ep_put8<NT>(g.D, g.d_t, (int64_t)row * g.ldd + col, n, v);
 }
-// The same for 16-bit results and N % 8 == 0, in two halves: what a row needs besides its sums is
+// one element
+__device__ __forceinline__ void ep_finish1(const EpArgs& g, int row, int col, float p) {
+  float r = 0.0f;
+  if (g.res) r = ep_get(g.res, g.d_t, (int64_t)row * g.ldr + col);
+  if (g.rs) p *= g.rs[row];
+  if (g.cs) p *= g.cs[col];
+  if (g.bias) p += ep_get(g.bias, g.bias_t, col);
+  if (g.Z) ep_put(g.Z, g.d_t, (int64_t)row * g.ldz + col, p);
+  ep_with_act(g.act, [&](auto act) { p = ep_act<decltype(act)::value>(p); });
+  ep_put(g.D, g.d_t, (int64_t)row * g.ldd + col, p + r);
+}
+// 8 columns of 16-bit results with N % 8 == 0, in two halves: what a row needs besides its sums is
 // loaded for several rows ahead of their stores (the residual may be D, so the compiler would not move
 // its load above a store), and no code for ragged columns is in the way.
 inline __host__ __device__ bool ep_even(const EpArgs& g) { return g.d_t != TG_F32 && g.N % 8 == 0; }

@@ -81,16 +81,22 @@ int check_workspace(const void* ws, int64_t bytes) {
 struct EpChoice {
   int kernel, bs, splits;
   int64_t kps, ws;
+  int waves;   // of a TOKENS workgroup
 };
 
 int64_t part_ld(int64_t N) { return (N + 7) / 8 * 8; }
 
 EpChoice choose_ep(int64_t M, int64_t N, int64_t K, int eb, bool direct, int64_t budget) {
-  EpChoice c{TG_EP_NONE, 0, 1, K, 0};
+  EpChoice c{TG_EP_NONE, 0, 1, K, 0, 0};
   if (M == 0 || N == 0) return c;
   if (K == 0) {
     c.kernel = TG_EP_JOIN;
     c.splits = 0;
+    return c;
+  }
+  if (M <= kTokenRows) {
+    c.kernel = TG_EP_TOKENS;
+    c.waves = (int)std::min<int64_t>(8, (K * eb + 127) / 128);   // a step of K each at least
     return c;
   }
   auto blocks = [&](int64_t b) { return ((M + b - 1) / b) * ((N + b - 1) / b); };
@@ -184,6 +190,11 @@ int plan_ep(const void* A, const void* B, const void* D, int64_t M, int64_t N, i
     plan->block_m = plan->block_n = c.bs;
     plan->block_k = 128 / eb;
     plan->grid = ((M + c.bs - 1) / c.bs) * ((N + c.bs - 1) / c.bs) * c.splits;
+  } else if (c.kernel == TG_EP_TOKENS) {
+    plan->block_m = M <= 16 ? 16 : 32;
+    plan->block_n = transB ? 16 : 32;
+    plan->block_k = transB ? 128 / eb : 32;
+    plan->grid = (N + plan->block_n - 1) / plan->block_n;
   } else {
     plan->grid = (M * ((N + 7) / 8) + 255) / 256;
   }
@@ -203,6 +214,7 @@ int plan_ep(const void* A, const void* B, const void* D, int64_t M, int64_t N, i
     g->tiles_m = (int32_t)((M + c.bs - 1) / c.bs);
     g->tiles_n = (int32_t)((N + c.bs - 1) / c.bs);
   }
+  g->waves = c.waves;
   g->splits = c.splits;
   g->k_per_split = (int32_t)c.kps;
   g->part = (float*)const_cast<void*>(ws);
@@ -227,6 +239,8 @@ int hip_status(const char* what, hipError_t e) {
 
 int run_ep(const EpArgs& g, const tg_ep_plan& p, int transA, int transB, int a_dtype, int b_dtype, hipStream_t s) {
   if (p.kernel == TG_EP_NONE) return TG_OK;
+  if (p.kernel == TG_EP_TOKENS)
+    return hip_status("tile_gemm_ep", launch_ep_tokens(g, transA, transB, a_dtype, b_dtype, g.waves, s));
   if (p.kernel == TG_EP_DIRECT || p.kernel == TG_EP_STAGED) {
     int st = hip_status("tile_gemm_ep", launch_ep_block(g, transA, transB, a_dtype, b_dtype, p.block_m,
                                                         p.kernel == TG_EP_STAGED, s));
