@@ -22,7 +22,7 @@ struct EpArgs {
   int64_t lda, ldb, ldd;       // elements
   int32_t M, N, K;
   int32_t tiles_m, tiles_n;
-  int32_t waves;               // few rows: waves of a workgroup
+  int32_t waves, cn;           // few rows: waves and columns of a workgroup
   int32_t splits, k_per_split; // the sum over K in `splits` parts of k_per_split (the last one shorter)
   float* part;                 // splits > 1: fp32 sums [splits][M][part_ld]
   int64_t part_ld;             // N rounded up to 8: rows stay 32-byte aligned
@@ -273,16 +273,21 @@ __device__ __forceinline__ void ep_finish8(const EpArgs& g, int row, int col, co
   for (int e = 0; e < 8; ++e) v[e] += r[e];
   ep_put8<NT>(g.D, g.d_t, (int64_t)row * g.ldd + col, n, v);
 }
-// one element
-__device__ __forceinline__ void ep_finish1(const EpArgs& g, int row, int col, float p) {
-  float r = 0.0f;
-  if (g.res) r = ep_get(g.res, g.d_t, (int64_t)row * g.ldr + col);
-  if (g.rs) p *= g.rs[row];
-  if (g.cs) p *= g.cs[col];
-  if (g.bias) p += ep_get(g.bias, g.bias_t, col);
+// one element: what its epilogue reads, and the finish
+struct EpOne {
+  float rs, cs, bias, res;
+};
+__device__ __forceinline__ void ep_one(const EpArgs& g, int row, int col, EpOne& x) {
+  x.rs = g.rs ? g.rs[row] : 1.0f;
+  x.cs = g.cs ? g.cs[col] : 1.0f;
+  x.bias = g.bias ? ep_get(g.bias, g.bias_t, col) : 0.0f;
+  x.res = g.res ? ep_get(g.res, g.d_t, (int64_t)row * g.ldr + col) : 0.0f;
+}
+__device__ __forceinline__ void ep_finish1(const EpArgs& g, int row, int col, const EpOne& x, float p) {
+  p = p * x.rs * x.cs + x.bias;
   if (g.Z) ep_put(g.Z, g.d_t, (int64_t)row * g.ldz + col, p);
   ep_with_act(g.act, [&](auto act) { p = ep_act<decltype(act)::value>(p); });
-  ep_put(g.D, g.d_t, (int64_t)row * g.ldd + col, p + r);
+  ep_put(g.D, g.d_t, (int64_t)row * g.ldd + col, p + x.res);
 }
 // 8 columns of 16-bit results with N % 8 == 0, in two halves: what a row needs besides its sums is
 // loaded for several rows ahead of their stores (the residual may be D, so the compiler would not move

@@ -1,14 +1,18 @@
 // Product with an epilogue for few rows (ep.h has the formulas): a stream of weights.
 //
-// Bound by reading B once; A is small and comes from the caches.  A workgroup owns CN columns and
-// all of K, so one launch does everything: no parts to join, no workspace.  Its waves take K steps
+// Bound by reading B once; A is small and comes from the caches.  A workgroup's waves take K steps
 // in turn, each with up to 16 KB of B in flight in registers before its first product, then the
-// waves' sums meet in LDS, are added in their order and finished.
+// waves' sums meet in LDS, are added in their order and finished with the epilogue operands that were
+// loaded first of all.  A CU draws about 26 GB/s from HBM this way whatever its waves ask for (131 KB:
+// 5 us), so the columns are cut until every CU has some.
 //
-//   B [N][K] (K-major): a step is 128 bytes of K of 16 columns.  Lane (n = l%16, g = l/16) loads bytes
-//     32g .. 32g+31 of its column, so four lanes read one whole line; the matrix instruction (16x16x32
-//     for 16-bit, 16x16x128 for fp8) takes K in that order, for A and B alike (a sum does not care).
-//   B [K][N]: a step is 32 k-rows of 32 columns.  Lane (j, g) loads columns 2j, 2j+1 of k-rows
+//   B [N][K] (K-major): a step is 128 bytes of K of 16 columns (32 for N >= 8192: A is read half as
+//     often).  Lane (n = l%16, g = l/16) loads bytes 32g .. 32g+31 of its column, so four lanes read one
+//     whole line; the matrix instruction (16x16x32 for 16-bit, 16x16x128 for fp8) takes K in that order,
+//     for A and B alike (a sum does not care).  For small N the workgroup owns 8 or 4 columns and the
+//     other lanes load nothing: more CUs, no parts to join.
+//   B [K][N]: a step is 32 k-rows of 32 columns.  Where that leaves CUs without work and a workgroup
+//     with much, K is cut into parts that ep_join adds.  Lane (j, g) loads columns 2j, 2j+1 of k-rows
 //     8g .. 8g+7 (16 lanes read 64 bytes of a row) and turns the 8 pairs into two K-vectors with
 //     byte permutes; column 2j + c is column j of instruction c.  64-byte runs rather than 128: twice
 //     the workgroups for the same N, and the other half of a line is read on the same XCD.
@@ -61,16 +65,17 @@ __device__ __forceinline__ u32x4 k_gather(const uint16_t* p, int64_t ld, int n) 
 struct __attribute__((packed, aligned(2))) Bytes4 { uint32_t v; };
 
 // MT: row tiles of 16.  blockDim.x / 64 waves.
-template <bool A_MN, bool B_MN, int DT, int MT>
+// NI: column tiles of 16.
+template <bool A_MN, bool B_MN, int DT, int MT, int NI>
 __global__ __launch_bounds__(512) void gemm_ep_tokens(EpArgs g) {
   using EL = Elem<DT>;
   constexpr int E = EL::kBytes;
-  constexpr int CN = B_MN ? 32 : 16;            // columns of a workgroup
-  constexpr int NI = B_MN ? 2 : 1;              // of 16 per instruction
+  static_assert(!B_MN || NI == 2, "a lane's two columns");
+  constexpr int CN = 16 * NI;                   // most columns of a workgroup
   constexpr int KS = B_MN ? 32 : 128 / E;       // K of a step
   constexpr int KI = E == 2 ? 32 : 128;         // K of an instruction
   constexpr int NF = KS / KI;                   // instructions of a step along K
-  constexpr int U = MT == 1 ? 8 : 4;            // steps in flight
+  constexpr int U = MT == 1 && (B_MN || NI == 1) ? 8 : 4;   // steps in flight
   using Frag = typename EL::Frag;               // one instruction's operand: 8 16-bit values, 32 fp8
   constexpr int LD = CN + 1;
   __shared__ float red[8][MT * 16][LD];
@@ -78,21 +83,31 @@ __global__ __launch_bounds__(512) void gemm_ep_tokens(EpArgs g) {
   const int nb = (int)gridDim.x;
   int bid = (int)blockIdx.x;
   if ((nb & 7) == 0) bid = (bid & 7) * (nb >> 3) + (bid >> 3);
-  const int n0 = bid * CN;
+  const int blocks_n = (g.N + g.cn - 1) / g.cn;
+  const int split = bid / blocks_n;
+  const int n0 = (bid - split * blocks_n) * g.cn;
+  const int n1 = min(g.N, n0 + g.cn);
   const int W = (int)blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = (int)threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4;
-  const int K = g.K, T = (K + KS - 1) / KS, full = K / KS;
+  const int kb = split * g.k_per_split;         // this part of K
+  const int K = min(g.K - kb, g.k_per_split), T = (K + KS - 1) / KS, full = K / KS;
+
+  // this thread's first output, and what its epilogue reads: on the way while the sum is taken
+  const int orow = (int)threadIdx.x / CN, ocol = n0 + (int)threadIdx.x % CN;
+  EpOne pre{};
+  if (g.splits == 1 && orow < g.M && orow < 16 * MT && ocol < n1) ep_one(g, orow, ocol, pre);
 
   // what a lane loads of B in a step, before it is made into fragments
   struct Raw {
-    uint32_t r[B_MN ? 8 : NF * (E == 2 ? 4 : 8)];
+    uint32_t r[B_MN ? 8 : NI * 8];
   };
   const int col = n0 + (B_MN ? 2 * li : li);
-  const int nc = g.N - col;   // valid columns from this lane's first on
+  const int nc = n1 - col;   // valid columns from this lane's first on
   // k of the lane's first element in a step (B_MN: k-rows; K-major: a run of 32 bytes)
   const int kl = B_MN ? 8 * lg : lg * (32 / E);
-  const uint8_t* pb = g.B + (B_MN ? (int64_t)kl * g.ldb + col : (int64_t)col * g.ldb + kl) * E;
+  const uint8_t* pb = g.B + (B_MN ? (int64_t)(kb + kl) * g.ldb + col : (int64_t)col * g.ldb + kb + kl) * E;
+  const uint8_t* pa = g.A + (A_MN ? (int64_t)kb * g.lda : (int64_t)kb) * E;
   auto load_b = [&](int step, auto partial, Raw& x) {
     constexpr bool kPartial = decltype(partial)::value;
     const int k0 = step * KS, left = K - k0 - kl;
@@ -106,16 +121,19 @@ __global__ __launch_bounds__(512) void gemm_ep_tokens(EpArgs g) {
         x.r[e] = v;
       }
     } else {
-      const uint8_t* p = pb + (int64_t)k0 * E;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        u32x4 v = {0, 0, 0, 0};
-        if (nc > 0) {
-          if constexpr (kPartial) v = k_chunk<E>(p + 16 * h, left - h * (16 / E));
-          else v = load16(p + 16 * h);
+      for (int c = 0; c < NI; ++c) {
+        const uint8_t* p = pb + ((int64_t)16 * c * g.ldb + k0) * E;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          u32x4 v = {0, 0, 0, 0};
+          if (nc > 16 * c) {
+            if constexpr (kPartial) v = k_chunk<E>(p + 16 * h, left - h * (16 / E));
+            else v = load16(p + 16 * h);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x.r[8 * c + 4 * h + i] = v[i];
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x.r[4 * h + i] = v[i];
       }
     }
   };
@@ -127,9 +145,11 @@ __global__ __launch_bounds__(512) void gemm_ep_tokens(EpArgs g) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = __builtin_amdgcn_perm(x.r[2 * e + 1], x.r[2 * e], sel);
     } else if constexpr (E == 2) {
-      o = Frag{x.r[4 * f], x.r[4 * f + 1], x.r[4 * f + 2], x.r[4 * f + 3]};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = x.r[8 * c + 4 * f + e];
     } else {
-      o = Frag{x.r[0], x.r[1], x.r[2], x.r[3], x.r[4], x.r[5], x.r[6], x.r[7]};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = x.r[8 * c + e];
     }
     return o;
   };
@@ -140,9 +160,9 @@ __global__ __launch_bounds__(512) void gemm_ep_tokens(EpArgs g) {
     Frag o = {};
     if (row < g.M) {
       if constexpr (A_MN) {
-        o = k_gather((const uint16_t*)g.A + (int64_t)k * g.lda + row, g.lda, kPartial ? left : 8);
+        o = k_gather((const uint16_t*)pa + (int64_t)k * g.lda + row, g.lda, kPartial ? left : 8);
       } else {
-        const uint8_t* p = g.A + ((int64_t)row * g.lda + k) * E;
+        const uint8_t* p = pa + ((int64_t)row * g.lda + k) * E;
         if constexpr (E == 2) {
           o = kPartial ? k_chunk<E>(p, left) : load16(p);
         } else {
@@ -204,23 +224,44 @@ __global__ __launch_bounds__(512) void gemm_ep_tokens(EpArgs g) {
 #pragma unroll
     for (int c = 0; c < NI; ++c)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) red[wave][16 * i + li][B_MN ? 2 * (4 * lg + r) + c : 4 * lg + r] = acc[i][c][r];
+      for (int r = 0; r < 4; ++r)
+        red[wave][16 * i + li][B_MN ? 2 * (4 * lg + r) + c : 16 * c + 4 * lg + r] = acc[i][c][r];
   __syncthreads();
-  for (int o = (int)threadIdx.x; o < MT * 16 * CN; o += (int)blockDim.x) {
-    const int row = o / CN, n = o % CN;
-    if (row >= g.M || n0 + n >= g.N) continue;
+  auto sum = [&](int row, int n) {
     float v = red[0][row][n];
-    for (int w = 1; w < W; ++w) v += red[w][row][n];
-    ep_finish1(g, row, n0 + n, v);
+    if (W == 8) {
+#pragma unroll
+      for (int w = 1; w < 8; ++w) v += red[w][row][n];
+    } else {
+      for (int w = 1; w < W; ++w) v += red[w][row][n];
+    }
+    return v;
+  };
+  for (int o = (int)threadIdx.x; o < MT * 16 * CN; o += (int)blockDim.x) {
+    const int row = o / CN, col_o = n0 + o % CN;
+    if (row >= g.M || col_o >= n1) continue;
+    const float v = sum(row, o % CN);
+    if (g.splits > 1) {
+      g.part[((int64_t)split * g.M + row) * g.part_ld + col_o] = v;
+    } else {
+      if (o != (int)threadIdx.x) ep_one(g, row, col_o, pre);
+      ep_finish1(g, row, col_o, pre, v);
+    }
   }
 }
 
 template <bool A_MN, bool B_MN, int DT>
 hipError_t go(const EpArgs& g, int waves, hipStream_t s) {
-  constexpr int CN = B_MN ? 32 : 16;
-  const dim3 grid((unsigned)(((int64_t)g.N + CN - 1) / CN)), block(64 * (unsigned)waves);
-  if (g.M <= 16) hipLaunchKernelGGL((gemm_ep_tokens<A_MN, B_MN, DT, 1>), grid, block, 0, s, g);
-  else hipLaunchKernelGGL((gemm_ep_tokens<A_MN, B_MN, DT, 2>), grid, block, 0, s, g);
+  const dim3 grid((unsigned)((((int64_t)g.N + g.cn - 1) / g.cn) * g.splits)), block(64 * (unsigned)waves);
+  constexpr int N1 = B_MN ? 2 : 1;
+  const bool wide = B_MN || g.cn == 32;
+  if (g.M <= 16) {
+    if (wide) hipLaunchKernelGGL((gemm_ep_tokens<A_MN, B_MN, DT, 1, 2>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((gemm_ep_tokens<A_MN, B_MN, DT, 1, N1>), grid, block, 0, s, g);
+  } else {
+    if (wide) hipLaunchKernelGGL((gemm_ep_tokens<A_MN, B_MN, DT, 2, 2>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((gemm_ep_tokens<A_MN, B_MN, DT, 2, N1>), grid, block, 0, s, g);
+  }
   return hipGetLastError();
 }
 template <int DT>

@@ -81,13 +81,13 @@ int check_workspace(const void* ws, int64_t bytes) {
 struct EpChoice {
   int kernel, bs, splits;
   int64_t kps, ws;
-  int waves;   // of a TOKENS workgroup
+  int waves, cn;   // of a TOKENS workgroup
 };
 
 int64_t part_ld(int64_t N) { return (N + 7) / 8 * 8; }
 
-EpChoice choose_ep(int64_t M, int64_t N, int64_t K, int eb, bool direct, int64_t budget) {
-  EpChoice c{TG_EP_NONE, 0, 1, K, 0, 0};
+EpChoice choose_ep(int64_t M, int64_t N, int64_t K, int transB, int eb, bool direct, int64_t budget) {
+  EpChoice c{TG_EP_NONE, 0, 1, K, 0, 0, 0};
   if (M == 0 || N == 0) return c;
   if (K == 0) {
     c.kernel = TG_EP_JOIN;
@@ -96,7 +96,23 @@ EpChoice choose_ep(int64_t M, int64_t N, int64_t K, int eb, bool direct, int64_t
   }
   if (M <= kTokenRows) {
     c.kernel = TG_EP_TOKENS;
-    c.waves = (int)std::min<int64_t>(8, (K * eb + 127) / 128);   // a step of K each at least
+    if (transB) {
+      // a workgroup for every CU, and no more where N has them to spare
+      c.cn = N >= 8192 ? 32 : N >= 4096 ? 16 : N >= 2048 ? 8 : 4;
+    } else {
+      // 64 bytes of each k-row: parts of K of at least 1024 rows (64 KB, 2.5 us, where the join costs
+      // 3 us) while there are fewer than 256 workgroups
+      c.cn = 32;
+      const int64_t per = M * part_ld(N) * 4;
+      int64_t s = std::min<int64_t>(256 / ((N + 31) / 32), K / 1024);
+      if (budget >= 0) s = std::min(s, budget / per);
+      if (s >= 2) {
+        c.kps = ((K + s - 1) / s + 31) / 32 * 32;
+        c.splits = (int)((K + c.kps - 1) / c.kps);
+        c.ws = per * c.splits;
+      }
+    }
+    c.waves = (int)std::min<int64_t>(8, (c.kps * eb + 127) / 128);   // a step of K each at least
     return c;
   }
   auto blocks = [&](int64_t b) { return ((M + b - 1) / b) * ((N + b - 1) / b); };
@@ -181,7 +197,7 @@ int plan_ep(const void* A, const void* B, const void* D, int64_t M, int64_t N, i
     return fail(TG_E_ALIAS, "D, Z and the workspace must not overlap");
 
   const bool direct = K > 0 && direct_operand(A, lda, transA, M, K, eb) && direct_operand(B, ldb, !transB, N, K, eb);
-  const EpChoice c = choose_ep(M, N, K, eb, direct, ws_bytes);
+  const EpChoice c = choose_ep(M, N, K, transB, eb, direct, ws_bytes);
   plan->kernel = c.kernel;
   plan->splits = c.splits;
   plan->k_per_split = (int32_t)c.kps;
@@ -192,9 +208,9 @@ int plan_ep(const void* A, const void* B, const void* D, int64_t M, int64_t N, i
     plan->grid = ((M + c.bs - 1) / c.bs) * ((N + c.bs - 1) / c.bs) * c.splits;
   } else if (c.kernel == TG_EP_TOKENS) {
     plan->block_m = M <= 16 ? 16 : 32;
-    plan->block_n = transB ? 16 : 32;
+    plan->block_n = c.cn;
     plan->block_k = transB ? 128 / eb : 32;
-    plan->grid = (N + plan->block_n - 1) / plan->block_n;
+    plan->grid = (N + c.cn - 1) / c.cn * c.splits;
   } else {
     plan->grid = (M * ((N + 7) / 8) + 255) / 256;
   }
@@ -215,6 +231,7 @@ int plan_ep(const void* A, const void* B, const void* D, int64_t M, int64_t N, i
     g->tiles_n = (int32_t)((N + c.bs - 1) / c.bs);
   }
   g->waves = c.waves;
+  g->cn = c.cn;
   g->splits = c.splits;
   g->k_per_split = (int32_t)c.kps;
   g->part = (float*)const_cast<void*>(ws);
@@ -239,11 +256,11 @@ int hip_status(const char* what, hipError_t e) {
 
 int run_ep(const EpArgs& g, const tg_ep_plan& p, int transA, int transB, int a_dtype, int b_dtype, hipStream_t s) {
   if (p.kernel == TG_EP_NONE) return TG_OK;
-  if (p.kernel == TG_EP_TOKENS)
-    return hip_status("tile_gemm_ep", launch_ep_tokens(g, transA, transB, a_dtype, b_dtype, g.waves, s));
-  if (p.kernel == TG_EP_DIRECT || p.kernel == TG_EP_STAGED) {
-    int st = hip_status("tile_gemm_ep", launch_ep_block(g, transA, transB, a_dtype, b_dtype, p.block_m,
-                                                        p.kernel == TG_EP_STAGED, s));
+  if (p.kernel != TG_EP_JOIN) {
+    const int st = hip_status("tile_gemm_ep", p.kernel == TG_EP_TOKENS
+                                                  ? launch_ep_tokens(g, transA, transB, a_dtype, b_dtype, g.waves, s)
+                                                  : launch_ep_block(g, transA, transB, a_dtype, b_dtype, p.block_m,
+                                                                    p.kernel == TG_EP_STAGED, s));
     if (st || g.splits == 1) return st;
   }
   return hip_status("tile_gemm_ep join", launch_ep_join(g, s));
@@ -268,10 +285,9 @@ extern "C" {
 int64_t tile_gemm_ep_workspace(int64_t M, int64_t N, int64_t K, int transA, int transB, int a_dtype) {
   if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim || (!is16(a_dtype) && !is8(a_dtype))) return 0;
   (void)transA;
-  (void)transB;
   // the direct and the staged kernel can differ in block size: the larger need
   const int eb = bytes_of(a_dtype);
-  return std::max(choose_ep(M, N, K, eb, true, -1).ws, choose_ep(M, N, K, eb, false, -1).ws);
+  return std::max(choose_ep(M, N, K, transB, eb, true, -1).ws, choose_ep(M, N, K, transB, eb, false, -1).ws);
 }
 
 int tile_gemm_ep_plan(const void* A, const void* B, const void* D, int64_t M, int64_t N, int64_t K,
