@@ -163,6 +163,12 @@ __device__ __forceinline__ uint32_t sm(uint32_t k) {
   if constexpr (SM == 0) return (k & 3u) << 1;
   else return ((k & 3u) << 1) ^ ((k & 1u) << 3);
 }
+// The swizzle for ROWB-byte k-rows: 128-byte rows (64-wide blocks of 16-bit operands) have 8 chunks.
+template <int SM, int ROWB>
+__device__ __forceinline__ uint32_t sm_row(uint32_t k) {
+  if constexpr (ROWB == 128) return sm<0>(k);
+  else return sm<SM>(k);
+}
 
 // M/N-major fp8 stage: 128 k-rows x ROWB bytes (256: 16 chunks, 128: 8 chunks); physical
 // chunk = c ^ s8(k).  A transposing read (ds_read_b64_tr_b8) of 32 lanes touches two adjacent
@@ -209,7 +215,7 @@ __device__ __forceinline__ void mn_dma_offsets(int64_t ld, int wave, int lane, u
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     const uint32_t k = RPB * (uint32_t)(PER * wave + p) + (uint32_t)lane / CH;
-    const uint32_t c = ((uint32_t)lane % CH) ^ sm<SMV>(k);
+    const uint32_t c = ((uint32_t)lane % CH) ^ sm_row<SMV, ROWB>(k);
     off[p] = (k * (uint32_t)ld + c * 8u) * 2u;    // bytes; < 64·ld·2 <= 2^32 (whole stages span at most 2^32 bytes)
   }
 }
@@ -266,7 +272,7 @@ template <int T, int ROWB>
 __device__ __forceinline__ void mn_frag_offsets(int mn_base, int lane, uint32_t (&off)[4]) {
   const uint32_t g = (uint32_t)lane >> 4, j = (uint32_t)lane & 15u;
   const uint32_t krow = 8u * (g >> 1) + (j >> 2);
-  const uint32_t x = sm<SMV>(krow);
+  const uint32_t x = sm_row<SMV, ROWB>(krow);
   const uint32_t mn_lane = 16u * (g & 1u) + 4u * (j & 3u);
   const uint32_t byte = (mn_lane & 7u) * 2u;
 #pragma unroll

@@ -3,7 +3,7 @@
 //   P = A·B (fp32 sums)   Z = row_scale[m]·col_scale[n]·P + bias[n]   D = act(Z) + residual
 //
 // Every kernel that finishes an output element (the block kernels, the token kernels and the join
-// of a split sum) goes through ep_finish8 or its even form, so all of them round once: Z and D are each
+// of a split sum) goes through ep_finish8, its 16-bit form or ep_finish1, so all of them round once: Z and D are each
 // rounded to d_dtype from the fp32 value.  Internal header.
 #pragma once
 
@@ -23,6 +23,7 @@ struct EpArgs {
   int32_t M, N, K;
   int32_t tiles_m, tiles_n;
   int32_t waves, cn;           // few rows: waves and columns of a workgroup
+  int32_t ring;                // direct blocks: four stages in flight (128 and 64 wide)
   int32_t splits, k_per_split; // the sum over K in `splits` parts of k_per_split (the last one shorter)
   float* part;                 // splits > 1: fp32 sums [splits][M][part_ld]
   int64_t part_ld;             // N rounded up to 8: rows stay 32-byte aligned
@@ -36,8 +37,12 @@ struct EpArgs {
 };
 
 // Kernel families of tile_gemm_ep (tg_ep_plan.kernel).
-hipError_t launch_ep_block(const EpArgs& g, int trans_a, int trans_b, int a_dtype, int b_dtype, int bs,
-                           bool staged, hipStream_t s);
+struct EpKernel {   // block kernels: block size 64 (staged and ring), 128 or 256 (direct)
+  int bs;
+  bool staged, ring;
+};
+hipError_t launch_ep_block(const EpArgs& g, int trans_a, int trans_b, int a_dtype, int b_dtype,
+                           const EpKernel& k, hipStream_t s);
 // M <= kTokenRows; `waves` (1 .. 8) waves share K
 constexpr int64_t kTokenRows = 32;
 hipError_t launch_ep_tokens(const EpArgs& g, int trans_a, int trans_b, int a_dtype, int b_dtype, int waves,
@@ -59,11 +64,11 @@ hipError_t launch_act_grad(const ActGradArgs& a, int groups, hipStream_t s);
 hipError_t launch_sum_rows(const float* part, int64_t G, int64_t N, float* out, hipStream_t s);
 
 // one orientation per translation unit (ep_gemm_*.hip)
-hipError_t launch_ep_kk(const EpArgs& g, int dtype, int bs, bool staged, hipStream_t s);
-hipError_t launch_ep_km(const EpArgs& g, int dtype, int bs, bool staged, hipStream_t s);
-hipError_t launch_ep_mk(const EpArgs& g, int dtype, int bs, bool staged, hipStream_t s);
-hipError_t launch_ep_mm(const EpArgs& g, int dtype, int bs, bool staged, hipStream_t s);
-hipError_t launch_ep_fp8(const EpArgs& g, int a_dtype, int b_dtype, int bs, bool staged, hipStream_t s);
+hipError_t launch_ep_kk(const EpArgs& g, int dtype, const EpKernel& k, hipStream_t s);
+hipError_t launch_ep_km(const EpArgs& g, int dtype, const EpKernel& k, hipStream_t s);
+hipError_t launch_ep_mk(const EpArgs& g, int dtype, const EpKernel& k, hipStream_t s);
+hipError_t launch_ep_mm(const EpArgs& g, int dtype, const EpKernel& k, hipStream_t s);
+hipError_t launch_ep_fp8(const EpArgs& g, int a_dtype, int b_dtype, const EpKernel& k, hipStream_t s);
 
 #ifdef __HIP__
 namespace {
@@ -289,10 +294,10 @@ __device__ __forceinline__ void ep_finish1(const EpArgs& g, int row, int col, co
   ep_with_act(g.act, [&](auto act) { p = ep_act<decltype(act)::value>(p); });
   ep_put(g.D, g.d_t, (int64_t)row * g.ldd + col, p + x.res);
 }
-// 8 columns of 16-bit results with N % 8 == 0, in two halves: what a row needs besides its sums is
-// loaded for several rows ahead of their stores (the residual may be D, so the compiler would not move
-// its load above a store), and no code for ragged columns is in the way.
-inline __host__ __device__ bool ep_even(const EpArgs& g) { return g.d_t != TG_F32 && g.N % 8 == 0; }
+// 8 whole columns of 16-bit results, in two halves: what a row needs besides its sums is loaded for
+// several rows ahead of their stores (the residual may be D, so the compiler would not move its load
+// above a store), and no code for ragged columns is in the way.
+__device__ __forceinline__ bool ep_16(const EpArgs& g) { return g.d_t != TG_F32; }
 struct EpRow {
   float rs;
   ep_u32x4 res;
@@ -302,7 +307,7 @@ __device__ __forceinline__ void ep_row(const EpArgs& g, int row, int col, EpRow&
   if (g.res) x.res = load16(g.res + 2 * ((int64_t)row * g.ldr + col));
 }
 template <int ACT>
-__device__ __forceinline__ void ep_finish8_even(const EpArgs& g, int row, int col, const EpCols& c, const EpRow& x,
+__device__ __forceinline__ void ep_finish8_16(const EpArgs& g, int row, int col, const EpCols& c, const EpRow& x,
                                                 float (&v)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = v[e] * x.rs * c.cs[e] + c.bias[e];

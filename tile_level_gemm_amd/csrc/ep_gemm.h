@@ -1,6 +1,6 @@
 // Block kernels of the matrix product with an epilogue (ep.h has the formulas).
 //
-// Blocks of BS x BS outputs by 8 waves (2 x 4), 128-byte stages of K, the LDS images, swizzles,
+// Blocks of BS x BS outputs, 128-byte stages of K, the LDS images, swizzles,
 // fragment reads and MFMA schedule of the direct-load GEMM (direct_gemm.h).  What differs:
 //
 //  * operands have leading dimensions, any M, N and K, and a block may sum only a part of K
@@ -48,10 +48,32 @@ struct StagedFetch {
   static constexpr int E = EL::kBytes, VE = 16 / E;   // elements per chunk
   u32x4 r[PER];
 
+  // A stage that is not the operand's last: every chunk is 16 bytes of memory that the operand owns.
+  // K-major rows past the end repeat the last one and M/N-major chunks may run into the next k-row;
+  // both only feed outputs that are not stored.
   // base: the block's first element at k = 0 of the block's part of K; rows: valid rows (K-major)
-  // or columns (M/N-major) of the block; kl: valid k.
-  __device__ __forceinline__ void get(const uint8_t* base, int64_t ld, int rows, int kl, int stage,
-                                      int wave, int lane) {
+  // or columns (M/N-major) of the block.
+  __device__ __forceinline__ void get_whole(const uint8_t* base, int64_t ld, int rows, int stage, int wave, int lane) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const uint32_t blk = (uint32_t)(PER * wave + i);
+      int64_t off;   // elements
+      if constexpr (MN) {
+        constexpr uint32_t ROWB = BS * E, CH = ROWB / 16, RPB = 1024 / ROWB;
+        const uint32_t k = RPB * blk + (uint32_t)lane / CH;
+        const uint32_t c = ((uint32_t)lane % CH) ^ sm_row<SMV, ROWB>(k);
+        off = (int64_t)(stage * EL::kBK + (int)k) * ld + min((int)c, (rows - 1) / VE) * VE;
+      } else {
+        const uint32_t row = 8u * blk + ((uint32_t)lane >> 3);
+        const uint32_t c = ((uint32_t)lane & 7u) ^ sk<SKV>(row);
+        off = (int64_t)min((int)row, rows - 1) * ld + stage * EL::kBK + (int)(c * VE);
+      }
+      r[i] = load16(base + off * E);
+    }
+  }
+  // any stage; kl: valid k
+  __device__ __forceinline__ void get(const uint8_t* base, int64_t ld, int rows, int kl, int stage, int wave,
+                                      int lane) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const uint32_t blk = (uint32_t)(PER * wave + i);
@@ -60,7 +82,7 @@ struct StagedFetch {
       if constexpr (MN) {
         constexpr uint32_t ROWB = BS * E, CH = ROWB / 16, RPB = 1024 / ROWB;
         const uint32_t k = RPB * blk + (uint32_t)lane / CH;
-        const uint32_t c = ((uint32_t)lane % CH) ^ sm<SMV>(k);
+        const uint32_t c = ((uint32_t)lane % CH) ^ sm_row<SMV, ROWB>(k);
         const int kk = stage * EL::kBK + (int)k;
         off = (int64_t)kk * ld + c * VE;
         n = kk < kl ? rows - (int)(c * VE) : 0;
@@ -92,52 +114,180 @@ struct StagedFetch {
   }
 };
 
-template <bool A_MN, bool B_MN, int DT, int BS, bool STAGED>
-__device__ __forceinline__ void ep_body(const EpArgs& g) {
+// Waves of a block: 2 x 4, on 64 rows and columns 2 x 2.  (4 waves of 64 x 64 on 128-wide blocks read a
+// third less of LDS, but one wave per SIMD waits for all of it: 512 x 2048 x 2048 17.2 -> 19.1 us.)
+constexpr int ep_threads(int bs) { return bs == 64 ? 256 : 512; }
+
+// What a workgroup computes: its block's first row and column, its part of K.
+struct EpTile {
+  int m0, n0, split, k0, kl;
+};
+// tile scheduler: contiguous ranges per XCD; parts of K outermost, then grouped tile-rows
+template <int BS>
+__device__ __forceinline__ EpTile ep_tile(const EpArgs& g) {
+  const int nb = (int)gridDim.x;
+  int bid = (int)blockIdx.x;
+  if ((nb & 7) == 0) bid = (bid & 7) * (nb >> 3) + (bid >> 3);
+  const int tiles = g.tiles_m * g.tiles_n;
+  EpTile t;
+  t.split = bid / tiles;
+  bid -= t.split * tiles;
+  const int group = kGroupM * g.tiles_n;
+  const int first_m = (bid / group) * kGroupM;
+  const int gsz = min(g.tiles_m - first_m, kGroupM);
+  t.m0 = (first_m + (bid % group) % gsz) * BS;
+  t.n0 = ((bid % group) / gsz) * BS;
+  t.k0 = t.split * g.k_per_split;
+  t.kl = min(g.K - t.k0, g.k_per_split);
+  return t;
+}
+
+// Epilogue, one 32-row band of the wave's tile at a time.  No wave reads or fills a stage buffer any
+// more, so the bands live there: s0 .. s3 are four stage arrays.
+// Accumulator element r of tile (i, j): row 32i + lane%32, column 32j + 8(r/4) + 4(lane/32) + r%4.
+template <int BS, int WN, int TM, int TN>
+__device__ __forceinline__ void ep_store(const EpArgs& g, const EpTile& t, f32x16 (&acc)[TM][TN], int wave,
+                                         int lane, int wm, int wn, uint8_t* s0, uint8_t* s1, uint8_t* s2,
+                                         uint8_t* s3) {
+  constexpr int LDF = WN + 4;   // floats per band row: 16-byte rows, 4 banks apart
+  static_assert((BS == 64 ? 1 : 2) * 32 * LDF * 4 <= BS * kRowBytes, "two bands (four waves: one) per stage array");
+  float* band = (float*)((wave & 2) ? ((wave & 1) ? s3 : s2) : ((wave & 1) ? s1 : s0)) + (wave >> 2) * 32 * LDF;
+  constexpr int LPR = WN / 8, RPP = 64 / LPR;   // lanes per row, rows per pass
+  const int bcol = 8 * (lane % LPR), brow = lane / LPR;
+  const int col = t.n0 + wn + bcol;
+  EpCols cols;
+  if (g.splits == 1) ep_cols(g, col, cols);
+  // The bands run in a loop, the accumulators moving down a row of tiles each time: unrolled, the
+  // epilogue was 250 KB of code, and fetching it took 16 us a 256-wide block.
+  auto from_band = [&](int p, float (&v)[8]) {
+    const float* src = band + (p * RPP + brow) * LDF + bcol;
+    const float4 lo = *(const float4*)src, hi = *(const float4*)(src + 4);
+    v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+    v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+  };
+  constexpr int NP = 32 / RPP;
+  const bool in = col < g.N, whole = ep_16(g) && col + 8 <= g.N;   // whole: the fast form
+  // residual and row scales: one band ahead of the one being stored
+  EpRow ahead[NP];
+  auto look = [&](int i) {
+    if (g.splits > 1) return;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const int row = t.m0 + wm + 32 * i + brow + p * RPP;
+      if (whole && row < g.M) ep_row(g, row, col, ahead[p]);
+    }
+  };
+  look(0);
+#pragma unroll 1
+  for (int i = 0; i < TM; ++i) {
+    const int row0 = t.m0 + wm + 32 * i + brow;
+    EpRow rows[NP];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) rows[p] = ahead[p];
+    if (i + 1 < TM) look(i + 1);
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(float4*)(band + (lane & 31) * LDF + 32 * j + 8 * q + 4 * (lane >> 5)) =
+            float4{acc[0][j][4 * q], acc[0][j][4 * q + 1], acc[0][j][4 * q + 2], acc[0][j][4 * q + 3]};
+#pragma unroll
+    for (int k = 0; k + 1 < TM; ++k)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[k][j] = acc[k + 1][j];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    float v[8];
+    if (g.splits > 1) {
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        from_band(p, v);
+        const int row = row0 + p * RPP;
+        if (in && row < g.M)
+          ep_put8((uint8_t*)g.part, TG_F32, ((int64_t)t.split * g.M + row) * g.part_ld + col, 8, v);
+      }
+    } else {
+      if (whole)
+        ep_with_act(g.act, [&](auto act) {
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            from_band(p, v);
+            const int row = row0 + p * RPP;
+            if (row < g.M) ep_finish8_16<decltype(act)::value>(g, row, col, cols, rows[p], v);
+          }
+        });
+      else if (in)
+#pragma unroll 1
+        for (int p = 0; p < NP; ++p) {
+          from_band(p, v);
+          const int row = row0 + p * RPP;
+          if (row < g.M) ep_finish8(g, row, col, cols, v);   // fp32 or a row's end: the L2 joins the pieces
+        }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+}
+
+// fills one stage's LDS images of both operands from memory
+template <bool A_MN, bool B_MN, int DT, int BS, class OA, class OB>
+struct DirectLoads {
   using EL = Elem<DT>;
-  using Frag = typename EL::Frag;
-  constexpr int WGM = 2, WGN = 4, NW = WGM * WGN;
-  constexpr int WM = BS / WGM, WN = BS / WGN, TM = WM / 32, TN = WN / 32;
-  constexpr int PER = BS / 8 / NW;
-  constexpr int E = EL::kBytes, BK = EL::kBK, NS = EL::kSteps;
-  static_assert(DT == TG_F16 || DT == TG_BF16 || (DT >= kF8 && DT < kMX), "16-bit or fp8 operands");
-  static_assert(!EL::kFp8 || (!A_MN && !B_MN), "fp8 operands are K-contiguous");
+  static constexpr int E = EL::kBytes, BK = EL::kBK;
+  OA& oa;
+  OB& ob;
+  const EpArgs& g;
+  int kl, wave;
+  uint32_t adv_a, adv_b;
+  __device__ __forceinline__ DirectLoads(OA& a, OB& b, const EpArgs& g_, const EpTile& t, int wave_)
+      : oa(a), ob(b), g(g_), kl(t.kl), wave(wave_) {
+    const uint8_t* pa = g.A + (A_MN ? (int64_t)t.k0 * g.lda + t.m0 : (int64_t)t.m0 * g.lda + t.k0) * E;
+    const uint8_t* pb = g.B + (B_MN ? (int64_t)t.k0 * g.ldb + t.n0 : (int64_t)t.n0 * g.ldb + t.k0) * E;
+    const int ra = g.M - t.m0, rb = g.N - t.n0;   // rows / columns from here to the end
+    // records: from the panel's first element to the last one of this part of K
+    oa.bind(pa, (A_MN ? (int64_t)(kl - 1) * g.lda + ra : (int64_t)(min(ra, BS) - 1) * g.lda + kl) * E);
+    ob.bind(pb, (B_MN ? (int64_t)(kl - 1) * g.ldb + rb : (int64_t)(min(rb, BS) - 1) * g.ldb + kl) * E);
+    adv_a = A_MN ? (uint32_t)(BK * g.lda * E) : (uint32_t)kRowBytes;
+    adv_b = B_MN ? (uint32_t)(BK * g.ldb * E) : (uint32_t)kRowBytes;
+  }
+  // valid bytes of each K row in stage s (K-major operands; 0 for a stage past the end)
+  __device__ __forceinline__ void operator()(int s, uint8_t* xa, uint8_t* xb) const {
+    const uint32_t lim = (uint32_t)max(0, min(kRowBytes, kl * E - s * kRowBytes));
+    oa.template load<true>((uint32_t)s * adv_a, g.lda, xa, wave, lim);
+    ob.template load<true>((uint32_t)s * adv_b, g.ldb, xb, wave, lim);
+  }
+};
+
+// Direct loads, two stages: 256-wide blocks (one workgroup per CU), and 128-wide ones where two
+// workgroups share a CU.
+template <bool A_MN, bool B_MN, int DT, int BS>
+__global__ __launch_bounds__(ep_threads(BS)) void gemm_ep_direct(EpArgs g) {
+  constexpr int WGM = 2, WGN = ep_threads(BS) / 128;
   // four named stages: their addresses stay compile-time immediates
   __shared__ __attribute__((aligned(1024))) uint8_t sa0[BS * kRowBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t sb0[BS * kRowBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t sa1[BS * kRowBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t sb1[BS * kRowBytes];
-
-  // tile scheduler: contiguous ranges per XCD; parts of K outermost, then grouped tile-rows
-  const int nb = (int)gridDim.x;
-  int bid = (int)blockIdx.x;
-  if ((nb & 7) == 0) bid = (bid & 7) * (nb >> 3) + (bid >> 3);
-  const int tiles = g.tiles_m * g.tiles_n;
-  const int split = bid / tiles;
-  bid -= split * tiles;
-  const int group = kGroupM * g.tiles_n;
-  const int first_m = (bid / group) * kGroupM;
-  const int gsz = min(g.tiles_m - first_m, kGroupM);
-  const int tm = first_m + (bid % group) % gsz;
-  const int tn = (bid % group) / gsz;
-  const int m0 = tm * BS, n0 = tn * BS;
-  const int k0 = split * g.k_per_split;
-  const int kl = min(g.K - k0, g.k_per_split);
-
+  using EL = Elem<DT>;
+  using Frag = typename EL::Frag;
+  constexpr int NW = WGM * WGN;
+  constexpr int WM = BS / WGM, WN = BS / WGN, TM = WM / 32, TN = WN / 32;
+  constexpr int PER = BS / 8 / NW;
+  constexpr int NS = EL::kSteps;
+  static_assert(DT == TG_F16 || DT == TG_BF16 || (DT >= kF8 && DT < kMX), "16-bit or fp8 operands");
+  static_assert(!EL::kFp8 || (!A_MN && !B_MN), "fp8 operands are K-contiguous");
+  const EpTile t = ep_tile<BS>(g);
   const int tid = (int)threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int wm = (wave / WGN) * WM, wn = (wave % WGN) * WN;
-
   using OA = Operand<A_MN, TM, PER, DT, BS>;
   using OB = Operand<B_MN, TN, PER, DT, BS>;
   OA oa;
   OB ob;
   oa.init(g.lda, wm, wave, lane);
   ob.init(g.ldb, wn, wave, lane);
-  const uint8_t* pa = g.A + (A_MN ? (int64_t)k0 * g.lda + m0 : (int64_t)m0 * g.lda + k0) * E;
-  const uint8_t* pb = g.B + (B_MN ? (int64_t)k0 * g.ldb + n0 : (int64_t)n0 * g.ldb + k0) * E;
-  const int ra = g.M - m0, rb = g.N - n0;   // rows / columns from here to the end
-
   f32x16 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -149,249 +299,323 @@ __device__ __forceinline__ void ep_body(const EpArgs& g) {
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = mfma32t<DT>(b[j], a[i], acc[i][j]);
   };
-  const int KT = (kl + BK - 1) / BK;   // >= 1
-  constexpr int kMfma = TM * TN;
-  constexpr int kReads = OA::kReads + OB::kReads;
+  Frag a[TM], b[TN];
+  constexpr int kReads = OA::kReads + OB::kReads, kMfma = TM * TN;
   using T_ = std::true_type;
   using F_ = std::false_type;
-  Frag a[TM], b[TN];
+  const DirectLoads<A_MN, B_MN, DT, BS, OA, OB> load_ab(oa, ob, g, t, wave);
+  const int KT = (t.kl + EL::kBK - 1) / EL::kBK;   // >= 1
+  load_ab(0, sa0, sb0);
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  Frag an[TM], bn[TN];
+  oa.frags(sa0, 0, a);
+  ob.frags(sb0, 0, b);
+  load_ab(1, sa1, sb1);
+  constexpr int kDma = 2 * PER;
 
-  if constexpr (STAGED) {
-    StagedFetch<A_MN, PER, DT, BS> fa;
-    StagedFetch<B_MN, PER, DT, BS> fb;
-    auto get = [&](int s) {
-      fa.get(pa, g.lda, ra, kl, s, wave, lane);
-      fb.get(pb, g.ldb, rb, kl, s, wave, lane);
-    };
-    auto compute = [&](const uint8_t* xa, const uint8_t* xb) {
+  // fp8: one K step in place, as direct_gemm.h — B's next fragments into spare registers, A
+  // tile i's into a[i] once its MFMAs are issued
+  auto step_inplace = [&](const uint8_t* xa, const uint8_t* xb, int sn, auto read, auto dma) {
+    if constexpr (EL::kFp8) {
+      constexpr bool kRead = decltype(read)::value;
+      if constexpr (kRead) ob.frags(xb, sn, bn);
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        oa.frags(xa, s, a);
-        ob.frags(xb, s, b);
-        mfmas(a, b);
+      for (int i = 0; i < TM; ++i) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = mfma32t<DT>(b[j], a[i], acc[i][j]);
+        if constexpr (kRead) oa.frag_tile(xa, sn, i, a[i]);
       }
-    };
-    get(0);
-    fa.put(sa0, wave, lane);
-    fb.put(sb0, wave, lane);
-    __syncthreads();
-    // stage kt from (ca, cb); stage kt+1 travels to registers meanwhile and to (na, nb_) after
-    auto stage = [&](const uint8_t* ca, const uint8_t* cb, uint8_t* na, uint8_t* nb_, int kt) {
-      const bool more = kt + 1 < KT;
-      if (more) get(kt + 1);
-      compute(ca, cb);
-      if (more) {
-        fa.put(na, wave, lane);
-        fb.put(nb_, wave, lane);
+      constexpr int nra = kRead ? OA::kTileReads : 0, nrb = kRead ? OB::kReads : 0;
+      interleave_inplace<TN, kMfma, nra, nrb, decltype(dma)::value ? kDma : 0>();
+      if constexpr (kRead) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) b[j] = bn[j];
       }
+    }
+  };
+  // one K stage; dma: also load stage kt+2 into the buffer this one frees; next: read the next
+  // stage's first fragments
+  auto stage = [&](uint8_t* ca, uint8_t* cb, const uint8_t* na, const uint8_t* nb_, int kt, auto dma,
+                   auto next) {
+    if constexpr (EL::kFp8) {
+      step_inplace(ca, cb, 1, T_{}, F_{});
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(0);
       __syncthreads();
-    };
-    for (int kt = 0; kt < KT; kt += 2) {
-      stage(sa0, sb0, sa1, sb1, kt);
-      if (kt + 1 < KT) stage(sa1, sb1, sa0, sb0, kt + 1);
-    }
-  } else {
-    // records: from the panel's first element to the last one of this part of K
-    oa.bind(pa, (A_MN ? (int64_t)(kl - 1) * g.lda + ra : (int64_t)(min(ra, BS) - 1) * g.lda + kl) * E);
-    ob.bind(pb, (B_MN ? (int64_t)(kl - 1) * g.ldb + rb : (int64_t)(min(rb, BS) - 1) * g.ldb + kl) * E);
-    const uint32_t adv_a = A_MN ? (uint32_t)(BK * g.lda * E) : (uint32_t)kRowBytes;
-    const uint32_t adv_b = B_MN ? (uint32_t)(BK * g.ldb * E) : (uint32_t)kRowBytes;
-    // valid bytes of each K row in stage s (K-major operands; 0 for a stage past the end)
-    auto lim = [&](int s) -> uint32_t { return (uint32_t)max(0, min(kRowBytes, kl * E - s * kRowBytes)); };
-    auto load_ab = [&](int s, uint8_t* xa, uint8_t* xb) {
-      oa.template load<true>((uint32_t)s * adv_a, g.lda, xa, wave, lim(s));
-      ob.template load<true>((uint32_t)s * adv_b, g.ldb, xb, wave, lim(s));
-    };
-    load_ab(0, sa0, sb0);
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    Frag an[TM], bn[TN];
-    oa.frags(sa0, 0, a);
-    ob.frags(sb0, 0, b);
-    load_ab(1, sa1, sb1);
-    constexpr int kDma = 2 * PER;
-
-    // fp8: one K step in place, as direct_gemm.h — B's next fragments into spare registers, A
-    // tile i's into a[i] once its MFMAs are issued
-    auto step_inplace = [&](const uint8_t* xa, const uint8_t* xb, int sn, auto read, auto dma) {
-      if constexpr (EL::kFp8) {
-        constexpr bool kRead = decltype(read)::value;
-        if constexpr (kRead) ob.frags(xb, sn, bn);
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-#pragma unroll
-          for (int j = 0; j < TN; ++j) acc[i][j] = mfma32t<DT>(b[j], a[i], acc[i][j]);
-          if constexpr (kRead) oa.frag_tile(xa, sn, i, a[i]);
-        }
-        constexpr int nra = kRead ? OA::kTileReads : 0, nrb = kRead ? OB::kReads : 0;
-        interleave_inplace<TN, kMfma, nra, nrb, decltype(dma)::value ? kDma : 0>();
-        if constexpr (kRead) {
-#pragma unroll
-          for (int j = 0; j < TN; ++j) b[j] = bn[j];
-        }
-      }
-    };
-    // one K stage; dma: also load stage kt+2 into the buffer this one frees; next: read the next
-    // stage's first fragments
-    auto stage = [&](uint8_t* ca, uint8_t* cb, const uint8_t* na, const uint8_t* nb_, int kt, auto dma,
-                     auto next) {
-      if constexpr (EL::kFp8) {
-        step_inplace(ca, cb, 1, T_{}, F_{});
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();
-        if constexpr (decltype(dma)::value) load_ab(kt + 2, ca, cb);
-        step_inplace(na, nb_, 0, next, dma);
-      } else {
-#pragma unroll
-        for (int s = 0; s < NS - 1; ++s) {
-          oa.frags(ca, s + 1, an);
-          ob.frags(cb, s + 1, bn);
-          mfmas(a, b);
-          interleave<kMfma, kReads, 0>();
-#pragma unroll
-          for (int i = 0; i < TM; ++i) a[i] = an[i];
-#pragma unroll
-          for (int j = 0; j < TN; ++j) b[j] = bn[j];
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();
-        if constexpr (decltype(next)::value) {
-          oa.frags(na, 0, an);
-          ob.frags(nb_, 0, bn);
-        }
-        if constexpr (decltype(dma)::value) load_ab(kt + 2, ca, cb);
-        mfmas(a, b);
-        if constexpr (decltype(dma)::value) interleave<kMfma, kReads, kDma>();
-        else if constexpr (decltype(next)::value) interleave<kMfma, kReads, 0>();
-        if constexpr (decltype(next)::value) {
-#pragma unroll
-          for (int i = 0; i < TM; ++i) a[i] = an[i];
-#pragma unroll
-          for (int j = 0; j < TN; ++j) b[j] = bn[j];
-        }
-      }
-    };
-    int kt = 0;
-    for (; kt + 2 < KT; kt += 2) {   // KT rounded up to even; the last two stages are peeled
-      stage(sa0, sb0, sa1, sb1, kt, T_{}, T_{});
-      stage(sa1, sb1, sa0, sb0, kt + 1, T_{}, T_{});
-    }
-    stage(sa0, sb0, sa1, sb1, kt, F_{}, T_{});
-    stage(sa1, sb1, sa0, sb0, kt + 1, F_{}, F_{});
-  }
-
-  // Epilogue, one 32-row band of the wave's tile at a time.  No wave reads a stage buffer after
-  // the last barrier, so the bands live there: two wave regions in each of the four arrays.
-  // Accumulator element r of tile (i, j): row 32i + lane%32, column 32j + 8(r/4) + 4(lane/32) + r%4.
-  constexpr int LDF = WN + 4;   // floats per band row: 16-byte rows, 4 banks apart
-  static_assert(2 * 32 * LDF * 4 <= BS * kRowBytes, "two bands per stage array");
-  float* band = (float*)((wave & 2) ? ((wave & 1) ? sb1 : sa1) : ((wave & 1) ? sb0 : sa0)) +
-                (wave >> 2) * 32 * LDF;
-  constexpr int LPR = WN / 8, RPP = 64 / LPR;   // lanes per row, rows per pass
-  const int bcol = 8 * (lane % LPR), brow = lane / LPR;
-  const int col = n0 + wn + bcol;
-  EpCols cols;
-  if (g.splits == 1) ep_cols(g, col, cols);
-  // The bands run in a loop whose only unrolled part is the write from the accumulators: unrolled
-  // whole, the epilogue was 250 KB of code, and fetching it took 16 us a 256-wide block.
-  auto to_band = [&](auto I) {
-    constexpr int i = decltype(I)::value < TM ? decltype(I)::value : 0;   // compile-time: registers
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *(float4*)(band + (lane & 31) * LDF + 32 * j + 8 * q + 4 * (lane >> 5)) =
-            float4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-  };
-  auto from_band = [&](int p, float (&v)[8]) {
-    const float* src = band + (p * RPP + brow) * LDF + bcol;
-    const float4 lo = *(const float4*)src, hi = *(const float4*)(src + 4);
-    v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
-    v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
-  };
-  constexpr int NP = 32 / RPP;
-  const bool even = ep_even(g), in = col < g.N;
-  // residual and row scales: one band ahead of the one being stored
-  EpRow ahead[NP];
-  auto look = [&](int i) {
-    if (g.splits > 1 || !even) return;
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      const int row = m0 + wm + 32 * i + brow + p * RPP;
-      if (in && row < g.M) ep_row(g, row, col, ahead[p]);
-    }
-  };
-  look(0);
-#pragma unroll 1
-  for (int i = 0; i < TM; ++i) {
-    const int row0 = m0 + wm + 32 * i + brow;
-    EpRow rows[NP];
-#pragma unroll
-    for (int p = 0; p < NP; ++p) rows[p] = ahead[p];
-    if (i + 1 < TM) look(i + 1);
-    if (i == 0) to_band(std::integral_constant<int, 0>{});
-    else if (i == 1) to_band(std::integral_constant<int, 1>{});
-    else if (i == 2) to_band(std::integral_constant<int, 2>{});
-    else to_band(std::integral_constant<int, 3>{});
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    float v[8];
-    if (g.splits > 1) {
-#pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        from_band(p, v);
-        const int row = row0 + p * RPP;
-        if (in && row < g.M)
-          ep_put8((uint8_t*)g.part, TG_F32, ((int64_t)split * g.M + row) * g.part_ld + col, 8, v);
-      }
-    } else if (even) {
-      ep_with_act(g.act, [&](auto act) {
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          from_band(p, v);
-          const int row = row0 + p * RPP;
-          if (in && row < g.M) ep_finish8_even<decltype(act)::value>(g, row, col, cols, rows[p], v);
-        }
-      });
+      if constexpr (decltype(dma)::value) load_ab(kt + 2, ca, cb);
+      step_inplace(na, nb_, 0, next, dma);
     } else {
-#pragma unroll 1
-      for (int p = 0; p < NP; ++p) {
-        from_band(p, v);
-        const int row = row0 + p * RPP;
-        if (in && row < g.M) ep_finish8(g, row, col, cols, v);   // fp32 or ragged: the L2 joins the pieces
+#pragma unroll
+      for (int s = 0; s < NS - 1; ++s) {
+        oa.frags(ca, s + 1, an);
+        ob.frags(cb, s + 1, bn);
+        mfmas(a, b);
+        interleave<kMfma, kReads, 0>();
+#pragma unroll
+        for (int i = 0; i < TM; ++i) a[i] = an[i];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) b[j] = bn[j];
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      if constexpr (decltype(next)::value) {
+        oa.frags(na, 0, an);
+        ob.frags(nb_, 0, bn);
+      }
+      if constexpr (decltype(dma)::value) load_ab(kt + 2, ca, cb);
+      mfmas(a, b);
+      if constexpr (decltype(dma)::value) interleave<kMfma, kReads, kDma>();
+      else if constexpr (decltype(next)::value) interleave<kMfma, kReads, 0>();
+      if constexpr (decltype(next)::value) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) a[i] = an[i];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) b[j] = bn[j];
       }
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  };
+  int kt = 0;
+  for (; kt + 2 < KT; kt += 2) {   // KT rounded up to even; the last two stages are peeled
+    stage(sa0, sb0, sa1, sb1, kt, T_{}, T_{});
+    stage(sa1, sb1, sa0, sb0, kt + 1, T_{}, T_{});
   }
+  stage(sa0, sb0, sa1, sb1, kt, F_{}, T_{});
+  stage(sa1, sb1, sa0, sb0, kt + 1, F_{}, F_{});
+  ep_store<BS, WN, TM, TN>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
 }
 
+// s_waitcnt: at most n vector memory instructions outstanding (n < 64), no LDS read
+constexpr int wait_vm(int n) { return (n & 15) | 7 << 4 | (n >> 4) << 14; }
+
+// Direct loads, a ring of four stages (128 KiB on 128-wide blocks): the loads of a stage have three
+// stages' time to arrive where two leave one.  For problems of few blocks, whose stages come from far
+// away and whose CUs hold one workgroup anyway.
+// Stage kt of slot kt % 4: before its last K step the wave waits until its own loads of stage kt + 1
+// have landed (those of kt + 2 and kt + 3 stay in flight) and meets the others at the barrier, so
+// stage kt + 1 is whole and slot kt % 4 free; the last step's products cover the first fragment reads
+// of kt + 1 and the issue of stage kt + 4.  Stages past K read as zeros and touch no memory.
 template <bool A_MN, bool B_MN, int DT, int BS>
-__global__ __launch_bounds__(512) void gemm_ep_direct(EpArgs g) {
-  ep_body<A_MN, B_MN, DT, BS, false>(g);
+__global__ __launch_bounds__(ep_threads(BS)) void gemm_ep_ring(EpArgs g) {
+  constexpr int WGM = 2, WGN = ep_threads(BS) / 128;
+  // one array a stage, A's image and then B's: the compiler tells the loads in flight apart by array
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[2 * BS * kRowBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t s1[2 * BS * kRowBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t s2[2 * BS * kRowBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t s3[2 * BS * kRowBytes];
+  constexpr int kB = BS * kRowBytes;
+  using EL = Elem<DT>;
+  using Frag = typename EL::Frag;
+  constexpr int NW = WGM * WGN;
+  constexpr int WM = BS / WGM, WN = BS / WGN, TM = WM / 32, TN = WN / 32;
+  constexpr int PER = BS / 8 / NW;
+  constexpr int NS = EL::kSteps;
+  static_assert(DT == TG_F16 || DT == TG_BF16 || (DT >= kF8 && DT < kMX), "16-bit or fp8 operands");
+  static_assert(!EL::kFp8 || (!A_MN && !B_MN), "fp8 operands are K-contiguous");
+  const EpTile t = ep_tile<BS>(g);
+  const int tid = (int)threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int wm = (wave / WGN) * WM, wn = (wave % WGN) * WN;
+  using OA = Operand<A_MN, TM, PER, DT, BS>;
+  using OB = Operand<B_MN, TN, PER, DT, BS>;
+  OA oa;
+  OB ob;
+  oa.init(g.lda, wm, wave, lane);
+  ob.init(g.ldb, wn, wave, lane);
+  f32x16 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = f32x16{};
+  auto mfmas = [&](const Frag (&a)[TM], const Frag (&b)[TN]) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = mfma32t<DT>(b[j], a[i], acc[i][j]);
+  };
+  Frag a[TM], b[TN];
+  constexpr int kReads = OA::kReads + OB::kReads, kMfma = TM * TN, kDma = 2 * PER;
+  const DirectLoads<A_MN, B_MN, DT, BS, OA, OB> load_ab(oa, ob, g, t, wave);
+  const int KT = (t.kl + EL::kBK - 1) / EL::kBK;   // >= 1
+  // the barrier alone: __syncthreads would wait for every load
+  auto meet = [&](auto n) {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(wait_vm(decltype(n)::value));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  load_ab(0, s0, s0 + kB);
+  load_ab(1, s1, s1 + kB);
+  load_ab(2, s2, s2 + kB);
+  load_ab(3, s3, s3 + kB);
+  meet(std::integral_constant<int, 3 * kDma>{});
+  Frag an[TM], bn[TN];
+  oa.frags(s0, 0, a);
+  ob.frags(s0 + kB, 0, b);
+  auto keep = [&]() {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) a[i] = an[i];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) b[j] = bn[j];
+  };
+  auto stage = [&](uint8_t* cur, const uint8_t* next, int kt) {
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) {
+      oa.frags(cur, s + 1, an);
+      ob.frags(cur + kB, s + 1, bn);
+      mfmas(a, b);
+      interleave<kMfma, kReads, 0>();
+      keep();
+    }
+    meet(std::integral_constant<int, 2 * kDma>{});
+    oa.frags(next, 0, an);
+    ob.frags(next + kB, 0, bn);
+    load_ab(kt + 4, cur, cur + kB);
+    mfmas(a, b);
+    interleave<kMfma, kReads, kDma>();
+    keep();
+  };
+  // No way out of the middle of a round: the compiler would count the loads of every exit as possibly
+  // in flight at the loop's head, and wait for all of them there.
+  int kt = 0;
+  for (; kt + 4 <= KT; kt += 4) {
+    stage(s0, s1, kt);
+    stage(s1, s2, kt + 1);
+    stage(s2, s3, kt + 2);
+    stage(s3, s0, kt + 3);
+  }
+  if (kt < KT) {
+    stage(s0, s1, kt);
+    if (kt + 1 < KT) {
+      stage(s1, s2, kt + 1);
+      if (kt + 2 < KT) stage(s2, s3, kt + 2);
+    }
+  }
+  // the zero stages still on their way must land before the epilogue takes the buffers
+  meet(std::integral_constant<int, 0>{});
+  ep_store<BS, WN, TM, TN>(g, t, acc, wave, lane, wm, wn, s0, s1, s2, s3);
 }
-template <bool A_MN, bool B_MN, int DT>
-__global__ __launch_bounds__(512) void gemm_ep_staged(EpArgs g) {
-  ep_body<A_MN, B_MN, DT, 128, true>(g);
+
+// Operands through registers, two stages ahead of the one computed.
+template <bool A_MN, bool B_MN, int DT, int BS>
+__global__ __launch_bounds__(ep_threads(BS)) void gemm_ep_staged(EpArgs g) {
+  constexpr int WGM = 2, WGN = ep_threads(BS) / 128;
+  __shared__ __attribute__((aligned(1024))) uint8_t sa0[BS * kRowBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t sb0[BS * kRowBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t sa1[BS * kRowBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t sb1[BS * kRowBytes];
+  using EL = Elem<DT>;
+  using Frag = typename EL::Frag;
+  constexpr int NW = WGM * WGN;
+  constexpr int WM = BS / WGM, WN = BS / WGN, TM = WM / 32, TN = WN / 32;
+  constexpr int PER = BS / 8 / NW;
+  constexpr int NS = EL::kSteps;
+  static_assert(DT == TG_F16 || DT == TG_BF16 || (DT >= kF8 && DT < kMX), "16-bit or fp8 operands");
+  static_assert(!EL::kFp8 || (!A_MN && !B_MN), "fp8 operands are K-contiguous");
+  const EpTile t = ep_tile<BS>(g);
+  const int tid = (int)threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int wm = (wave / WGN) * WM, wn = (wave % WGN) * WN;
+  using OA = Operand<A_MN, TM, PER, DT, BS>;
+  using OB = Operand<B_MN, TN, PER, DT, BS>;
+  OA oa;
+  OB ob;
+  oa.init(g.lda, wm, wave, lane);
+  ob.init(g.ldb, wn, wave, lane);
+  f32x16 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = f32x16{};
+  auto mfmas = [&](const Frag (&a)[TM], const Frag (&b)[TN]) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = mfma32t<DT>(b[j], a[i], acc[i][j]);
+  };
+  Frag a[TM], b[TN];
+  constexpr int E = EL::kBytes;
+  const uint8_t* pa = g.A + (A_MN ? (int64_t)t.k0 * g.lda + t.m0 : (int64_t)t.m0 * g.lda + t.k0) * E;
+  const uint8_t* pb = g.B + (B_MN ? (int64_t)t.k0 * g.ldb + t.n0 : (int64_t)t.n0 * g.ldb + t.k0) * E;
+  const int ra = g.M - t.m0, rb = g.N - t.n0;   // rows / columns from here to the end
+  const int KT = (t.kl + EL::kBK - 1) / EL::kBK;   // >= 1
+  StagedFetch<A_MN, PER, DT, BS> fa0, fa1;
+  StagedFetch<B_MN, PER, DT, BS> fb0, fb1;
+  // (a row pitch below 16 bytes could leave the operand even before its last stage)
+  const bool pitch = (!A_MN || g.lda >= 16 / E) && (!B_MN || g.ldb >= 16 / E);
+  using T_ = std::true_type;
+  using F_ = std::false_type;
+  // inner: stage s is known to be a whole one
+  auto get = [&](auto& fa, auto& fb, int s, auto inner) {
+    if (decltype(inner)::value || (pitch && s + 1 < KT)) {
+      fa.get_whole(pa, g.lda, ra, s, wave, lane);
+      fb.get_whole(pb, g.ldb, rb, s, wave, lane);
+    } else if (s < KT) {
+      fa.get(pa, g.lda, ra, t.kl, s, wave, lane);
+      fb.get(pb, g.ldb, rb, t.kl, s, wave, lane);
+    }
+    __builtin_amdgcn_sched_barrier(0);   // on their way before the stage's products
+  };
+  get(fa0, fb0, 0, F_{});
+  get(fa1, fb1, 1, F_{});
+  fa0.put(sa0, wave, lane);
+  fb0.put(sb0, wave, lane);
+  __syncthreads();
+  // stage kt from (ca, cb); stage kt + 1, loaded a stage ago, goes to (na, nb) after it, and its
+  // registers' successor kt + 2 sets out before it
+  auto stage = [&](const uint8_t* ca, const uint8_t* cb, uint8_t* na, uint8_t* nb, int kt, auto& fa, auto& fb,
+                   const auto& ga, const auto& gb, auto inner) {
+    get(fa, fb, kt + 2, inner);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      oa.frags(ca, s, a);
+      ob.frags(cb, s, b);
+      mfmas(a, b);
+    }
+    if (decltype(inner)::value || kt + 1 < KT) {
+      ga.put(na, wave, lane);
+      gb.put(nb, wave, lane);
+    }
+    __syncthreads();
+  };
+  // the loop that counts has whole stages only: element-by-element loads beside it would make the
+  // compiler wait for every load in flight
+  int kt = 0;
+  if (pitch)
+    for (; kt + 4 < KT; kt += 2) {
+      stage(sa0, sb0, sa1, sb1, kt, fa0, fb0, fa1, fb1, T_{});
+      stage(sa1, sb1, sa0, sb0, kt + 1, fa1, fb1, fa0, fb0, T_{});
+    }
+  for (; kt < KT; kt += 2) {
+    stage(sa0, sb0, sa1, sb1, kt, fa0, fb0, fa1, fb1, F_{});
+    if (kt + 1 < KT) stage(sa1, sb1, sa0, sb0, kt + 1, fa1, fb1, fa0, fb0, F_{});
+  }
+  ep_store<BS, WN, TM, TN>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
 }
 
 template <bool A_MN, bool B_MN, int DT>
-hipError_t launch_ep_one(const EpArgs& g, int bs, bool staged, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)g.tiles_m * g.tiles_n * g.splits)), block(512);
-  if (staged) hipLaunchKernelGGL((gemm_ep_staged<A_MN, B_MN, DT>), grid, block, 0, s, g);
-  else if (bs == 256) hipLaunchKernelGGL((gemm_ep_direct<A_MN, B_MN, DT, 256>), grid, block, 0, s, g);
-  else hipLaunchKernelGGL((gemm_ep_direct<A_MN, B_MN, DT, 128>), grid, block, 0, s, g);
+hipError_t launch_ep_one(const EpArgs& g, const EpKernel& k, hipStream_t s) {
+  const dim3 grid((unsigned)((int64_t)g.tiles_m * g.tiles_n * g.splits)), block(ep_threads(k.bs));
+  if (k.staged) {
+    if (k.bs == 64) hipLaunchKernelGGL((gemm_ep_staged<A_MN, B_MN, DT, 64>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((gemm_ep_staged<A_MN, B_MN, DT, 128>), grid, block, 0, s, g);
+  } else if (k.ring) {
+    if (k.bs == 64) hipLaunchKernelGGL((gemm_ep_ring<A_MN, B_MN, DT, 64>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((gemm_ep_ring<A_MN, B_MN, DT, 128>), grid, block, 0, s, g);
+  } else {
+    if (k.bs == 256) hipLaunchKernelGGL((gemm_ep_direct<A_MN, B_MN, DT, 256>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((gemm_ep_direct<A_MN, B_MN, DT, 128>), grid, block, 0, s, g);
+  }
   return hipGetLastError();
 }
 
 template <bool A_MN, bool B_MN>
-hipError_t launch_ep_layout(const EpArgs& g, int dtype, int bs, bool staged, hipStream_t s) {
-  return dtype == TG_F16 ? launch_ep_one<A_MN, B_MN, TG_F16>(g, bs, staged, s)
-                         : launch_ep_one<A_MN, B_MN, TG_BF16>(g, bs, staged, s);
+hipError_t launch_ep_layout(const EpArgs& g, int dtype, const EpKernel& k, hipStream_t s) {
+  return dtype == TG_F16 ? launch_ep_one<A_MN, B_MN, TG_F16>(g, k, s)
+                         : launch_ep_one<A_MN, B_MN, TG_BF16>(g, k, s);
 }
 
 }  // namespace

@@ -3,8 +3,8 @@
 
 namespace tg {
 
-hipError_t launch_ep_kk(const EpArgs& g, int dtype, int bs, bool staged, hipStream_t s) {
-  return launch_ep_layout<false, false>(g, dtype, bs, staged, s);
+hipError_t launch_ep_kk(const EpArgs& g, int dtype, const EpKernel& k, hipStream_t s) {
+  return launch_ep_layout<false, false>(g, dtype, k, s);
 }
 
 }  // namespace tg

@@ -112,11 +112,11 @@ hipError_t launch_sum_rows(const float* part, int64_t G, int64_t N, float* out, 
   return hipGetLastError();
 }
 
-hipError_t launch_ep_block(const EpArgs& g, int trans_a, int trans_b, int a_dtype, int b_dtype, int bs,
-                           bool staged, hipStream_t s) {
-  if (a_dtype == TG_FP8_E4M3 || a_dtype == TG_FP8_E5M2) return launch_ep_fp8(g, a_dtype, b_dtype, bs, staged, s);
-  if (trans_a) return trans_b ? launch_ep_mk(g, a_dtype, bs, staged, s) : launch_ep_mm(g, a_dtype, bs, staged, s);
-  return trans_b ? launch_ep_kk(g, a_dtype, bs, staged, s) : launch_ep_km(g, a_dtype, bs, staged, s);
+hipError_t launch_ep_block(const EpArgs& g, int trans_a, int trans_b, int a_dtype, int b_dtype,
+                           const EpKernel& k, hipStream_t s) {
+  if (a_dtype == TG_FP8_E4M3 || a_dtype == TG_FP8_E5M2) return launch_ep_fp8(g, a_dtype, b_dtype, k, s);
+  if (trans_a) return trans_b ? launch_ep_mk(g, a_dtype, k, s) : launch_ep_mm(g, a_dtype, k, s);
+  return trans_b ? launch_ep_kk(g, a_dtype, k, s) : launch_ep_km(g, a_dtype, k, s);
 }
 
 }  // namespace tg

@@ -82,12 +82,13 @@ struct EpChoice {
   int kernel, bs, splits;
   int64_t kps, ws;
   int waves, cn;   // of a TOKENS workgroup
+  bool ring;       // direct blocks in the four-stage ring
 };
 
 int64_t part_ld(int64_t N) { return (N + 7) / 8 * 8; }
 
 EpChoice choose_ep(int64_t M, int64_t N, int64_t K, int transB, int eb, bool direct, int64_t budget) {
-  EpChoice c{TG_EP_NONE, 0, 1, K, 0, 0, 0};
+  EpChoice c{TG_EP_NONE, 0, 1, K, 0, 0, 0, false};
   if (M == 0 || N == 0) return c;
   if (K == 0) {
     c.kernel = TG_EP_JOIN;
@@ -116,19 +117,34 @@ EpChoice choose_ep(int64_t M, int64_t N, int64_t K, int transB, int eb, bool dir
     return c;
   }
   auto blocks = [&](int64_t b) { return ((M + b - 1) / b) * ((N + b - 1) / b); };
-  // 256-wide blocks once they fill the chip, as tile_gemm's choice; the staged kernel has 128 only
+  // Times below: bf16, MI355X, M x N x K.
+  const int64_t bk = 128 / eb, steps = (K + bk - 1) / bk;
   c.kernel = direct ? TG_EP_DIRECT : TG_EP_STAGED;
-  c.bs = direct && (blocks(256) >= 256 || blocks(128) > 512) ? 256 : 128;
-  if (c.bs == 256) return c;
-  // Few tiles and a long sum: parts of K until two workgroups per CU are busy, each part at least
-  // four stages (128 bytes of K per stage)
-  const int64_t tiles = blocks(128), bk = 128 / eb, steps = (K + bk - 1) / bk;
+  int64_t s = 1;   // parts of K
+  if (direct && (blocks(256) >= 256 || blocks(128) > 512)) {
+    // 256-wide blocks once they fill the chip (2048 x 4096 x 4096, 128 of them: 77 us, 128-wide 69)
+    c.bs = 256;
+  } else if (direct && blocks(256) >= 112 && blocks(256) <= 128 && steps >= 96) {
+    // half the chip's worth and a long sum: two parts (4096 x 2048 x 8192: 129 us, 128-wide 138)
+    c.bs = 256;
+    s = 2;
+  } else if (blocks(128) >= 192) {
+    // 128-wide; at most one a CU: the ring of four stages (2048 x 2048 x 2048: 23.7 us, two stages
+    // 28.3), else two workgroups of two stages on a CU (2048 x 3000 x 1000: 26.9 us, ring 30.8)
+    c.bs = 128;
+    c.ring = direct && blocks(128) <= 256;
+  } else {
+    // 64-wide (1024 x 1024 x 1024: 7.7 us, 128-wide 11.4), and parts of K of at least 16 stages while
+    // they leave CUs without work (64 x 4096 x 4096: one part 16.4 us, four 12.6, eight 13.8)
+    c.bs = 64;
+    c.ring = direct;
+    s = std::min(256 / blocks(64), steps / 16);
+  }
   const int64_t per = M * part_ld(N) * 4;
-  int64_t s = std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), steps / 4);
   if (budget >= 0) s = std::min(s, budget / per);
   if (s < 2) return c;
   int64_t each = (steps + s - 1) / s;
-  each += each & 1;   // whole stage pairs
+  if (c.bs == 256) each += each & 1;   // whole stage pairs
   c.splits = (int)((steps + each - 1) / each);
   c.kps = each * bk;
   if (c.splits < 2) {
@@ -144,7 +160,7 @@ EpChoice choose_ep(int64_t M, int64_t N, int64_t K, int transB, int eb, bool dir
 // every 32-bit offset of a block's panel below 2^31.
 bool direct_operand(const void* p, int64_t ld, bool mn, int64_t extent, int64_t K, int eb) {
   if (misaligned(p, 16) || (ld * eb) % 16) return false;
-  if (mn) return (extent * eb) % 16 == 0 && (K + 256) * ld * eb < kDirectSpan;
+  if (mn) return (extent * eb) % 16 == 0 && (K + 512) * ld * eb < kDirectSpan;
   return (K * eb) % 16 == 0 && 256 * ld * eb + K * eb + 1024 < kDirectSpan;
 }
 
@@ -232,6 +248,7 @@ int plan_ep(const void* A, const void* B, const void* D, int64_t M, int64_t N, i
   }
   g->waves = c.waves;
   g->cn = c.cn;
+  g->ring = c.ring;
   g->splits = c.splits;
   g->k_per_split = (int32_t)c.kps;
   g->part = (float*)const_cast<void*>(ws);
@@ -259,8 +276,8 @@ int run_ep(const EpArgs& g, const tg_ep_plan& p, int transA, int transB, int a_d
   if (p.kernel != TG_EP_JOIN) {
     const int st = hip_status("tile_gemm_ep", p.kernel == TG_EP_TOKENS
                                                   ? launch_ep_tokens(g, transA, transB, a_dtype, b_dtype, g.waves, s)
-                                                  : launch_ep_block(g, transA, transB, a_dtype, b_dtype, p.block_m,
-                                                                    p.kernel == TG_EP_STAGED, s));
+                                                  : launch_ep_block(g, transA, transB, a_dtype, b_dtype,
+                                                                    {p.block_m, p.kernel == TG_EP_STAGED, g.ring != 0}, s));
     if (st || g.splits == 1) return st;
   }
   return hip_status("tile_gemm_ep join", launch_ep_join(g, s));
