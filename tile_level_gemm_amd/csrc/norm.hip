@@ -7,9 +7,10 @@
 //   backward: g = dY·w, xh = H·rstd, dX = rstd·(g − xh·mean(g·xh)) + dH, dw = Σ_rows dY·xh.
 //
 // All of it is bound by memory: one pass, the row kept in registers between the reduction and
-// the result (TPR threads per row x NV chunks of 8 columns).  Rows up to 1024 columns take one
-// wave each and no barrier; longer ones a workgroup.  The sum of squares and max|H·w| (a row
-// scale needs it: max|Y| = rstd·max|H·w|) travel in one reduction.
+// the result, NV chunks of 8 columns a thread.  Rows up to 1024 columns take one wave each and no
+// barrier; longer ones a workgroup of as many waves as their chunks need (1003 x 2057: 5 waves of one
+// chunk 5.4 us, 4 waves of two 6.2).  The sum of squares and max|H·w| (a row scale needs it:
+// max|Y| = rstd·max|H·w|) travel in one reduction.
 // Rows whose length is not a multiple of 8 end in a chunk moved back to the row's last 8
 // columns: every load is a whole vector, the columns another chunk owns (`dup` of them) are left
 // out of the sums, and both owners store the same values.
@@ -72,13 +73,15 @@ __device__ __forceinline__ int block_exp(float amax, int t) {
   return (int)((b + 0x1fffffu) >> 23) - 127 - (t == TG_FP8_E4M3 ? 8 : 15);
 }
 
-// Reduce (sum, max) over TPR threads; every thread gets the result.  red: one slot per wave.
-template <int TPR>
+// Reduce (sum, max) over a row's threads; every thread gets the result.  WAVE: one wave, else the
+// workgroup's waves, one slot of `red` each.
+constexpr int kMaxWaves = 16;
+template <bool WAVE>
 __device__ __forceinline__ void row_reduce(float& s, float& m, bool want_max, float (*red)[2]) {
   s = wave_sum(s);
   if (want_max) m = wave_max(m);
-  if constexpr (TPR > 64) {
-    const int w = (int)threadIdx.x >> 6;
+  if constexpr (!WAVE) {
+    const int w = (int)threadIdx.x >> 6, n = (int)blockDim.x >> 6;
     if ((threadIdx.x & 63) == 0) {
       red[w][0] = s;
       red[w][1] = m;
@@ -86,8 +89,8 @@ __device__ __forceinline__ void row_reduce(float& s, float& m, bool want_max, fl
     __syncthreads();
     s = 0.0f;
     m = red[0][1];
-#pragma unroll
-    for (int i = 0; i < TPR / 64; ++i) {
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
       s += red[i][0];
       if (want_max) m = nan_max(m, red[i][1]);
     }
@@ -95,12 +98,14 @@ __device__ __forceinline__ void row_reduce(float& s, float& m, bool want_max, fl
 }
 
 // SC: tg_scale_kind of the result
-template <int DT, int TPR, int NV, int SC>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm(NormArgs a) {
-  __shared__ float red[TPR > 64 ? TPR / 64 : 1][2];
-  const int t = (int)threadIdx.x % TPR;
-  const int64_t row = TPR == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
-  if (TPR == 64 && row >= a.rows) return;
+// WAVE: a wave per row, four rows a workgroup; else a workgroup per row.
+template <int DT, int NV, int SC, bool WAVE, int MAXT>
+__global__ __launch_bounds__(MAXT) void rmsnorm(NormArgs a) {
+  __shared__ float red[WAVE ? 1 : kMaxWaves][2];
+  const int TPR = WAVE ? 64 : (int)blockDim.x;
+  const int t = WAVE ? (int)threadIdx.x & 63 : (int)threadIdx.x;
+  const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
+  if (WAVE && row >= a.rows) return;
   const int cols = (int)a.cols;
   float h[NV][8], w[NV][8];
 #pragma unroll
@@ -136,7 +141,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm(NormArgs a) {
       if constexpr (SC == TG_SCALE_ROW) top = nan_max(top, fabsf(h[j][e] * w[j][e]));
     }
   }
-  row_reduce<TPR>(ss, top, SC == TG_SCALE_ROW, red);
+  row_reduce<WAVE>(ss, top, SC == TG_SCALE_ROW, red);
   const float rstd = 1.0f / sqrtf(ss / (float)cols + a.eps);
   float inv = 1.0f;
   if constexpr (SC == TG_SCALE_ROW) {
@@ -207,7 +212,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_long(NormArgs a) {
       if constexpr (SC == TG_SCALE_ROW) top = nan_max(top, fabsf(h[e] * w[e]));
     }
   }
-  row_reduce<1024>(ss, top, SC == TG_SCALE_ROW, red);
+  row_reduce<false>(ss, top, SC == TG_SCALE_ROW, red);
   const float rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
   float inv = 1.0f;
   if constexpr (SC == TG_SCALE_ROW) {
@@ -254,12 +259,32 @@ __global__ __launch_bounds__(1024) void rmsnorm_long(NormArgs a) {
 // ---- backward --------------------------------------------------------------------------------
 // A workgroup walks rows blockIdx.x, + gridDim.x, … (four at a time with one wave per row) and
 // keeps its share of dw in registers; the shares are written once per workgroup and summed by
-// sum_rows, so the order is fixed.
-template <int DT, int TPR, int NV>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_bwd(NormBwdArgs a) {
-  constexpr int RPB = TPR == 64 ? 4 : 1;
-  __shared__ float red[2][TPR > 64 ? TPR / 64 : 1][2];
-  const int t = (int)threadIdx.x % TPR;
+// sum_rows, so the order is fixed.  The next row sets out before this one is reduced: rows as they
+// are held in memory wait in registers (packed for 16-bit types).
+template <int DT>
+struct Raw8 {
+  ep_u32x4 v[DT == TG_F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const uint8_t* p, int64_t i) {
+    v[0] = load16(p + (DT == TG_F32 ? 4 : 2) * i);
+    if constexpr (DT == TG_F32) v[1] = load16(p + 4 * i + 16);
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    if constexpr (DT == TG_F32) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = __builtin_bit_cast(float, (uint32_t)v[e / 4][e % 4]);
+    } else {
+      ep_unpack8(DT, v[0], f);
+    }
+  }
+};
+template <int DT, int NV, bool WAVE, int MAXT>
+__global__ __launch_bounds__(MAXT) void rmsnorm_bwd(NormBwdArgs a) {
+  constexpr int RPB = WAVE ? 4 : 1;
+  // 1024 threads leave 128 registers: two fp32 rows do not fit
+  constexpr bool AHEAD = !(DT == TG_F32 && MAXT == 1024);
+  __shared__ float red[2][WAVE ? 1 : kMaxWaves][2];
+  const int TPR = WAVE ? 64 : (int)blockDim.x;
+  const int t = WAVE ? (int)threadIdx.x & 63 : (int)threadIdx.x;
   const int cols = (int)a.cols;
   float w[NV][8], dw[NV][8];
 #pragma unroll
@@ -270,42 +295,61 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_bwd(NormBwdArgs
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[j][e] = 0.0f;
   }
-  int par = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + (RPB > 1 ? threadIdx.x >> 6 : 0); row < a.rows;
-       row += (int64_t)gridDim.x * RPB, par ^= 1) {
-    float dy[NV][8], h[NV][8], dh[NV][8];
+  struct Row {
+    Raw8<DT> dy[NV], h[NV], dh[NV];
+    float rstd;
+  };
+  auto load = [&](int64_t row, Row& x) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int col = min((j * TPR + t) * 8, cols - 8);
-      ep_get8(a.dY, DT, row * a.ldy + col, 8, dy[j]);
-      ep_get8(a.H, DT, row * a.ldh + col, 8, h[j]);
+      x.dy[j].load(a.dY, row * a.ldy + col);
+      x.h[j].load(a.H, row * a.ldh + col);
+      if (a.dH) x.dh[j].load(a.dH, row * a.ldd + col);
     }
-    if (a.dH) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) ep_get8(a.dH, DT, row * a.ldd + min((j * TPR + t) * 8, cols - 8), 8, dh[j]);
+    x.rstd = a.rstd[row];
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + (WAVE ? threadIdx.x >> 6 : 0);
+  Row x;
+  if (AHEAD && row < a.rows) load(row, x);
+  for (int par = 0; row < a.rows; row += step, par ^= 1) {
+    Row next;
+    if constexpr (AHEAD) {
+      if (row + step < a.rows) load(row + step, next);
+    } else {
+      load(row, x);
     }
-    const float rstd = a.rstd[row];
+    const float rstd = x.rstd;
     float dot = 0.0f, none = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int dup = (j * TPR + t) * 8 - (cols - 8);
+      float dy[8], h[8];
+      x.dy[j].get(dy);
+      x.h[j].get(h);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float x = dy[j][e] * (h[j][e] * rstd);   // dY·xh
-        dw[j][e] += x;
-        dot += e >= dup ? x * w[j][e] : 0.0f;
+        const float p = dy[e] * (h[e] * rstd);   // dY·xh
+        dw[j][e] += p;
+        dot += e >= dup ? p * w[j][e] : 0.0f;
       }
     }
-    row_reduce<TPR>(dot, none, false, red[par]);
+    row_reduce<WAVE>(dot, none, false, red[par]);
     const float c = dot / (float)cols;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int at = (j * TPR + t) * 8, col = min(at, cols - 8);
-      float dx[8];
+      float dx[8], dy[8], h[8];
+      x.dy[j].get(dy);
+      x.h[j].get(h);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        dx[e] = rstd * (dy[j][e] * w[j][e] - h[j][e] * rstd * c);
-        if (a.dH) dx[e] += dh[j][e];
+      for (int e = 0; e < 8; ++e) dx[e] = rstd * (dy[e] * w[j][e] - h[e] * rstd * c);
+      if (a.dH) {
+        float dh[8];
+        x.dh[j].get(dh);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dx[e] += dh[e];
       }
       // dX may be dH, whose loads no barrier waits for: a moved chunk stores only its own columns
       if (at + 8 <= cols) {
@@ -316,9 +360,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_bwd(NormBwdArgs
           if (e >= at - col) ep_put(a.dX, DT, row * a.ldx + col + e, dx[e]);
       }
     }
+    if constexpr (AHEAD) x = next;
   }
   if (!a.dw) return;
-  if constexpr (TPR == 64) {
+  if constexpr (WAVE) {
     // the four waves' shares, joined in LDS
     __shared__ float part[4][NV * 512];
     const int wv = (int)threadIdx.x >> 6;
@@ -361,7 +406,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_dot(NormBwdArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) dot += dy[e] * (h[e] * rstd) * w[e];
   }
-  row_reduce<1024>(dot, none, false, red);
+  row_reduce<false>(dot, none, false, red);
   if (threadIdx.x == 0) a.dot[row] = dot / (float)a.cols;
 }
 // ... then dX and dw by panels of 2048 columns (blockIdx.y), rows shared over blockIdx.x.
@@ -390,16 +435,19 @@ __global__ __launch_bounds__(256) void rmsnorm_bwd_panel(NormBwdArgs a) {
   if (a.dw) ep_put8((uint8_t*)a.dw, TG_F32, (int64_t)blockIdx.x * a.cols + col, n, dw);
 }
 
+// threads of a workgroup that holds a row, nv chunks each: whole waves
+unsigned row_threads(int64_t cols, int nv) { return (unsigned)((cols + 512 * nv - 1) / (512 * nv) * 64); }
+
 template <int DT, int SC>
 hipError_t go_fwd(const NormArgs& a, hipStream_t s) {
   const dim3 rows((unsigned)a.rows), waves((unsigned)((a.rows + 3) / 4));
+  const dim3 one(row_threads(a.cols, 1)), two(row_threads(a.cols, 2));
   if (!norm_in_registers(a.cols)) hipLaunchKernelGGL((rmsnorm_long<DT, SC>), rows, dim3(1024), 0, s, a);
-  else if (a.cols <= 512) hipLaunchKernelGGL((rmsnorm<DT, 64, 1, SC>), waves, dim3(256), 0, s, a);
-  else if (a.cols <= 1024) hipLaunchKernelGGL((rmsnorm<DT, 64, 2, SC>), waves, dim3(256), 0, s, a);
-  else if (a.cols <= 2048) hipLaunchKernelGGL((rmsnorm<DT, 256, 1, SC>), rows, dim3(256), 0, s, a);
-  else if (a.cols <= 4096) hipLaunchKernelGGL((rmsnorm<DT, 256, 2, SC>), rows, dim3(256), 0, s, a);
-  else if (a.cols <= 8192) hipLaunchKernelGGL((rmsnorm<DT, 256, 4, SC>), rows, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((rmsnorm<DT, 1024, 2, SC>), rows, dim3(1024), 0, s, a);
+  else if (a.cols <= 512) hipLaunchKernelGGL((rmsnorm<DT, 1, SC, true, 256>), waves, dim3(256), 0, s, a);
+  else if (a.cols <= 1024) hipLaunchKernelGGL((rmsnorm<DT, 2, SC, true, 256>), waves, dim3(256), 0, s, a);
+  else if (a.cols <= 4096) hipLaunchKernelGGL((rmsnorm<DT, 1, SC, false, 512>), rows, one, 0, s, a);
+  else if (a.cols <= 8192) hipLaunchKernelGGL((rmsnorm<DT, 2, SC, false, 512>), rows, two, 0, s, a);
+  else hipLaunchKernelGGL((rmsnorm<DT, 2, SC, false, 1024>), rows, two, 0, s, a);
   return hipGetLastError();
 }
 template <int DT>
@@ -415,12 +463,11 @@ hipError_t go_bwd(const NormBwdArgs& a, int64_t groups, hipStream_t s) {
     hipLaunchKernelGGL((rmsnorm_bwd_dot<DT>), dim3((unsigned)a.rows), dim3(1024), 0, s, a);
     hipLaunchKernelGGL((rmsnorm_bwd_panel<DT>), dim3((unsigned)groups, (unsigned)((a.cols + 2047) / 2048)),
                        dim3(256), 0, s, a);
-  } else if (a.cols <= 512) hipLaunchKernelGGL((rmsnorm_bwd<DT, 64, 1>), g, dim3(256), 0, s, a);
-  else if (a.cols <= 1024) hipLaunchKernelGGL((rmsnorm_bwd<DT, 64, 2>), g, dim3(256), 0, s, a);
-  else if (a.cols <= 2048) hipLaunchKernelGGL((rmsnorm_bwd<DT, 256, 1>), g, dim3(256), 0, s, a);
-  else if (a.cols <= 4096) hipLaunchKernelGGL((rmsnorm_bwd<DT, 256, 2>), g, dim3(256), 0, s, a);
-  else if (a.cols <= 8192) hipLaunchKernelGGL((rmsnorm_bwd<DT, 256, 4>), g, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((rmsnorm_bwd<DT, 1024, 2>), g, dim3(1024), 0, s, a);
+  } else if (a.cols <= 512) hipLaunchKernelGGL((rmsnorm_bwd<DT, 1, true, 256>), g, dim3(256), 0, s, a);
+  else if (a.cols <= 1024) hipLaunchKernelGGL((rmsnorm_bwd<DT, 2, true, 256>), g, dim3(256), 0, s, a);
+  else if (a.cols <= 4096) hipLaunchKernelGGL((rmsnorm_bwd<DT, 1, false, 512>), g, dim3(row_threads(a.cols, 1)), 0, s, a);
+  else if (a.cols <= 8192) hipLaunchKernelGGL((rmsnorm_bwd<DT, 2, false, 512>), g, dim3(row_threads(a.cols, 2)), 0, s, a);
+  else hipLaunchKernelGGL((rmsnorm_bwd<DT, 2, false, 1024>), g, dim3(row_threads(a.cols, 2)), 0, s, a);
   return hipGetLastError();
 }
 
