@@ -116,22 +116,34 @@ __device__ __forceinline__ void ep_unpack8(int t, ep_u32x4 a, float (&v)[8]) {
     }
   }
 }
-// n >= 1 valid elements of 8
-__device__ __forceinline__ void ep_get8(const uint8_t* p, int t, int64_t i, int n, float (&v)[8]) {
-  if (n >= 8) {
-    if (t == TG_F32) {
-      const ep_u32x4 a = load16(p + 4 * i), b = load16(p + 4 * i + 16);
+// n >= 1 valid elements of 8, zeros behind them.  At a row's end the last element is loaded again where
+// there is none, so that the eight loads wait together.
+__device__ __forceinline__ ep_u32x4 ep_load8_16(const uint8_t* p, int64_t i, int n) {
+  if (n >= 8) return load16(p + 2 * i);
+  uint16_t u[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = __builtin_bit_cast(float, (uint32_t)a[e]);
-        v[4 + e] = __builtin_bit_cast(float, (uint32_t)b[e]);
-      }
-    } else {
-      ep_unpack8(t, load16(p + 2 * i), v);
+  for (int e = 0; e < 8; ++e) u[e] = ((const uint16_t*)p)[i + min(e, n - 1)];
+  ep_u32x4 w;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    w[e] = (2 * e < n ? (uint32_t)u[2 * e] : 0u) | (2 * e + 1 < n ? (uint32_t)u[2 * e + 1] << 16 : 0u);
+  return w;
+}
+__device__ __forceinline__ void ep_get8(const uint8_t* p, int t, int64_t i, int n, float (&v)[8]) {
+  if (t != TG_F32) {
+    ep_unpack8(t, ep_load8_16(p, i, n), v);
+  } else if (n >= 8) {
+    const ep_u32x4 a = load16(p + 4 * i), b = load16(p + 4 * i + 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = __builtin_bit_cast(float, (uint32_t)a[e]);
+      v[4 + e] = __builtin_bit_cast(float, (uint32_t)b[e]);
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < n ? ep_get(p, t, i + e) : 0.0f;
+    for (int e = 0; e < 8; ++e) v[e] = ((const float*)p)[i + min(e, n - 1)];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < n ? v[e] : 0.0f;
   }
 }
 __device__ __forceinline__ ep_u32x4 ep_pack8(int t, const float (&v)[8]) {
@@ -145,24 +157,31 @@ __device__ __forceinline__ ep_u32x4 ep_pack8(int t, const float (&v)[8]) {
   return o;
 }
 template <bool NT = false>
-__device__ __forceinline__ void ep_put8(uint8_t* p, int t, int64_t i, int n, const float (&v)[8]) {
+__device__ __forceinline__ void ep_store8_16(uint8_t* p, int64_t i, int n, ep_u32x4 w) {
   if (n >= 8) {
-    if (t == TG_F32) {
-      ep_u32x4 a, b;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        a[e] = __builtin_bit_cast(uint32_t, v[e]);
-        b[e] = __builtin_bit_cast(uint32_t, v[4 + e]);
-      }
-      store16<NT>(p + 4 * i, a);
-      store16<NT>(p + 4 * i + 16, b);
-    } else {
-      store16<NT>(p + 2 * i, ep_pack8(t, v));
-    }
+    store16<NT>(p + 2 * i, w);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (e < n) ep_put(p, t, i + e, v[e]);
+      if (e < n) ((uint16_t*)p)[i + e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+  }
+}
+__device__ __forceinline__ void ep_put8(uint8_t* p, int t, int64_t i, int n, const float (&v)[8]) {
+  if (t != TG_F32) {
+    ep_store8_16(p, i, n, ep_pack8(t, v));
+  } else if (n >= 8) {
+    ep_u32x4 a, b;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      a[e] = __builtin_bit_cast(uint32_t, v[e]);
+      b[e] = __builtin_bit_cast(uint32_t, v[4 + e]);
+    }
+    store16(p + 4 * i, a);
+    store16(p + 4 * i + 16, b);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) ((float*)p)[i + e] = v[e];
   }
 }
 
@@ -261,7 +280,6 @@ __device__ __forceinline__ void ep_cols(const EpArgs& g, int col, EpCols& c) {
 }
 // v: the sums P of row `row`, columns col .. col+7 (row < M, col < N); any type, any number of
 // columns left.
-template <bool NT = false>
 __device__ __forceinline__ void ep_finish8(const EpArgs& g, int row, int col, const EpCols& c, float (&v)[8]) {
   const int n = g.N - col;
   const float rs = g.rs ? g.rs[row] : 1.0f;
@@ -269,14 +287,14 @@ __device__ __forceinline__ void ep_finish8(const EpArgs& g, int row, int col, co
   if (g.res) ep_get8(g.res, g.d_t, (int64_t)row * g.ldr + col, n, r);
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = v[e] * rs * c.cs[e] + c.bias[e];
-  if (g.Z) ep_put8<NT>(g.Z, g.d_t, (int64_t)row * g.ldz + col, n, v);
+  if (g.Z) ep_put8(g.Z, g.d_t, (int64_t)row * g.ldz + col, n, v);
   ep_with_act(g.act, [&](auto act) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = ep_act<decltype(act)::value>(v[e]);
   });
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] += r[e];
-  ep_put8<NT>(g.D, g.d_t, (int64_t)row * g.ldd + col, n, v);
+  ep_put8(g.D, g.d_t, (int64_t)row * g.ldd + col, n, v);
 }
 // one element: what its epilogue reads, and the finish
 struct EpOne {
@@ -294,24 +312,23 @@ __device__ __forceinline__ void ep_finish1(const EpArgs& g, int row, int col, co
   ep_with_act(g.act, [&](auto act) { p = ep_act<decltype(act)::value>(p); });
   ep_put(g.D, g.d_t, (int64_t)row * g.ldd + col, p + x.res);
 }
-// 8 whole columns of 16-bit results, in two halves: what a row needs besides its sums is loaded for
-// several rows ahead of their stores (the residual may be D, so the compiler would not move its load
-// above a store), and no code for ragged columns is in the way.
-__device__ __forceinline__ bool ep_16(const EpArgs& g) { return g.d_t != TG_F32; }
+// 8 columns of 16-bit results, in two halves: what a row needs besides its sums is loaded for several
+// rows ahead of their stores (the residual may be D, so the compiler would not move its load above a
+// store).
 struct EpRow {
   float rs;
   ep_u32x4 res;
 };
 __device__ __forceinline__ void ep_row(const EpArgs& g, int row, int col, EpRow& x) {
   x.rs = g.rs ? g.rs[row] : 1.0f;
-  if (g.res) x.res = load16(g.res + 2 * ((int64_t)row * g.ldr + col));
+  if (g.res) x.res = ep_load8_16(g.res, (int64_t)row * g.ldr + col, g.N - col);
 }
 template <int ACT>
 __device__ __forceinline__ void ep_finish8_16(const EpArgs& g, int row, int col, const EpCols& c, const EpRow& x,
                                                 float (&v)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = v[e] * x.rs * c.cs[e] + c.bias[e];
-  if (g.Z) store16<true>(g.Z + 2 * ((int64_t)row * g.ldz + col), ep_pack8(g.d_t, v));
+  if (g.Z) ep_store8_16<true>(g.Z, (int64_t)row * g.ldz + col, g.N - col, ep_pack8(g.d_t, v));
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = ep_act<ACT>(v[e]);
   if (g.res) {
@@ -320,7 +337,7 @@ __device__ __forceinline__ void ep_finish8_16(const EpArgs& g, int row, int col,
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += r[e];
   }
-  store16<true>(g.D + 2 * ((int64_t)row * g.ldd + col), ep_pack8(g.d_t, v));
+  ep_store8_16<true>(g.D, (int64_t)row * g.ldd + col, g.N - col, ep_pack8(g.d_t, v));
 }
 
 }  // namespace

@@ -40,6 +40,16 @@ __device__ __forceinline__ f32x16 mfma32t(F b, F a, f32x16 c) {
         0);
 }
 
+// 128 bits shifted down by `bits` (0 .. , per lane), zeros from above
+__device__ __forceinline__ u32x4 shift_down(u32x4 v, uint32_t bits) {
+  if (bits & 64) v = u32x4{v[2], v[3], 0, 0};
+  if (bits & 32) v = u32x4{v[1], v[2], v[3], 0};
+  const uint32_t r = bits & 31;
+  v = u32x4{__builtin_amdgcn_alignbit(v[1], v[0], r), __builtin_amdgcn_alignbit(v[2], v[1], r),
+            __builtin_amdgcn_alignbit(v[3], v[2], r), v[3] >> r};
+  return bits < 128 ? v : u32x4{0, 0, 0, 0};
+}
+
 // Fills one operand's LDS stage through registers.  Slot mapping as Operand::load: instruction
 // i of wave w fills the 1 KiB block PER·w + i, lane l its bytes 16l .. 16l+15.
 template <bool MN, int PER, int DT, int BS>
@@ -48,62 +58,64 @@ struct StagedFetch {
   static constexpr int E = EL::kBytes, VE = 16 / E;   // elements per chunk
   u32x4 r[PER];
 
-  // A stage that is not the operand's last: every chunk is 16 bytes of memory that the operand owns.
-  // K-major rows past the end repeat the last one and M/N-major chunks may run into the next k-row;
-  // both only feed outputs that are not stored.
-  // base: the block's first element at k = 0 of the block's part of K; rows: valid rows (K-major)
-  // or columns (M/N-major) of the block.
-  __device__ __forceinline__ void get_whole(const uint8_t* base, int64_t ld, int rows, int stage, int wave, int lane) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const uint32_t blk = (uint32_t)(PER * wave + i);
-      int64_t off;   // elements
-      if constexpr (MN) {
-        constexpr uint32_t ROWB = BS * E, CH = ROWB / 16, RPB = 1024 / ROWB;
-        const uint32_t k = RPB * blk + (uint32_t)lane / CH;
-        const uint32_t c = ((uint32_t)lane % CH) ^ sm_row<SMV, ROWB>(k);
-        off = (int64_t)(stage * EL::kBK + (int)k) * ld + min((int)c, (rows - 1) / VE) * VE;
-      } else {
-        const uint32_t row = 8u * blk + ((uint32_t)lane >> 3);
-        const uint32_t c = ((uint32_t)lane & 7u) ^ sk<SKV>(row);
-        off = (int64_t)min((int)row, rows - 1) * ld + stage * EL::kBK + (int)(c * VE);
-      }
-      r[i] = load16(base + off * E);
+  // instruction i's chunk of a stage: its row (K-major) or k (M/N-major) and its first k or column
+  __device__ __forceinline__ static void where(int i, int stage, int wave, int lane, int& line, int& first) {
+    const uint32_t blk = (uint32_t)(PER * wave + i);
+    if constexpr (MN) {
+      constexpr uint32_t ROWB = BS * E, CH = ROWB / 16, RPB = 1024 / ROWB;
+      const uint32_t k = RPB * blk + (uint32_t)lane / CH;
+      line = stage * EL::kBK + (int)k;
+      first = (int)(((uint32_t)lane % CH) ^ sm_row<SMV, ROWB>(k)) * VE;
+    } else {
+      const uint32_t row = 8u * blk + ((uint32_t)lane >> 3);
+      line = (int)row;
+      first = stage * EL::kBK + (int)(((uint32_t)lane & 7u) ^ sk<SKV>(row)) * VE;
     }
   }
-  // any stage; kl: valid k
+  // base: the block's first element at k = 0 of the block's part of K; rows: rows (K-major) or columns
+  // (M/N-major) from there to the operand's end; kl: k of this part.
+  // Every load is 16 whole bytes inside the operand, whatever the edge: a chunk that would pass the end
+  // of its line is moved back to the line's last 16 bytes (the line holds as many), a line past the end
+  // repeats the last one.  So the loads of all stages are alike, no branch hides how many are in
+  // flight, and fix() puts the moved chunks right once they are here.
   __device__ __forceinline__ void get(const uint8_t* base, int64_t ld, int rows, int kl, int stage, int wave,
                                       int lane) {
+    const int lines = MN ? kl : rows, width = MN ? rows : kl;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const uint32_t blk = (uint32_t)(PER * wave + i);
-      int64_t off;   // elements
-      int n;         // valid elements of the chunk
-      if constexpr (MN) {
-        constexpr uint32_t ROWB = BS * E, CH = ROWB / 16, RPB = 1024 / ROWB;
-        const uint32_t k = RPB * blk + (uint32_t)lane / CH;
-        const uint32_t c = ((uint32_t)lane % CH) ^ sm_row<SMV, ROWB>(k);
-        const int kk = stage * EL::kBK + (int)k;
-        off = (int64_t)kk * ld + c * VE;
-        n = kk < kl ? rows - (int)(c * VE) : 0;
-      } else {
-        const uint32_t row = 8u * blk + ((uint32_t)lane >> 3);
-        const uint32_t c = ((uint32_t)lane & 7u) ^ sk<SKV>(row);
-        const int k = stage * EL::kBK + (int)(c * VE);
-        off = (int64_t)row * ld + k;
-        n = (int)row < rows ? kl - k : 0;
-      }
-      const uint8_t* p = base + off * E;
-      u32x4 v = {0, 0, 0, 0};
-      if (n >= VE) {
-        v = load16(p);
-      } else if (n > 0) {
+      int line, first;
+      where(i, stage, wave, lane, line, first);
+      r[i] = load16(base + ((int64_t)min(line, lines - 1) * ld + min(first, width - VE)) * E);
+    }
+  }
+  // Moved chunks down to their place, zeros for k past the end (a row or column past the end feeds
+  // only outputs that are not stored).
+  __device__ __forceinline__ void fix(int rows, int kl, int stage, int wave, int lane) {
+    const int width = MN ? rows : kl;
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          uint32_t x = 0;
-          if (e < n) x = E == 2 ? (uint32_t)((const uint16_t*)p)[e] : (uint32_t)p[e];
-          v[e * E / 4] |= x << (8 * E * (e % (4 / E)));
-        }
+    for (int i = 0; i < PER; ++i) {
+      int line, first;
+      where(i, stage, wave, lane, line, first);
+      const int back = MN && line >= kl ? VE : max(0, first - (width - VE));
+      r[i] = shift_down(r[i], 8u * E * (uint32_t)min(back, VE));
+    }
+  }
+  // Element by element: lines shorter than 16 bytes.
+  __device__ __forceinline__ void get_each(const uint8_t* base, int64_t ld, int rows, int kl, int stage, int wave,
+                                           int lane) {
+    const int lines = MN ? kl : rows, width = MN ? rows : kl;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      int line, first;
+      where(i, stage, wave, lane, line, first);
+      const uint8_t* p = base + ((int64_t)line * ld + first) * E;
+      const int n = line < lines ? width - first : 0;
+      u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        uint32_t x = 0;
+        if (e < n) x = E == 2 ? (uint32_t)((const uint16_t*)p)[e] : (uint32_t)p[e];
+        v[e * E / 4] |= x << (8 * E * (e % (4 / E)));
       }
       r[i] = v;
     }
@@ -166,15 +178,15 @@ __device__ __forceinline__ void ep_store(const EpArgs& g, const EpTile& t, f32x1
     v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
   };
   constexpr int NP = 32 / RPP;
-  const bool in = col < g.N, whole = ep_16(g) && col + 8 <= g.N;   // whole: the fast form
+  const bool in = col < g.N, half = g.d_t != TG_F32;   // half: 16-bit results
   // residual and row scales: one band ahead of the one being stored
   EpRow ahead[NP];
   auto look = [&](int i) {
-    if (g.splits > 1) return;
+    if (g.splits > 1 || !half) return;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
       const int row = t.m0 + wm + 32 * i + brow + p * RPP;
-      if (whole && row < g.M) ep_row(g, row, col, ahead[p]);
+      if (in && row < g.M) ep_row(g, row, col, ahead[p]);
     }
   };
   look(0);
@@ -207,23 +219,22 @@ __device__ __forceinline__ void ep_store(const EpArgs& g, const EpTile& t, f32x1
         if (in && row < g.M)
           ep_put8((uint8_t*)g.part, TG_F32, ((int64_t)t.split * g.M + row) * g.part_ld + col, 8, v);
       }
-    } else {
-      if (whole)
-        ep_with_act(g.act, [&](auto act) {
+    } else if (half) {
+      ep_with_act(g.act, [&](auto act) {
 #pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            from_band(p, v);
-            const int row = row0 + p * RPP;
-            if (row < g.M) ep_finish8_16<decltype(act)::value>(g, row, col, cols, rows[p], v);
-          }
-        });
-      else if (in)
-#pragma unroll 1
         for (int p = 0; p < NP; ++p) {
           from_band(p, v);
           const int row = row0 + p * RPP;
-          if (row < g.M) ep_finish8(g, row, col, cols, v);   // fp32 or a row's end: the L2 joins the pieces
+          if (in && row < g.M) ep_finish8_16<decltype(act)::value>(g, row, col, cols, rows[p], v);
         }
+      });
+    } else {
+#pragma unroll 1
+      for (int p = 0; p < NP; ++p) {
+        from_band(p, v);
+        const int row = row0 + p * RPP;
+        if (in && row < g.M) ep_finish8(g, row, col, cols, v);   // the L2 joins a row's 16-byte pieces
+      }
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -263,7 +274,7 @@ struct DirectLoads {
 // Direct loads, two stages: 256-wide blocks (one workgroup per CU), and 128-wide ones where two
 // workgroups share a CU.
 template <bool A_MN, bool B_MN, int DT, int BS>
-__global__ __launch_bounds__(ep_threads(BS)) void gemm_ep_direct(EpArgs g) {
+__global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_direct(EpArgs g) {
   constexpr int WGM = 2, WGN = ep_threads(BS) / 128;
   // four named stages: their addresses stay compile-time immediates
   __shared__ __attribute__((aligned(1024))) uint8_t sa0[BS * kRowBytes];
@@ -499,9 +510,10 @@ __global__ __launch_bounds__(ep_threads(BS)) void gemm_ep_ring(EpArgs g) {
   ep_store<BS, WN, TM, TN>(g, t, acc, wave, lane, wm, wn, s0, s1, s2, s3);
 }
 
-// Operands through registers, two stages ahead of the one computed.
+// Operands through registers, D stages ahead of the one computed: four on 64-wide blocks (a CU holds one
+// or two and waits for memory), two on 128-wide ones (four would leave one workgroup a CU).
 template <bool A_MN, bool B_MN, int DT, int BS>
-__global__ __launch_bounds__(ep_threads(BS)) void gemm_ep_staged(EpArgs g) {
+__global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_staged(EpArgs g) {
   constexpr int WGM = 2, WGN = ep_threads(BS) / 128;
   __shared__ __attribute__((aligned(1024))) uint8_t sa0[BS * kRowBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t sb0[BS * kRowBytes];
@@ -542,56 +554,88 @@ __global__ __launch_bounds__(ep_threads(BS)) void gemm_ep_staged(EpArgs g) {
   const uint8_t* pb = g.B + (B_MN ? (int64_t)t.k0 * g.ldb + t.n0 : (int64_t)t.n0 * g.ldb + t.k0) * E;
   const int ra = g.M - t.m0, rb = g.N - t.n0;   // rows / columns from here to the end
   const int KT = (t.kl + EL::kBK - 1) / EL::kBK;   // >= 1
-  StagedFetch<A_MN, PER, DT, BS> fa0, fa1;
-  StagedFetch<B_MN, PER, DT, BS> fb0, fb1;
-  // (a row pitch below 16 bytes could leave the operand even before its last stage)
-  const bool pitch = (!A_MN || g.lda >= 16 / E) && (!B_MN || g.ldb >= 16 / E);
-  using T_ = std::true_type;
-  using F_ = std::false_type;
-  // inner: stage s is known to be a whole one
-  auto get = [&](auto& fa, auto& fb, int s, auto inner) {
-    if (decltype(inner)::value || (pitch && s + 1 < KT)) {
-      fa.get_whole(pa, g.lda, ra, s, wave, lane);
-      fb.get_whole(pb, g.ldb, rb, s, wave, lane);
-    } else if (s < KT) {
-      fa.get(pa, g.lda, ra, t.kl, s, wave, lane);
-      fb.get(pb, g.ldb, rb, t.kl, s, wave, lane);
-    }
-    __builtin_amdgcn_sched_barrier(0);   // on their way before the stage's products
-  };
-  get(fa0, fb0, 0, F_{});
-  get(fa1, fb1, 1, F_{});
-  fa0.put(sa0, wave, lane);
-  fb0.put(sb0, wave, lane);
-  __syncthreads();
-  // stage kt from (ca, cb); stage kt + 1, loaded a stage ago, goes to (na, nb) after it, and its
-  // registers' successor kt + 2 sets out before it
-  auto stage = [&](const uint8_t* ca, const uint8_t* cb, uint8_t* na, uint8_t* nb, int kt, auto& fa, auto& fb,
-                   const auto& ga, const auto& gb, auto inner) {
-    get(fa, fb, kt + 2, inner);
+  constexpr int D = 2;
+  StagedFetch<A_MN, PER, DT, BS> fa[D];
+  StagedFetch<B_MN, PER, DT, BS> fb[D];
+  auto compute = [&](const uint8_t* xa, const uint8_t* xb) {
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      oa.frags(ca, s, a);
-      ob.frags(cb, s, b);
+      oa.frags(xa, s, a);
+      ob.frags(xb, s, b);
       mfmas(a, b);
     }
-    if (decltype(inner)::value || kt + 1 < KT) {
-      ga.put(na, wave, lane);
-      gb.put(nb, wave, lane);
+  };
+  constexpr int VE = 16 / E;
+  if (g.K < VE || (A_MN && g.M < VE) || (B_MN && g.N < VE)) {
+    // one stage after the other
+    for (int kt = 0; kt < KT; ++kt) {
+      fa[0].get_each(pa, g.lda, ra, t.kl, kt, wave, lane);
+      fb[0].get_each(pb, g.ldb, rb, t.kl, kt, wave, lane);
+      __syncthreads();
+      fa[0].put(sa0, wave, lane);
+      fb[0].put(sb0, wave, lane);
+      __syncthreads();
+      compute(sa0, sb0);
     }
     __syncthreads();
-  };
-  // the loop that counts has whole stages only: element-by-element loads beside it would make the
-  // compiler wait for every load in flight
-  int kt = 0;
-  if (pitch)
-    for (; kt + 4 < KT; kt += 2) {
-      stage(sa0, sb0, sa1, sb1, kt, fa0, fb0, fa1, fb1, T_{});
-      stage(sa1, sb1, sa0, sb0, kt + 1, fa1, fb1, fa0, fb0, T_{});
+  } else {
+    // stages past the last load what is not used
+    auto get = [&](auto q, int s) {
+      constexpr int set = decltype(q)::value;
+      fa[set].get(pa, g.lda, ra, t.kl, s, wave, lane);
+      fb[set].get(pb, g.ldb, rb, t.kl, s, wave, lane);
+      __builtin_amdgcn_sched_barrier(0);   // on their way before the stage's products
+    };
+    const bool edge_a = A_MN && ra < BS, edge_b = B_MN && rb < BS;
+    auto put = [&](auto q, int s, uint8_t* xa, uint8_t* xb) {
+      constexpr int set = decltype(q)::value;
+      if (edge_a || s + 1 >= KT) fa[set].fix(ra, t.kl, s, wave, lane);
+      if (edge_b || s + 1 >= KT) fb[set].fix(rb, t.kl, s, wave, lane);
+      fa[set].put(xa, wave, lane);
+      fb[set].put(xb, wave, lane);
+    };
+    constexpr std::integral_constant<int, 0> S0{};
+    constexpr std::integral_constant<int, 1> S1{};
+    constexpr std::integral_constant<int, D == 4 ? 2 : 0> S2{};
+    constexpr std::integral_constant<int, D == 4 ? 3 : 1> S3{};
+    get(S0, 0);
+    get(S1, 1);
+    if constexpr (D == 4) {
+      get(S2, 2);
+      get(S3, 3);
     }
-  for (; kt < KT; kt += 2) {
-    stage(sa0, sb0, sa1, sb1, kt, fa0, fb0, fa1, fb1, F_{});
-    if (kt + 1 < KT) stage(sa1, sb1, sa0, sb0, kt + 1, fa1, fb1, fa0, fb0, F_{});
+    put(S0, 0, sa0, sb0);
+    __syncthreads();
+    // stage kt from (ca, cb); its registers, set `q`, take stage kt + D, and stage kt + 1, loaded
+    // D - 1 stages ago, goes to (na, nb) after it
+    auto stage = [&](const uint8_t* ca, const uint8_t* cb, uint8_t* na, uint8_t* nb, int kt, auto q, auto next) {
+      get(q, kt + D);
+      compute(ca, cb);
+      put(next, kt + 1, na, nb);
+      __syncthreads();
+    };
+    int kt = 0;
+    if constexpr (D == 4) {
+      for (; kt + 4 <= KT; kt += 4) {
+        stage(sa0, sb0, sa1, sb1, kt, S0, S1);
+        stage(sa1, sb1, sa0, sb0, kt + 1, S1, S2);
+        stage(sa0, sb0, sa1, sb1, kt + 2, S2, S3);
+        stage(sa1, sb1, sa0, sb0, kt + 3, S3, S0);
+      }
+      if (kt < KT) {
+        stage(sa0, sb0, sa1, sb1, kt, S0, S1);
+        if (kt + 1 < KT) {
+          stage(sa1, sb1, sa0, sb0, kt + 1, S1, S2);
+          if (kt + 2 < KT) stage(sa0, sb0, sa1, sb1, kt + 2, S2, S3);
+        }
+      }
+    } else {
+      for (; kt + 2 <= KT; kt += 2) {
+        stage(sa0, sb0, sa1, sb1, kt, S0, S1);
+        stage(sa1, sb1, sa0, sb0, kt + 1, S1, S0);
+      }
+      if (kt < KT) stage(sa0, sb0, sa1, sb1, kt, S0, S1);
+    }
   }
   ep_store<BS, WN, TM, TN>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
 }
