@@ -126,8 +126,9 @@ struct StagedFetch {
   }
 };
 
-// Waves of a block: 2 x 4, on 64 rows and columns 2 x 2.  (4 waves of 64 x 64 on 128-wide blocks read a
-// third less of LDS, but one wave per SIMD waits for all of it: 512 x 2048 x 2048 17.2 -> 19.1 us.)
+// Waves of a block: 2 x 4, on 64 rows and columns 2 x 2.  (4 waves read a third less of LDS, but one wave
+// per SIMD waits for all of it and for its epilogue: 128-wide blocks, 512 x 2048 x 2048, 17.2 -> 19.1 us;
+// 256-wide ones, 8192^3 bf16, 781 -> 818.)
 constexpr int ep_threads(int bs) { return bs == 64 ? 256 : 512; }
 
 // What a workgroup computes: its block's first row and column, its part of K.
@@ -189,14 +190,17 @@ __device__ __forceinline__ void ep_store(const EpArgs& g, const EpTile& t, f32x1
       if (in && row < g.M) ep_row(g, row, col, ahead[p]);
     }
   };
-  look(0);
+  // (128- and 64-wide blocks share a CU with another and have no registers for it)
+  constexpr bool kAhead = BS == 256;
+  if (kAhead) look(0);
 #pragma unroll 1
   for (int i = 0; i < TM; ++i) {
     const int row0 = t.m0 + wm + 32 * i + brow;
+    if (!kAhead) look(i);
     EpRow rows[NP];
 #pragma unroll
     for (int p = 0; p < NP; ++p) rows[p] = ahead[p];
-    if (i + 1 < TM) look(i + 1);
+    if (kAhead && i + 1 < TM) look(i + 1);
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll

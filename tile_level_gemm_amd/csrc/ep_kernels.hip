@@ -40,7 +40,7 @@ __global__ __launch_bounds__(256) void ep_join(EpArgs g, int64_t chunks) {
 
 // dZ = dY·act'(Z), and the column sums of dZ (before its rounding) over the workgroup's rows.
 // 64 columns x rows_per rows per workgroup: 8 lanes of 8 columns (a 128-byte line of each row), 32
-// rows at a time, four such in flight.  One pass over dY and Z, bound by memory.
+// rows at a time, eight such in flight.  One pass over dY and Z, bound by memory.
 __global__ __launch_bounds__(256) void act_grad(ActGradArgs a) {
   __shared__ float red[32][64 + 1];
   const int lane = (int)threadIdx.x & 7, rl = (int)threadIdx.x >> 3;
@@ -59,16 +59,16 @@ __global__ __launch_bounds__(256) void act_grad(ActGradArgs a) {
     };
     if (n >= 8) {
       // dZ may be dY or Z: each element is read by the thread that writes it, before it does
-      for (int r = r0 + rl; r < r1; r += 128) {
-        ep_u32x4 y[4], z[4];
+      for (int r = r0 + rl; r < r1; r += 256) {
+        ep_u32x4 y[8], z[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 8; ++k)
           if (r + 32 * k < r1) {
             y[k] = load16(a.dY + 2 * ((int64_t)(r + 32 * k) * a.ldy + col));
             if constexpr (ACT != TG_ACT_NONE) z[k] = load16(a.Z + 2 * ((int64_t)(r + 32 * k) * a.ldz + col));
           }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 8; ++k)
           if (r + 32 * k < r1) {
             float dy[8], zz[8] = {};
             ep_unpack8(a.t, y[k], dy);
