@@ -407,10 +407,13 @@ constexpr int wait_vm(int n) { return (n & 15) | 7 << 4 | (n >> 4) << 14; }
 // Direct loads, a ring of four stages (128 KiB on 128-wide blocks): the loads of a stage have three
 // stages' time to arrive where two leave one.  For problems of few blocks, whose stages come from far
 // away and whose CUs hold one workgroup anyway.
-// Stage kt of slot kt % 4: before its last K step the wave waits until its own loads of stage kt + 1
-// have landed (those of kt + 2 and kt + 3 stay in flight) and meets the others at the barrier, so
-// stage kt + 1 is whole and slot kt % 4 free; the last step's products cover the first fragment reads
-// of kt + 1 and the issue of stage kt + 4.  Stages past K read as zeros and touch no memory.
+// Stage kt of slot kt % 4, all of whose fragments are in registers: the wave waits until its own loads
+// of stage kt + 1 have landed (those of kt + 2 and kt + 3 stay in flight) and meets the others at the
+// barrier, so stage kt + 1 is whole and slot kt % 4 free; then the products of stage kt cover the
+// reads of all fragments of kt + 1 and the issue of stage kt + 4.  A step at a time, as the two-stage
+// kernel reads, every step of a 64-wide block waited for LDS: one wave per SIMD has 32 cycles of
+// products a step against about 130 of latency.
+// Stages past K read as zeros and touch no memory.
 template <bool A_MN, bool B_MN, int DT, int BS>
 __global__ __launch_bounds__(ep_threads(BS)) void gemm_ep_ring(EpArgs g) {
   constexpr int WGM = 2, WGN = ep_threads(BS) / 128;
@@ -449,7 +452,6 @@ __global__ __launch_bounds__(ep_threads(BS)) void gemm_ep_ring(EpArgs g) {
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = mfma32t<DT>(b[j], a[i], acc[i][j]);
   };
-  Frag a[TM], b[TN];
   constexpr int kReads = OA::kReads + OB::kReads, kMfma = TM * TN, kDma = 2 * PER;
   const DirectLoads<A_MN, B_MN, DT, BS, OA, OB> load_ab(oa, ob, g, t, wave);
   const int KT = (t.kl + EL::kBK - 1) / EL::kBK;   // >= 1
@@ -467,46 +469,40 @@ __global__ __launch_bounds__(ep_threads(BS)) void gemm_ep_ring(EpArgs g) {
   load_ab(2, s2, s2 + kB);
   load_ab(3, s3, s3 + kB);
   meet(std::integral_constant<int, 3 * kDma>{});
-  Frag an[TM], bn[TN];
-  oa.frags(s0, 0, a);
-  ob.frags(s0 + kB, 0, b);
-  auto keep = [&]() {
+  Frag fa[2][NS][TM], fb[2][NS][TN];   // fragments of two stages, the even and the odd one
+  auto read = [&](const uint8_t* st, Frag (&x)[NS][TM], Frag (&y)[NS][TN]) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) a[i] = an[i];
-#pragma unroll
-    for (int j = 0; j < TN; ++j) b[j] = bn[j];
-  };
-  auto stage = [&](uint8_t* cur, const uint8_t* next, int kt) {
-#pragma unroll
-    for (int s = 0; s < NS - 1; ++s) {
-      oa.frags(cur, s + 1, an);
-      ob.frags(cur + kB, s + 1, bn);
-      mfmas(a, b);
-      interleave<kMfma, kReads, 0>();
-      keep();
+    for (int s = 0; s < NS; ++s) {
+      oa.frags(st, s, x[s]);
+      ob.frags(st + kB, s, y[s]);
     }
-    meet(std::integral_constant<int, 2 * kDma>{});
-    oa.frags(next, 0, an);
-    ob.frags(next + kB, 0, bn);
-    load_ab(kt + 4, cur, cur + kB);
-    mfmas(a, b);
-    interleave<kMfma, kReads, kDma>();
-    keep();
   };
+  read(s0, fa[0], fb[0]);
+  auto stage = [&](uint8_t* cur, const uint8_t* next, int kt, auto odd) {
+    constexpr int p = decltype(odd)::value;
+    meet(std::integral_constant<int, 2 * kDma>{});
+    read(next, fa[1 - p], fb[1 - p]);
+    load_ab(kt + 4, cur, cur + kB);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) mfmas(fa[p][s], fb[p][s]);
+    interleave<kMfma * NS, kReads * NS, kDma>();
+  };
+  constexpr std::integral_constant<int, 0> even{};
+  constexpr std::integral_constant<int, 1> odd{};
   // No way out of the middle of a round: the compiler would count the loads of every exit as possibly
   // in flight at the loop's head, and wait for all of them there.
   int kt = 0;
   for (; kt + 4 <= KT; kt += 4) {
-    stage(s0, s1, kt);
-    stage(s1, s2, kt + 1);
-    stage(s2, s3, kt + 2);
-    stage(s3, s0, kt + 3);
+    stage(s0, s1, kt, even);
+    stage(s1, s2, kt + 1, odd);
+    stage(s2, s3, kt + 2, even);
+    stage(s3, s0, kt + 3, odd);
   }
   if (kt < KT) {
-    stage(s0, s1, kt);
+    stage(s0, s1, kt, even);
     if (kt + 1 < KT) {
-      stage(s1, s2, kt + 1);
-      if (kt + 2 < KT) stage(s2, s3, kt + 2);
+      stage(s1, s2, kt + 1, odd);
+      if (kt + 2 < KT) stage(s2, s3, kt + 2, even);
     }
   }
   // the zero stages still on their way must land before the epilogue takes the buffers
