@@ -34,7 +34,7 @@ def test_few_rows_against_transposed_weights_part_a_long_sum(N, K):
 
 @pytest.mark.parametrize("M,N,K,bs", [
     (33, 64, 64, 64), (200, 264, 520, 64), (1024, 1024, 1024, 64), (512, 2048, 2048, 64),   # fewer than 192 128-wide blocks
-    (2048, 2048, 2048, 128), (2048, 1536, 64, 128), (2048, 4096, 4096, 128),
+    (2048, 2048, 2048, 128), (2048, 1536, 64, 128), (2048, 4096, 4096, 128), (256, 4096, 8192, 128), (256, 4096, 4096, 64),
     (4096, 4096, 64, 256), (8192, 8192, 8192, 256), (4096, 2048, 8192, 256)])
 def test_block_sizes(M, N, K, bs):
     p = plan(M, N, K)
@@ -42,11 +42,12 @@ def test_block_sizes(M, N, K, bs):
     assert p.grid == -(-M // bs) * -(-N // bs) * p.splits
     assert p.splits * p.k_per_split >= K > (p.splits - 1) * p.k_per_split
     q = plan(M, N, K, lda=K + 1)   # rows of A at any alignment: through registers, 128-wide at most
-    assert q.kernel == tg.TG_EP_STAGED and q.block_m == min(bs, 128)
+    assert q.kernel == tg.TG_EP_STAGED and q.block_m == (128 if -(-M // 128) * -(-N // 128) >= 192 else 64)
 
 
 @pytest.mark.parametrize("M,N,K,parts", [(64, 4096, 4096, 4), (128, 4096, 4096, 2), (512, 520, 4160, 3), (64, 64, 1000, 1),
-                                         (64, 64, 2048, 2), (4096, 2048, 8192, 2), (4096, 2048, 4096, 1), (2048, 2048, 8192, 1)])
+                                         (64, 64, 2048, 2), (4096, 2048, 8192, 2), (4096, 2048, 4096, 1), (2048, 2048, 8192, 1),
+                                         (256, 4096, 8192, 4), (256, 4096, 4096, 1), (1024, 2048, 4096, 2)])
 def test_parts_of_the_sum(M, N, K, parts):
     p = plan(M, N, K)
     assert p.splits == parts

@@ -97,6 +97,7 @@ def some_rows(M):
 @pytest.mark.parametrize("M,N,K,ta,tb", [
     (2048, 1544, 200, 0, 1), (1536, 2048, 72, 0, 0), (2000, 2056, 320, 1, 0), (2048, 1600, 600, 1, 1),   # 128-wide, ring
     (2056, 3000, 136, 0, 1), (3000, 2304, 192, 1, 0),                                                    # 128-wide, two a CU
+    (200, 4000, 9000, 0, 1), (264, 4104, 8200, 1, 0),                                                    # 128-wide, ring, parts
     (2001, 1999, 201, 0, 1), (2001, 1999, 201, 0, 0), (1999, 2001, 135, 1, 0),                           # 128-wide, staged
     (4096, 2048, 6208, 0, 0), (3848, 2048, 6144, 1, 1)])                                                 # 256-wide, two parts
 def test_large_blocks(M, N, K, ta, tb):
@@ -111,7 +112,7 @@ def test_large_blocks(M, N, K, ta, tb):
     assert bool(torch.isfinite(D).all())
 
 
-@pytest.mark.parametrize("M,N,K", [(2048, 2048, 384), (2048, 2050, 201), (2304, 3000, 256), (300, 520, 4224), (4096, 4352, 384)])
+@pytest.mark.parametrize("M,N,K", [(2048, 2048, 384), (2048, 2050, 201), (2304, 3000, 256), (300, 520, 4224), (4096, 4352, 384), (300, 4000, 16384)])
 def test_large_blocks_fp8(M, N, K):
     say(f"large blocks fp8 {M}x{N}x{K}")
     a, b = rand(M, (M, K), "e4m3", 4.0), rand(N, (N, K), "e5m2", 4.0)

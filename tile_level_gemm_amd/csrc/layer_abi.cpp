@@ -133,8 +133,15 @@ EpChoice choose_ep(int64_t M, int64_t N, int64_t K, int transB, int eb, bool dir
     // 28.3), else two workgroups of two stages on a CU (2048 x 3000 x 1000: 26.9 us, ring 30.8)
     c.bs = 128;
     c.ring = direct && blocks(128) <= 256;
+  } else if (direct && blocks(128) <= 128 && blocks(64) * steps >= 256 * 128) {
+    // 128-wide in parts where 64-wide ones would be bound by the L2, which both feed from at about
+    // 13 TB/s and 64-wide ones ask twice as much of (256 x 4096 x 8192: 36 us, 64-wide 42;
+    // 256 x 4096 x 4096: 22, 64-wide 18)
+    c.bs = 128;
+    c.ring = true;
+    s = std::min(256 / blocks(128), steps / 16);
   } else {
-    // 64-wide (1024 x 1024 x 1024: 7.7 us, 128-wide 11.4), and parts of K of at least 16 stages while
+    // 64-wide (1024 x 1024 x 1024: 7.1 us, 128-wide 11.4), and parts of K of at least 16 stages while
     // they leave CUs without work (64 x 4096 x 4096: one part 16.4 us, four 12.6, eight 13.8)
     c.bs = 64;
     c.ring = direct;
