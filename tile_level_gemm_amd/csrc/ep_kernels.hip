@@ -39,63 +39,57 @@ __global__ __launch_bounds__(256) void ep_join(EpArgs g, int64_t chunks) {
 }
 
 // dZ = dY·act'(Z), and the column sums of dZ (before its rounding) over the workgroup's rows.
-// 64 columns x rows_per rows per workgroup: 8 lanes of 8 columns (a 128-byte line of each row), 32
-// rows at a time, eight such in flight.  One pass over dY and Z, bound by memory.
-__global__ __launch_bounds__(256) void act_grad(ActGradArgs a) {
-  __shared__ float red[32][64 + 1];
+// 64 columns x rows_per rows per workgroup: 8 lanes of 8 columns (a 128-byte line of each row), RL
+// rows at a time, K such in flight.  One pass over dY and Z, bound by memory: 256 threads with four
+// rows each in flight (4096 x 8192: 43 us; 1024 threads with two 51).  A problem that one workgroup per
+// 64 columns holds waits for its instructions as well as its rows: there 1024 threads with two
+// (200 x 520: 5.4 us; 256 with eight rows 7.3).
+template <int RL, int K>
+__global__ __launch_bounds__(8 * RL) void act_grad(ActGradArgs a) {
+  __shared__ float red[RL][64 + 1];
   const int lane = (int)threadIdx.x & 7, rl = (int)threadIdx.x >> 3;
   const int col = (int)blockIdx.x * 64 + lane * 8, n = a.N - col;
   const int r0 = (int)blockIdx.y * a.rows_per, r1 = min(a.M, r0 + a.rows_per);
   float sum[8] = {};
+  // dZ may be dY or Z: each element is read by the thread that writes it, before it does
   ep_with_act(a.act, [&](auto act) {
     constexpr int ACT = decltype(act)::value;
-    auto finish = [&](int64_t r, float (&dy)[8], const float (&z)[8]) {
+    for (int r = n > 0 ? r0 + rl : r1; r < r1; r += RL * K) {
+      ep_u32x4 y[K], z[K];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if constexpr (ACT != TG_ACT_NONE) dy[e] *= ep_act_grad<ACT>(z[e]);
-        sum[e] += dy[e];
-      }
-      if (a.dZ) ep_put8(a.dZ, a.t, r * a.N + col, n, dy);
-    };
-    if (n >= 8) {
-      // dZ may be dY or Z: each element is read by the thread that writes it, before it does
-      for (int r = r0 + rl; r < r1; r += 256) {
-        ep_u32x4 y[8], z[8];
+      for (int k = 0; k < K; ++k)
+        if (k == 0 || r + RL * k < r1) {
+          y[k] = ep_load8_16(a.dY, (int64_t)(r + RL * k) * a.ldy + col, n);
+          if constexpr (ACT != TG_ACT_NONE) z[k] = ep_load8_16(a.Z, (int64_t)(r + RL * k) * a.ldz + col, n);
+        }
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (r + 32 * k < r1) {
-            y[k] = load16(a.dY + 2 * ((int64_t)(r + 32 * k) * a.ldy + col));
-            if constexpr (ACT != TG_ACT_NONE) z[k] = load16(a.Z + 2 * ((int64_t)(r + 32 * k) * a.ldz + col));
+      for (int k = 0; k < K; ++k)
+        if (k == 0 || r + RL * k < r1) {
+          float dy[8], zz[8];
+          ep_unpack8(a.t, y[k], dy);
+          if constexpr (ACT != TG_ACT_NONE) {
+            ep_unpack8(a.t, z[k], zz);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dy[e] *= ep_act_grad<ACT>(zz[e]);
           }
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (r + 32 * k < r1) {
-            float dy[8], zz[8] = {};
-            ep_unpack8(a.t, y[k], dy);
-            if constexpr (ACT != TG_ACT_NONE) ep_unpack8(a.t, z[k], zz);
-            finish(r + 32 * k, dy, zz);
-          }
-      }
-    } else if (n > 0) {
-      for (int r = r0 + rl; r < r1; r += 32) {
-        float dy[8], zz[8] = {};
-        ep_get8(a.dY, a.t, (int64_t)r * a.ldy + col, n, dy);
-        if constexpr (ACT != TG_ACT_NONE) ep_get8(a.Z, a.t, (int64_t)r * a.ldz + col, n, zz);
-        finish(r, dy, zz);
-      }
+          for (int e = 0; e < 8; ++e) sum[e] += dy[e];
+          if (a.dZ) ep_store8_16(a.dZ, (int64_t)(r + RL * k) * a.N + col, n, ep_pack8(a.t, dy));
+        }
     }
   });
   if (!a.sums) return;
 #pragma unroll
   for (int e = 0; e < 8; ++e) red[rl][lane * 8 + e] = sum[e];
   __syncthreads();
-  // 4 threads a column, 8 rows each, then their sums: always in the same order
-  const int c = (int)threadIdx.x >> 2, q = (int)threadIdx.x & 3, gc = (int)blockIdx.x * 64 + c;
+  // RL / 8 threads a column, 8 rows each, then their sums: always in the same order
+  constexpr int Q = RL / 8;
+  const int c = (int)threadIdx.x / Q, q = (int)threadIdx.x % Q, gc = (int)blockIdx.x * 64 + c;
   float s = 0.0f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) s += red[8 * q + k][c];
-  s += __shfl_xor(s, 1);
-  s += __shfl_xor(s, 2);
+#pragma unroll
+  for (int m = 1; m < Q; m <<= 1) s += __shfl_xor(s, m);
   if (q == 0 && gc < a.N) a.sums[(int64_t)blockIdx.y * a.N + gc] = s;
 }
 
@@ -131,7 +125,9 @@ hipError_t launch_ep_join(const EpArgs& g, hipStream_t s) {
 }
 
 hipError_t launch_act_grad(const ActGradArgs& a, int groups, hipStream_t s) {
-  hipLaunchKernelGGL(act_grad, dim3((unsigned)((a.N + 63) / 64), (unsigned)groups), dim3(256), 0, s, a);
+  const dim3 grid((unsigned)((a.N + 63) / 64), (unsigned)groups);
+  if (groups == 1) hipLaunchKernelGGL((act_grad<128, 2>), grid, dim3(1024), 0, s, a);
+  else hipLaunchKernelGGL((act_grad<32, 4>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
