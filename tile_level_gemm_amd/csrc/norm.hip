@@ -11,6 +11,9 @@
 // barrier; longer ones a workgroup of as many waves as their chunks need (1003 x 2057: 5 waves of one
 // chunk 5.4 us, 4 waves of two 6.2).  The sum of squares and max|H·w| (a row scale needs it:
 // max|Y| = rstd·max|H·w|) travel in one reduction.
+// Measured: 16384 x 8192 bf16 with residual to e4m3 blocks 163 us (5.8 TB/s of 944 MB); backward of
+// 8192 x 8192 bf16 with dH 100 us and 4 for the sum of dw's shares (5.2 TB/s of 537 MB); one row of
+// 4096 2.9 us, launch and latency.
 // Rows whose length is not a multiple of 8 end in a chunk moved back to the row's last 8
 // columns: every load is a whole vector, the columns another chunk owns (`dup` of them) are left
 // out of the sums, and both owners store the same values.
