@@ -18,6 +18,9 @@ def plan(M, N, K, ta=0, tb=1, t=BF, budget=None, **kw):
 @pytest.mark.parametrize("t", [BF, E4])
 def test_few_rows_take_the_token_kernel(M, N, cols, t):
     p = plan(M, N, 4096, t=t)
+    if t == BF and M > 16 and N * 4096 > 1 << 22:   # blocks are faster where they take the operands directly
+        assert p.kernel == tg.TG_EP_DIRECT
+        p = plan(M, N, 4096, t=t, lda=4097)
     assert (p.kernel, p.block_n, p.splits, p.workspace_bytes) == (tg.TG_EP_TOKENS, cols, 1, 0)
     assert p.block_m >= M and p.grid * p.block_n >= N > (p.grid - 1) * p.block_n
 
@@ -26,10 +29,24 @@ def test_few_rows_take_the_token_kernel(M, N, cols, t):
 def test_few_rows_against_transposed_weights_part_a_long_sum(N, K):
     for M in (1, 32):
         p = plan(M, N, K, tb=0)
+        if N * K > 1 << 23 and N % 8 == 0:
+            assert p.kernel == tg.TG_EP_DIRECT
+            p = plan(M, N, K, tb=0, lda=K + 1)
         blocks = (N + 31) // 32
         assert p.kernel == tg.TG_EP_TOKENS and p.block_n == 32 and p.grid == blocks * p.splits
         assert p.splits == 1 or (p.grid <= 256 and p.k_per_split >= 1024 and p.splits * p.k_per_split >= K)
         assert plan(M, N, K, tb=0, budget=0).splits == 1
+
+
+@pytest.mark.parametrize("ta", [0, 1])
+@pytest.mark.parametrize("tb", [0, 1])
+@pytest.mark.parametrize("M,N,K", [(700, 272, 136), (16, 4096, 4096), (3056, 21, 27), (4096, 24, 4096), (30, 2048, 4096), (64, 4096, 64)])
+def test_backward_workspace_holds_both_products_best_plans(M, N, K, ta, tb):
+    need = tg.tile_gemm_ep_bwd_workspace(M, N, K, ta, tb, BF)
+    da = (K, M, N, tb, 1) if ta else (M, K, N, 0, 1 - tb)
+    db = (N, K, M, 1, ta) if tb else (K, N, M, 1 - ta, 0)
+    for p in (da, db):
+        assert need >= plan(*p).workspace_bytes
 
 
 @pytest.mark.parametrize("M,N,K,bs", [

@@ -43,7 +43,7 @@ struct EpKernel {   // block kernels: block size 64 (staged and ring), 128 or 25
 };
 hipError_t launch_ep_block(const EpArgs& g, int trans_a, int trans_b, int a_dtype, int b_dtype,
                            const EpKernel& k, hipStream_t s);
-// M <= kTokenRows; `waves` (1 .. 8) waves share K
+// M <= kTokenRows; `waves` (1 .. 16) waves share K
 constexpr int64_t kTokenRows = 32;
 hipError_t launch_ep_tokens(const EpArgs& g, int trans_a, int trans_b, int a_dtype, int b_dtype, int waves,
                             hipStream_t s);

@@ -1,7 +1,7 @@
 // Product with an epilogue for few rows (ep.h has the formulas): a stream of weights.
 //
 // Bound by reading B once; A is small and comes from the caches.  A workgroup's waves take K steps
-// in turn, each with up to 16 KB of B in flight in registers before its first product, then the
+// in turn, 16 waves with 8 KB of B each in flight in registers before their first product, then the
 // waves' sums meet in LDS, are added in their order and finished with the epilogue operands that were
 // loaded first of all.  A CU draws about 26 GB/s from HBM this way whatever its waves ask for (131 KB:
 // 5 us), so the columns are cut until every CU has some.
@@ -20,9 +20,8 @@
 // The instruction's operands are exchanged (Bᵀ·Aᵀ), so a lane holds 4 consecutive columns of one row.
 // Any alignment, leading dimension and K: the last partial step loads element by element.
 //
-// Measured, weights from HBM: 1 x 4096 x 4096 bf16 9.3 us (3.6 TB/s with launch and first bytes, about
-// 4 us), 1 x 8192 x 8192 29.5 us (4.5 TB/s), 16 x 8192 x 4096 e4m3 10.9 us; [K][N] weights 4096 x 4096
-// 15 us with its join, as the 64-byte runs come slower.
+// Measured, weights from HBM: 1 x 4096 x 4096 bf16 8.5 us (8 waves with twice as much each 9.3), 1 x 8192 x
+// 8192 25.8 us (5.2 TB/s), 16 x 8192 x 4096 e4m3 9.8 us; about 4 us of each are launch and first bytes.
 #include "direct_gemm.h"
 #include "ep.h"
 
@@ -71,7 +70,7 @@ struct __attribute__((packed, aligned(2))) Bytes4 { uint32_t v; };
 // MT: row tiles of 16.  blockDim.x / 64 waves.
 // NI: column tiles of 16.
 template <bool A_MN, bool B_MN, int DT, int MT, int NI>
-__global__ __launch_bounds__(512) void gemm_ep_tokens(EpArgs g) {
+__global__ __launch_bounds__(1024) void gemm_ep_tokens(EpArgs g) {
   using EL = Elem<DT>;
   constexpr int E = EL::kBytes;
   static_assert(!B_MN || NI == 2, "a lane's two columns");
@@ -79,10 +78,10 @@ __global__ __launch_bounds__(512) void gemm_ep_tokens(EpArgs g) {
   constexpr int KS = B_MN ? 32 : 128 / E;       // K of a step
   constexpr int KI = E == 2 ? 32 : 128;         // K of an instruction
   constexpr int NF = KS / KI;                   // instructions of a step along K
-  constexpr int U = MT == 1 && (B_MN || NI == 1) ? 8 : 4;   // steps in flight
+  constexpr int U = MT == 1 && (B_MN || NI == 1) ? 4 : 2;   // steps in flight
   using Frag = typename EL::Frag;               // one instruction's operand: 8 16-bit values, 32 fp8
   constexpr int LD = CN + 1;
-  __shared__ float red[8][MT * 16][LD];
+  __shared__ float red[16][MT * 16][LD];
 
   const int nb = (int)gridDim.x;
   int bid = (int)blockIdx.x;
@@ -233,9 +232,9 @@ __global__ __launch_bounds__(512) void gemm_ep_tokens(EpArgs g) {
   __syncthreads();
   auto sum = [&](int row, int n) {
     float v = red[0][row][n];
-    if (W == 8) {
+    if (W == 16) {
 #pragma unroll
-      for (int w = 1; w < 8; ++w) v += red[w][row][n];
+      for (int w = 1; w < 16; ++w) v += red[w][row][n];
     } else {
       for (int w = 1; w < W; ++w) v += red[w][row][n];
     }

@@ -95,7 +95,12 @@ EpChoice choose_ep(int64_t M, int64_t N, int64_t K, int transB, int eb, bool dir
     c.splits = 0;
     return c;
   }
-  if (M <= kTokenRows) {
+  // Few rows: the token kernel, unless blocks can take the operands directly and are faster.  Weights
+  // [K][N] come to it in 64-byte runs (1 x 4096 x 4096 bf16 12.1 us, blocks 10.8; 1 x 2048 x 2048 9.0,
+  // blocks 9.3); 17 to 32 rows of 16 bits read A twice over (24 x 4096 x 4096 13.2 us, blocks 11.1;
+  // 32 x 1024 x 1024 5.4, blocks 6.0; fp8 32 x 8192 x 4096 11.6, blocks 12.9).
+  const bool blocks_win = direct && (!transB ? N * K > (int64_t)1 << 23 : M > 16 && eb == 2 && N * K > (int64_t)1 << 22);
+  if (M <= kTokenRows && !blocks_win) {
     c.kernel = TG_EP_TOKENS;
     if (transB) {
       // a workgroup for every CU, and no more where N has them to spare
@@ -113,7 +118,7 @@ EpChoice choose_ep(int64_t M, int64_t N, int64_t K, int transB, int eb, bool dir
         c.ws = per * c.splits;
       }
     }
-    c.waves = (int)std::min<int64_t>(8, (c.kps * eb + 127) / 128);   // a step of K each at least
+    c.waves = (int)std::min<int64_t>(16, (c.kps * eb + 127) / 128);   // a step of K each at least
     return c;
   }
   auto blocks = [&](int64_t b) { return ((M + b - 1) / b) * ((N + b - 1) / b); };
@@ -345,8 +350,10 @@ int64_t tile_gemm_ep_bwd_workspace(int64_t M, int64_t N, int64_t K, int transA, 
   if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim || !is16(dtype)) return 0;
   const int64_t groups = bias_groups(M, N);
   int64_t ws = groups > 1 ? groups * N * 4 : 0;
-  ws = std::max(ws, transA ? tile_gemm_ep_workspace(K, M, N, 0, 0, dtype) : tile_gemm_ep_workspace(M, K, N, 0, 0, dtype));
-  ws = std::max(ws, transB ? tile_gemm_ep_workspace(N, K, M, 0, 0, dtype) : tile_gemm_ep_workspace(K, N, M, 0, 0, dtype));
+  ws = std::max(ws, transA ? tile_gemm_ep_workspace(K, M, N, transB, 1, dtype)
+                           : tile_gemm_ep_workspace(M, K, N, 0, !transB, dtype));
+  ws = std::max(ws, transB ? tile_gemm_ep_workspace(N, K, M, 1, transA, dtype)
+                           : tile_gemm_ep_workspace(K, N, M, !transA, 0, dtype));
   return ws;
 }
 
