@@ -649,10 +649,12 @@ typedef enum tg_scale_kind {
  *   Y       device [rows, cols] of y_dtype, leading dimension ld_y.  TG_SCALE_NONE: y_dtype ==
  *           dtype.  Otherwise TG_FP8_E4M3 or TG_FP8_E5M2 holding Y/S rounded once (qmax 448 or
  *           57344; nothing saturates), and max|Y| is taken as at least 2^-100.  A row or block
- *           that holds a NaN or an infinity gets a NaN scale.
+ *           whose Y holds a NaN or an infinity gets a NaN scale (from an infinite weight too, or a
+ *           product past fp32).
  *   S       device scales, packed (see tg_scale_kind), or NULL for TG_SCALE_NONE.  TG_SCALE_BLOCK
  *           needs cols % 32 == 0 (TG_E_SHAPE).
- *   rstd    device fp32 [rows], or NULL: for the backward pass.
+ *   rstd    device fp32 [rows], or NULL: for the backward pass.  The mean of squares is taken in
+ *           fp32: rows with |H| above about 2^63 overflow it (rstd 0).
  *   rows, cols   rows 0 .. 2^30, cols 1 .. 2^30 (rows == 0 is a no-op); eps >= 0.
  */
 int tile_rmsnorm(const void* X, const void* R, const void* W, void* H, void* Y, void* S, float* rstd,

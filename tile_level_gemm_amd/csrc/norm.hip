@@ -10,7 +10,8 @@
 // the result, NV chunks of 8 columns a thread.  Rows up to 1024 columns take one wave each and no
 // barrier; longer ones a workgroup of as many waves as their chunks need (1003 x 2057: 5 waves of one
 // chunk 5.4 us, 4 waves of two 6.2).  The sum of squares and max|H·w| (a row scale needs it:
-// max|Y| = rstd·max|H·w|) travel in one reduction.
+// max|Y| = rstd·max|H·w|) travel in one reduction; a row whose max|H·w| is out of fp32's range
+// (top_fits) takes a second one for max|Y| itself.
 // Measured: 16384 x 8192 bf16 with residual to e4m3 blocks 163 us (5.8 TB/s of 944 MB); backward of
 // 8192 x 8192 bf16 with dH 100 us and 4 for the sum of dw's shares (5.2 TB/s of 537 MB); one row of
 // 4096 2.9 us, launch and latency.
@@ -100,6 +101,18 @@ __device__ __forceinline__ void row_reduce(float& s, float& m, bool want_max, fl
   }
 }
 
+// Whether rstd·max|H·w| is max|Y|: the product with the weight has neither overflowed nor lost bits
+// below the floor of max|Y| (NaN: no).
+__device__ __forceinline__ bool top_fits(float top) { return top >= kAmaxFloor && top < __builtin_inff(); }
+// Row scale of max|Y| >= the floor, and what Y is multiplied by; NaN for a row with a NaN or an infinity.
+__device__ __forceinline__ float row_scale(float amax, int t, float& inv) {
+  const float q = t == TG_FP8_E4M3 ? 448.0f : 57344.0f, nan = __builtin_nanf("");
+  amax = nan_max(amax, kAmaxFloor);
+  const bool fine = amax < __builtin_inff();
+  inv = fine ? q / amax : nan;
+  return fine ? amax / q : nan;
+}
+
 // SC: tg_scale_kind of the result
 // WAVE: a wave per row, four rows a workgroup; else a workgroup per row.
 template <int DT, int NV, int SC, bool WAVE, int MAXT>
@@ -148,10 +161,19 @@ __global__ __launch_bounds__(MAXT) void rmsnorm(NormArgs a) {
   const float rstd = 1.0f / sqrtf(ss / (float)cols + a.eps);
   float inv = 1.0f;
   if constexpr (SC == TG_SCALE_ROW) {
-    const float q = a.y_t == TG_FP8_E4M3 ? 448.0f : 57344.0f;
-    const float amax = nan_max(top * rstd, kAmaxFloor);
-    inv = q / amax;
-    if (t == 0) ((float*)a.S)[row] = amax / q;
+    float amax = top * rstd;
+    if (!top_fits(top)) {   // the same for all of the row's threads
+      float none = 0.0f;
+      amax = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = nan_max(amax, fabsf(h[j][e] * rstd * w[j][e]));
+      if constexpr (!WAVE) __syncthreads();   // every wave has read the first reduction
+      row_reduce<WAVE>(none, amax, true, red);
+    }
+    const float s = row_scale(amax, a.y_t, inv);
+    if (t == 0) ((float*)a.S)[row] = s;
   }
   if (a.rstd && t == 0) a.rstd[row] = rstd;
 #pragma unroll
@@ -219,10 +241,20 @@ __global__ __launch_bounds__(1024) void rmsnorm_long(NormArgs a) {
   const float rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
   float inv = 1.0f;
   if constexpr (SC == TG_SCALE_ROW) {
-    const float q = a.y_t == TG_FP8_E4M3 ? 448.0f : 57344.0f;
-    const float amax = nan_max(top * rstd, kAmaxFloor);
-    inv = q / amax;
-    if (threadIdx.x == 0) ((float*)a.S)[row] = amax / q;
+    float amax = top * rstd;
+    if (!top_fits(top)) {
+      float none = 0.0f;
+      amax = 0.0f;
+      for (int64_t col = (int64_t)threadIdx.x * 8; col < a.cols; col += 8192) {
+        get(col, (int)min((int64_t)8, a.cols - col), h, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = nan_max(amax, fabsf(h[e] * rstd * w[e]));
+      }
+      __syncthreads();
+      row_reduce<false>(none, amax, true, red);
+    }
+    const float s = row_scale(amax, a.y_t, inv);
+    if (threadIdx.x == 0) ((float*)a.S)[row] = s;
   }
   if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
   // whole waves take the shuffles: the bound is rounded up to a wave's 512 columns
