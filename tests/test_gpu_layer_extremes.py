@@ -1,4 +1,4 @@
-"""Norm results where Y or the product H·w leaves the ordinary range.
+"""Norm results where Y or the product H·w leaves the ordinary range, and 8-bit codes at their borders.
 Bounds are oracle/layer.py's."""
 
 import numpy as np
@@ -44,3 +44,16 @@ def test_row_scale_where_the_product_with_the_weight_leaves_fp32(cols, hx, wx, r
     X, W = rand(1, (rows, cols), "f32", hx), rand(2, (cols,), "f32", wx)
     for fmt in ("e4m3", "e5m2"):
         check_norm(tg.rms_norm(X, W, 0.0, out_dtype=T[fmt], scales="row"), X, None, W, 0.0, "f32", fmt, "row")
+
+
+@pytest.mark.parametrize("cols", [5, 64, 1000, 2057, 4096, 20000])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_row_scaled_codes_are_the_quotient_rounded_once(cols, fmt):
+    """fp32 rows: the 16-bit-free call gives the Y that the codes are made of, so every code is known."""
+    say(f"norm codes cols={cols} {fmt}")
+    rows = 4_000_000 // cols
+    X, W = rand(cols, (rows, cols), "f32", 3.0), rand(cols + 1, (cols,), "f32")
+    Y = tg.rms_norm(X, W).y
+    r = tg.rms_norm(X, W, out_dtype=T[fmt], scales="row")
+    want = (Y / r.scale[:, None]).to(T[fmt])
+    assert torch.equal(r.y.view(torch.uint8), want.view(torch.uint8)), int((r.y.view(torch.uint8) != want.view(torch.uint8)).sum())
