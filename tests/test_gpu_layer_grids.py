@@ -1,0 +1,93 @@
+"""Layer operators past 2^32 threads a grid dimension and past 2^16 workgroups in y: many short rows, very long
+rows.  Sampled rows and columns against float64."""
+
+import numpy as np
+import pytest
+import torch
+
+import tile_level_gemm_amd as tg
+from oracle import layer as ol
+
+from .gpu_util import say
+from .test_gpu_layer import T, check, check_norm, dev, host
+
+pytestmark = pytest.mark.gpu
+
+
+def filled(seed, shape, dtype, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.empty(shape, dtype=T[dtype], device=dev()).normal_(0.0, scale, generator=g)
+
+
+def some(n):
+    """The first and last of n, those around powers of two, and others."""
+    edges = [2 ** k + d for k in range(10, 31) for d in (-1, 0, 1)]
+    r = np.concatenate([np.arange(40), np.arange(n - 40, n), edges, np.random.default_rng(n).integers(0, n, 400)])
+    return torch.from_numpy(np.unique(r[(r >= 0) & (r < n)])).to(dev())
+
+
+@pytest.mark.parametrize("rows,cols", [((1 << 22) + 3, 4), ((1 << 26) + 5, 8)])
+def test_norm_of_many_short_rows(rows, cols):
+    say(f"norm rows={rows} cols={cols}")
+    X, R, W = filled(1, (rows, cols), "f16", 3.0), filled(2, (rows, cols), "f16"), filled(3, (cols,), "f16")
+    pick = some(rows)
+    r = tg.rms_norm(X, W, residual=R)
+    part = tg.Norm(r.y[pick], None, r.rstd[pick], r.h[pick])
+    check_norm(part, X[pick], R[pick], W, 1e-5, "f16", None, None)
+    assert bool((r.rstd > 0).all())
+    r8 = tg.rms_norm(X, W, residual=R, scales="row")
+    part = tg.Norm(r8.y.view(torch.uint8)[pick].view(T["e4m3"]), r8.scale[pick], r8.rstd[pick], r8.h[pick])
+    check_norm(part, X[pick], R[pick], W, 1e-5, "f16", "e4m3", "row")
+    assert torch.equal(r8.rstd, r.rstd)
+
+
+@pytest.mark.parametrize("rows,cols", [((1 << 22) + 3, 4), ((1 << 26) + 5, 8)])
+def test_norm_backward_of_many_short_rows(rows, cols):
+    say(f"norm backward rows={rows} cols={cols}")
+    H, W, dY = filled(1, (rows, cols), "f16", 3.0), filled(2, (cols,), "f16"), filled(3, (rows, cols), "f16")
+    rstd = torch.rsqrt(H.float().square().mean(dim=1) + 1e-5)
+    dX, dw = tg.rms_norm_backward(dY, H, W, rstd)
+    pick = some(rows)
+    ref, bound, _, _ = ol.norm_backward(host(dY[pick]), host(H[pick]), host(W), host(rstd[pick]), None, "f16")
+    check(dX[pick], ref, bound, "dX")
+    terms = torch.zeros(2, cols, dtype=torch.float64, device=dev())
+    for at in range(0, rows, 1 << 24):
+        s = slice(at, at + (1 << 24))
+        t = dY[s].double() * (H[s].double() * rstd[s, None].double())
+        terms += torch.stack([t.sum(dim=0), t.abs().sum(dim=0)])
+    # at most 512 workgroups share the rows, each adds its rows in turn, then up to 512 shares: 2^-24 of
+    # the magnitudes for every addition on the way and three products
+    adds = (rows + 511) // 512 + 512 + 3
+    check(dw, host_64(terms[0]), host_64(terms[1]) * adds * 2.0 ** -24, "dw")
+
+
+def host_64(t):
+    return t.cpu().numpy()
+
+
+@pytest.mark.parametrize("cols", [(1 << 27) + 4099])
+def test_norm_of_a_very_long_row(cols):
+    """More panels of 2048 columns than grid.y holds."""
+    say(f"norm cols={cols}")
+    X, W, dY = filled(1, (1, cols), "bf16", 3.0), filled(2, (cols,), "bf16"), filled(3, (1, cols), "bf16")
+    r = tg.rms_norm(X, W)
+    # 1024 threads add cols / 1024 squares each, one after the other: 2^-24 of the sum for each addition,
+    # half of that in the root
+    rel = (cols / 1024 + 32) * 2.0 ** -25
+    want = float(torch.rsqrt(X.double().square().mean() + 1e-5))
+    rstd = float(r.rstd)
+    assert abs(rstd - want) <= rel * want
+    pick = some(cols)
+    x, w, dy = host(X[0, pick]), host(W[pick]), host(dY[0, pick])
+    Y = x * rstd * w
+    check(r.y[0, pick], Y, np.abs(Y) * (2.0 ** -8 + 4 * 2.0 ** -24) + ol.TINY["bf16"], "Y")
+    dX, dw = tg.rms_norm_backward(dY, X, W, r.rstd)
+    xh = X.double() * rstd
+    t = dY.double() * W.double() * xh
+    c, cerr = float(t.mean()), float(t.abs().mean()) * 2 * rel
+    g = dy * w
+    xh = x * rstd
+    ref = rstd * (g - xh * c)
+    err = rstd * (6 * 2.0 ** -24 * (np.abs(g) + np.abs(xh * c)) + np.abs(xh) * cerr)
+    check(dX[0, pick], ref, err * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref) + ol.TINY["bf16"], "dX")
+    check(dw[pick], dy * xh, 4 * 2.0 ** -24 * np.abs(dy * xh), "dw")

@@ -125,8 +125,8 @@ __global__ __launch_bounds__(MAXT) void rmsnorm(NormArgs a) {
   __shared__ float red[WAVE ? 1 : kMaxWaves][2];
   const int TPR = WAVE ? 64 : (int)blockDim.x;
   const int t = WAVE ? (int)threadIdx.x & 63 : (int)threadIdx.x;
-  const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
-  if (WAVE && row >= a.rows) return;
+  const int64_t row = WAVE ? wide_block() * 4 + (threadIdx.x >> 6) : wide_block();
+  if (row >= a.rows) return;
   const int cols = (int)a.cols;
   float h[NV][8], w[NV][8];
 #pragma unroll
@@ -217,7 +217,8 @@ __global__ __launch_bounds__(MAXT) void rmsnorm(NormArgs a) {
 template <int DT, int SC>
 __global__ __launch_bounds__(1024) void rmsnorm_long(NormArgs a) {
   __shared__ float red[16][2];
-  const int64_t row = blockIdx.x;
+  const int64_t row = wide_block();
+  if (row >= a.rows) return;
   auto get = [&](int64_t col, int n, float (&h)[8], float (&w)[8]) {
     ep_get8(a.X, DT, row * a.ldx + col, n, h);
     if (a.R) {
@@ -435,7 +436,8 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_bwd(NormBwdArgs a) {
 template <int DT>
 __global__ __launch_bounds__(1024) void rmsnorm_bwd_dot(NormBwdArgs a) {
   __shared__ float red[16][2];
-  const int64_t row = blockIdx.x;
+  const int64_t row = wide_block();
+  if (row >= a.rows) return;
   const float rstd = a.rstd[row];
   float dot = 0.0f, none = 0.0f;
   for (int64_t col = (int64_t)threadIdx.x * 8; col < a.cols; col += 8192) {
@@ -451,10 +453,11 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_dot(NormBwdArgs a) {
   row_reduce<false>(dot, none, false, red);
   if (threadIdx.x == 0) a.dot[row] = dot / (float)a.cols;
 }
-// ... then dX and dw by panels of 2048 columns (blockIdx.y), rows shared over blockIdx.x.
+// ... then dX and dw by panels of 2048 columns (blockIdx.y, and z past 2^15 of them), rows shared over
+// blockIdx.x.
 template <int DT>
 __global__ __launch_bounds__(256) void rmsnorm_bwd_panel(NormBwdArgs a) {
-  const int64_t col = (int64_t)blockIdx.y * 2048 + threadIdx.x * 8;
+  const int64_t col = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * 2048 + threadIdx.x * 8;
   if (col >= a.cols) return;
   const int n = (int)min((int64_t)8, a.cols - col);
   float w[8], dw[8] = {};
@@ -479,12 +482,14 @@ __global__ __launch_bounds__(256) void rmsnorm_bwd_panel(NormBwdArgs a) {
 
 // threads of a workgroup that holds a row, nv chunks each: whole waves
 unsigned row_threads(int64_t cols, int nv) { return (unsigned)((cols + 512 * nv - 1) / (512 * nv) * 64); }
+// threads of a two-pass kernel's workgroup: rows of fewer than 8 columns are one thread's
+dim3 long_threads(int64_t cols) { return dim3(cols < 8 ? 64 : 1024); }
 
 template <int DT, int SC>
 hipError_t go_fwd(const NormArgs& a, hipStream_t s) {
-  const dim3 rows((unsigned)a.rows), waves((unsigned)((a.rows + 3) / 4));
+  const dim3 rows = wide_grid(a.rows), waves = wide_grid((a.rows + 3) / 4);
   const dim3 one(row_threads(a.cols, 1)), two(row_threads(a.cols, 2));
-  if (!norm_in_registers(a.cols)) hipLaunchKernelGGL((rmsnorm_long<DT, SC>), rows, dim3(1024), 0, s, a);
+  if (!norm_in_registers(a.cols)) hipLaunchKernelGGL((rmsnorm_long<DT, SC>), rows, long_threads(a.cols), 0, s, a);
   else if (a.cols <= 512) hipLaunchKernelGGL((rmsnorm<DT, 1, SC, true, 256>), waves, dim3(256), 0, s, a);
   else if (a.cols <= 1024) hipLaunchKernelGGL((rmsnorm<DT, 2, SC, true, 256>), waves, dim3(256), 0, s, a);
   else if (a.cols <= 4096) hipLaunchKernelGGL((rmsnorm<DT, 1, SC, false, 512>), rows, one, 0, s, a);
@@ -502,8 +507,11 @@ template <int DT>
 hipError_t go_bwd(const NormBwdArgs& a, int64_t groups, hipStream_t s) {
   const dim3 g((unsigned)groups);
   if (!norm_in_registers(a.cols)) {
-    hipLaunchKernelGGL((rmsnorm_bwd_dot<DT>), dim3((unsigned)a.rows), dim3(1024), 0, s, a);
-    hipLaunchKernelGGL((rmsnorm_bwd_panel<DT>), dim3((unsigned)groups, (unsigned)((a.cols + 2047) / 2048)),
+    hipLaunchKernelGGL((rmsnorm_bwd_dot<DT>), wide_grid(a.rows), long_threads(a.cols), 0, s, a);
+    const hipError_t e = hipGetLastError();   // without the dot products there is nothing to read
+    if (e != hipSuccess) return e;
+    const int64_t panels = (a.cols + 2047) / 2048, z = (panels + 32767) / 32768;
+    hipLaunchKernelGGL((rmsnorm_bwd_panel<DT>), dim3((unsigned)groups, (unsigned)((panels + z - 1) / z), (unsigned)z),
                        dim3(256), 0, s, a);
   } else if (a.cols <= 512) hipLaunchKernelGGL((rmsnorm_bwd<DT, 1, true, 256>), g, dim3(256), 0, s, a);
   else if (a.cols <= 1024) hipLaunchKernelGGL((rmsnorm_bwd<DT, 2, true, 256>), g, dim3(256), 0, s, a);

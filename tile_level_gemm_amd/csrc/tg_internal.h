@@ -38,6 +38,18 @@ int partition(int64_t rows, int64_t cols, int eb, int threads, const Side& drive
 bool tile_steps_aligned(const Side& s, int64_t tile_rows, int64_t tile_cols, int64_t tiles_r,
                         int64_t tiles_c, int64_t vec);
 
+// ------------------------------------------------------------ launch size ---
+// A launch holds fewer than 2^32 threads in each dimension: `blocks` workgroups of up to 1024 threads
+// (0 .. 2^37 of them) lie over x and y.  The last few may lie past the end; a kernel finds its place
+// with wide_block().
+inline dim3 wide_grid(int64_t blocks) {
+  const int64_t most = (int64_t)1 << 21, y = (blocks + most - 1) / most;
+  return y <= 1 ? dim3((unsigned)blocks) : dim3((unsigned)((blocks + y - 1) / y), (unsigned)y);
+}
+#ifdef __HIP__
+__device__ __forceinline__ int64_t wide_block() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+#endif
+
 // --------------------------------------------------------- launch structs ---
 struct CopyPhase {
   int32_t outer;       // rounds per thread
