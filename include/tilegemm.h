@@ -579,7 +579,10 @@ typedef struct tg_ep_plan {
  *           16-bit: a_dtype == b_dtype, TG_F16 or TG_BF16, any orientation.  fp8: each
  *           TG_FP8_E4M3 or TG_FP8_E5M2, transA == 0 and transB == 1 (else TG_E_LAYOUT).
  *   D       device [M,N] of d_dtype (TG_F16, TG_BF16 or TG_F32), leading dimension ldd.
- *   M,N,K   any, 0 .. 2^30.  M == 0 or N == 0 is a no-op; K == 0 has A·B = 0.
+ *   M,N,K   any, 0 .. 2^30.  M == 0 or N == 0 is a no-op; K == 0 has A·B = 0.  TG_E_SHAPE above 2^41
+ *           results, and where the plan's workgroups would hold 2^32 threads: 2^23 blocks of 128 x 128
+ *           or 256 x 256 (an extent within 128 of 2^30 where rows are no multiples of 16 bytes, an extent
+ *           above 2^29 with more than 128 of the other, ...).
  *   ep      the epilogue, or NULL for none of it.
  *   workspace, workspace_bytes   device, 16-byte aligned, or NULL and 0: problems with few output
  *           tiles and a long K sum parts of K in different workgroups when the parts' fp32

@@ -91,3 +91,48 @@ def test_norm_of_a_very_long_row(cols):
     err = rstd * (6 * 2.0 ** -24 * (np.abs(g) + np.abs(xh * c)) + np.abs(xh) * cerr)
     check(dX[0, pick], ref, err * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref) + ol.TINY["bf16"], "dX")
     check(dw[pick], dy * xh, 4 * 2.0 ** -24 * np.abs(dy * xh), "dw")
+
+
+@pytest.mark.parametrize("cols", [(1 << 27) + 4099])
+def test_norm_backward_sums_shares_of_very_long_rows(cols):
+    """Two rows, a share of dw each."""
+    say(f"norm backward shares cols={cols}")
+    X, W, dY = filled(1, (2, cols), "bf16", 3.0), filled(2, (cols,), "bf16"), filled(3, (2, cols), "bf16")
+    rstd = torch.tensor([0.25, 0.5], device=dev())
+    _, dw = tg.rms_norm_backward(dY, X, W, rstd)
+    pick = some(cols)
+    t = host(dY[:, pick]) * host(X[:, pick]) * host(rstd)[:, None]
+    check(dw[pick], t.sum(axis=0), 6 * 2.0 ** -24 * np.abs(t).sum(axis=0), "dw")
+
+
+@pytest.mark.parametrize("M", [1, 2, 300])
+@pytest.mark.parametrize("act", ["none", "relu"])
+def test_bias_gradient_of_very_many_columns(M, act):
+    """300 rows: narrower, but in two groups of rows."""
+    N = (1 << 28) + 1033 if M < 300 else (1 << 21) - 7
+    say(f"bias gradient {M}x{N} {act}")
+    bf = T["bf16"]
+    dY, Z = filled(1, (M, N), "bf16"), filled(2, (M, N), "bf16")
+    A, B = torch.empty(M, 1, dtype=bf, device=dev()), torch.empty(N, 1, dtype=bf, device=dev())
+    dZ, _, _, dbias = tg.gemm_ep_backward(dY, A, B, Z=Z, act=act, need_dA=False, need_dB=False)
+    pick = some(N)
+    ref, bound, sref, sbound = ol.act_backward(host(dY[:, pick]), host(Z[:, pick]), act, "bf16")
+    check(dZ[:, pick], ref, bound, "dZ")
+    check(dbias[pick], sref, sbound, "dbias")
+    if M == 1:   # every column: one term each
+        assert torch.equal(dbias, dY[0].float() if act == "none" else torch.where(Z[0] > 0, dY[0], 0).float())
+
+
+def test_epilogue_of_a_zero_product_past_two_to_the_35_results():
+    M, N = 1 << 18, (1 << 17) + 8
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 69 GB for the result")
+    say(f"zero product {M}x{N}")
+    bf = T["bf16"]
+    bias = filled(1, (N,), "bf16")
+    D = tg.gemm_ep(torch.empty(M, 0, dtype=bf, device=dev()), torch.empty(N, 0, dtype=bf, device=dev()), bias=bias, act="relu")
+    want = torch.relu(bias)
+    for at in range(0, M, 1 << 14):
+        assert bool((D[at:at + (1 << 14)] == want).all()), at
+    del D
+    torch.cuda.empty_cache()

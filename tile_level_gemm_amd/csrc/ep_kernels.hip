@@ -10,7 +10,7 @@ namespace {
 // written: two parts of 4096 x 2048, 84 MB, 15.5 us (5.4 TB/s).  Four parts' loads are in flight
 // together: one at a time, 16 parts of one row took 7.9 us, nearly all of it waiting.
 __global__ __launch_bounds__(256) void ep_join(EpArgs g, int64_t chunks) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t i = wide_block() * 256 + threadIdx.x;
   if (i >= chunks) return;
   const int per_row = (g.N + 7) / 8;
   const int row = (int)(i / per_row), col = (int)(i % per_row) * 8;
@@ -48,7 +48,8 @@ template <int RL, int K>
 __global__ __launch_bounds__(8 * RL) void act_grad(ActGradArgs a) {
   __shared__ float red[RL][64 + 1];
   const int lane = (int)threadIdx.x & 7, rl = (int)threadIdx.x >> 3;
-  const int col = (int)blockIdx.x * 64 + lane * 8, n = a.N - col;
+  const int first = ((int)blockIdx.z * (int)gridDim.x + (int)blockIdx.x) * 64;   // of the workgroup's columns
+  const int col = first + lane * 8, n = a.N - col;
   const int r0 = (int)blockIdx.y * a.rows_per, r1 = min(a.M, r0 + a.rows_per);
   float sum[8] = {};
   // dZ may be dY or Z: each element is read by the thread that writes it, before it does
@@ -84,7 +85,7 @@ __global__ __launch_bounds__(8 * RL) void act_grad(ActGradArgs a) {
   __syncthreads();
   // RL / 8 threads a column, 8 rows each, then their sums: always in the same order
   constexpr int Q = RL / 8;
-  const int c = (int)threadIdx.x / Q, q = (int)threadIdx.x % Q, gc = (int)blockIdx.x * 64 + c;
+  const int c = (int)threadIdx.x / Q, q = (int)threadIdx.x % Q, gc = first + c;
   float s = 0.0f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) s += red[8 * q + k][c];
@@ -99,7 +100,7 @@ __global__ __launch_bounds__(8 * RL) void act_grad(ActGradArgs a) {
 __global__ __launch_bounds__(1024) void sum_rows(const float* part, int64_t G, int64_t N, float* out) {
   __shared__ float red[32][33];
   const int c = (int)threadIdx.x & 31, l = (int)threadIdx.x >> 5;
-  const int64_t n = (int64_t)blockIdx.x * 32 + c;
+  const int64_t first = wide_block() * 32, n = first + c;
   float s = 0.0f;
   if (n < N) {
     const float* p = part + (int64_t)l * N + n;
@@ -112,7 +113,7 @@ __global__ __launch_bounds__(1024) void sum_rows(const float* part, int64_t G, i
   s = red[c][l];
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) s += __shfl_xor(s, m);
-  const int64_t o = (int64_t)blockIdx.x * 32 + l;
+  const int64_t o = first + l;
   if (c == 0 && o < N) out[o] = s;
 }
 
@@ -120,19 +121,20 @@ __global__ __launch_bounds__(1024) void sum_rows(const float* part, int64_t G, i
 
 hipError_t launch_ep_join(const EpArgs& g, hipStream_t s) {
   const int64_t chunks = (int64_t)g.M * ((g.N + 7) / 8);
-  hipLaunchKernelGGL(ep_join, dim3((unsigned)((chunks + 255) / 256)), dim3(256), 0, s, g, chunks);
+  hipLaunchKernelGGL(ep_join, wide_grid((chunks + 255) / 256), dim3(256), 0, s, g, chunks);
   return hipGetLastError();
 }
 
 hipError_t launch_act_grad(const ActGradArgs& a, int groups, hipStream_t s) {
-  const dim3 grid((unsigned)((a.N + 63) / 64), (unsigned)groups);
+  // columns over x, and z where x would pass its threads; rows over y
+  const dim3 cols = wide_grid(((int64_t)a.N + 63) / 64), grid(cols.x, (unsigned)groups, cols.y);
   if (groups == 1) hipLaunchKernelGGL((act_grad<128, 2>), grid, dim3(1024), 0, s, a);
   else hipLaunchKernelGGL((act_grad<32, 4>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 hipError_t launch_sum_rows(const float* part, int64_t G, int64_t N, float* out, hipStream_t s) {
-  hipLaunchKernelGGL(sum_rows, dim3((unsigned)((N + 31) / 32)), dim3(1024), 0, s, part, G, N, out);
+  hipLaunchKernelGGL(sum_rows, wide_grid((N + 31) / 32), dim3(1024), 0, s, part, G, N, out);
   return hipGetLastError();
 }
 

@@ -242,8 +242,10 @@ int plan_ep(const void* A, const void* B, const void* D, int64_t M, int64_t N, i
   } else {
     plan->grid = (M * ((N + 7) / 8) + 255) / 256;
   }
-  if (plan->grid > 0x7fffffff || M * ((N + 7) / 8) > ((int64_t)1 << 38))
-    return fail(TG_E_SHAPE, "too many output tiles");
+  // a launch of blocks holds fewer than 2^32 threads
+  const int64_t threads = c.kernel == TG_EP_TOKENS ? 64 * c.waves : c.bs == 64 ? 256 : 512;
+  if ((c.kernel != TG_EP_JOIN && plan->grid * threads >= (int64_t)1 << 32) || M * ((N + 7) / 8) > ((int64_t)1 << 38))
+    return fail(TG_E_SHAPE, fmt("too many output tiles (%lld workgroups of %lld threads)", plan->grid, threads));
   *g = EpArgs{};
   g->A = (const uint8_t*)A;
   g->B = (const uint8_t*)B;
