@@ -608,7 +608,7 @@ int tile_gemm_ep_plan(const void* A, const void* B, const void* D, int64_t M, in
 int64_t tile_gemm_ep_workspace(int64_t M, int64_t N, int64_t K, int transA, int transB, int a_dtype);
 
 /*
- * tile_gemm_ep_bwd — gradients of D = act(A·B + bias) + residual for the gradient dY of D:
+ * tile_gemm_ep_bwd — gradients of D = act(A·B + bias) + residual, without scales, for the gradient dY of D:
  *
  *   dZ = dY·act'(Z)    dbias[n] = sum_m dZ[m][n]    dA = dZ·B^T    dB = A^T·dZ
  *
@@ -630,6 +630,22 @@ int tile_gemm_ep_bwd(const void* dY, const void* Z, const void* A, const void* B
                      void* dB, float* dbias, int64_t M, int64_t N, int64_t K, int64_t ld_dy,
                      int64_t ld_z, int64_t lda, int64_t ldb, int transA, int transB, int dtype,
                      int act, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * tile_gemm_ep_bwd_scaled — the same for a scaled product, Z = row_scale[m]·col_scale[n]·A·B + bias:
+ *
+ *   dZ = row_scale[m]·col_scale[n]·dY·act'(Z)    dbias[n] = sum_m dY·act'(Z)
+ *   dA = dZ·B^T    dB = A^T·dZ
+ *
+ * so dZ is the gradient of A·B here.  row_scale, col_scale: device fp32 [M], [N] as given to
+ * tile_gemm_ep, or NULL (both NULL: tile_gemm_ep_bwd); they get no gradients.  dZ may be NULL only
+ * without scales and without an activation.  The rest, and the workspace, as for tile_gemm_ep_bwd.
+ */
+int tile_gemm_ep_bwd_scaled(const void* dY, const void* Z, const void* A, const void* B,
+                            const float* row_scale, const float* col_scale, void* dZ, void* dA, void* dB,
+                            float* dbias, int64_t M, int64_t N, int64_t K, int64_t ld_dy, int64_t ld_z,
+                            int64_t lda, int64_t ldb, int transA, int transB, int dtype, int act,
+                            void* workspace, int64_t workspace_bytes, void* stream);
 
 /* tile_gemm_ep_bwd_workspace — host-only: bytes of workspace tile_gemm_ep_bwd uses at most. */
 int64_t tile_gemm_ep_bwd_workspace(int64_t M, int64_t N, int64_t K, int transA, int transB, int dtype);

@@ -171,6 +171,8 @@ _SIGS = {
     "tile_gemm_ep_workspace": (_I64, [_I64, _I64, _I64, _INT, _INT, _INT]),
     "tile_gemm_ep_bwd": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _I64,
                                 _I64, _I64, _INT, _INT, _INT, _INT, _VP, _I64, _VP]),
+    "tile_gemm_ep_bwd_scaled": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64,
+                                       _I64, _I64, _I64, _INT, _INT, _INT, _INT, _VP, _I64, _VP]),
     "tile_gemm_ep_bwd_workspace": (_I64, [_I64, _I64, _I64, _INT, _INT, _INT]),
     "tile_rmsnorm": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _I64, _I64, _F,
                             _INT, _INT, _INT, _INT, _VP]),
@@ -618,8 +620,8 @@ def tile_gemm_ep_workspace(M, N, K, transA, transB, a_dtype):
 
 
 def tile_gemm_ep_bwd(dY, Z, A, B, dZ, dA, dB, dbias, M, N, K, transA, transB, dtype, act, *, ld_dy=0, ld_z=0,
-                     lda=0, ldb=0, workspace=None, workspace_bytes=None, stream=None):
-    """Gradients of tile_gemm_ep for 16-bit operands (see include/tilegemm.h)."""
+                     lda=0, ldb=0, row_scale=None, col_scale=None, workspace=None, workspace_bytes=None, stream=None):
+    """Gradients of tile_gemm_ep for 16-bit operands, scaled or not (see include/tilegemm.h)."""
     e = ELEM_BYTES.get(int(dtype), 1)
     m, n, k = max(int(M), 0), max(int(N), 0), max(int(K), 0)
     if workspace is not None and workspace_bytes is None:
@@ -629,9 +631,14 @@ def tile_gemm_ep_bwd(dY, Z, A, B, dZ, dA, dB, dbias, M, N, K, transA, transB, dt
               ("A", A, e, _span(k if transA else m, m if transA else k, lda, e)),
               ("B", B, e, _span(n if transB else k, k if transB else n, ldb, e)),
               ("dZ", dZ, e, m * n * e), ("dA", dA, e, m * k * e), ("dB", dB, e, k * n * e),
-              ("dbias", dbias, 4, n * 4), ("workspace", workspace, None, nb))
-    _check(lib().tile_gemm_ep_bwd(*p[:8], M, N, K, int(ld_dy), int(ld_z), int(lda), int(ldb), int(transA),
-                                  int(transB), int(dtype), int(act), p[8], nb, _stream(stream)))
+              ("dbias", dbias, 4, n * 4), ("workspace", workspace, None, nb), ("row_scale", row_scale, 4, m * 4),
+              ("col_scale", col_scale, 4, n * 4))
+    rest = (M, N, K, int(ld_dy), int(ld_z), int(lda), int(ldb), int(transA), int(transB), int(dtype), int(act), p[8], nb,
+            _stream(stream))
+    if p[9] is None and p[10] is None:
+        _check(lib().tile_gemm_ep_bwd(*p[:8], *rest))
+    else:
+        _check(lib().tile_gemm_ep_bwd_scaled(*p[:4], *p[9:], *p[4:8], *rest))
 
 
 def tile_gemm_ep_bwd_workspace(M, N, K, transA, transB, dtype):
@@ -729,16 +736,19 @@ def gemm_ep(A, B, bias=None, act="none", residual=None, row_scale=None, col_scal
 
 
 def gemm_ep_backward(dY, A, B, Z=None, act="none", trans_a=False, trans_b=True, need_dA=True, need_dB=True,
-                     need_dbias=True, stream=None):
+                     need_dbias=True, stream=None, row_scale=None, col_scale=None):
     """Gradients of gemm_ep for 16-bit operands: (dZ, dA, dB, dbias), None for what is not needed.
 
-    Z is what gemm_ep returned with keep_z.  Without an activation dZ is dY itself.  dA and dB have
-    A's and B's stored orientation, dbias is float32; the residual's gradient is dY."""
+    Z is what gemm_ep returned with keep_z, row_scale and col_scale what it was given; they get no
+    gradients.  Without scales and an activation dZ is dY itself; with scales it carries them (the
+    gradient of A·B).  dA and dB have A's and B's stored orientation, dbias is float32; the
+    residual's gradient is dY.  The products take dZ as it is held, in 16 bits."""
     if stream is not None:
         with _On(stream):
-            return gemm_ep_backward(dY, A, B, Z, act, trans_a, trans_b, need_dA, need_dB, need_dbias)
+            return gemm_ep_backward(dY, A, B, Z, act, trans_a, trans_b, need_dA, need_dB, need_dbias, None, row_scale,
+                                    col_scale)
     return (_calls or _native()).gemm_ep_backward(dY, A, B, Z, _act(act), trans_a, trans_b, need_dA, need_dB,
-                                                  need_dbias)
+                                                  need_dbias, row_scale, col_scale)
 
 
 class Norm:

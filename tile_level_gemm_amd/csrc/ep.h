@@ -49,12 +49,15 @@ hipError_t launch_ep_tokens(const EpArgs& g, int trans_a, int trans_b, int a_dty
                             hipStream_t s);
 hipError_t launch_ep_join(const EpArgs& g, hipStream_t s);
 
-// dZ = dY·act'(Z) ([M][N] packed, may be NULL) and column sums [groups][N] (may be NULL).
+// dZ = dY·act'(Z) ([M][N] packed, may be NULL) and column sums [groups][N] (may be NULL).  With scales the
+// sums are of that, and dZ receives row_scale·col_scale·dY·act'(Z).
 struct ActGradArgs {
   const uint8_t* dY;
   const uint8_t* Z;
   uint8_t* dZ;
   float* sums;
+  const float* rs;   // row and column scales, or NULL
+  const float* cs;
   int64_t ldy, ldz;
   int32_t M, N, rows_per;   // rows per group
   int32_t t, act;

@@ -44,14 +44,20 @@ __global__ __launch_bounds__(256) void ep_join(EpArgs g, int64_t chunks) {
 // rows each in flight (4096 x 8192: 43 us; 1024 threads with two 51).  A problem that one workgroup per
 // 64 columns holds waits for its instructions as well as its rows: there 1024 threads with two
 // (200 x 520: 5.4 us; 256 with eight rows 7.3).
-template <int RL, int K>
+// SCALED: a scaled product's gradient, with the scales in registers beside them.
+template <int RL, int K, bool SCALED>
 __global__ __launch_bounds__(8 * RL) void act_grad(ActGradArgs a) {
   __shared__ float red[RL][64 + 1];
   const int lane = (int)threadIdx.x & 7, rl = (int)threadIdx.x >> 3;
   const int first = ((int)blockIdx.z * (int)gridDim.x + (int)blockIdx.x) * 64;   // of the workgroup's columns
   const int col = first + lane * 8, n = a.N - col;
   const int r0 = (int)blockIdx.y * a.rows_per, r1 = min(a.M, r0 + a.rows_per);
-  float sum[8] = {};
+  float sum[8] = {}, cs[8];
+  if constexpr (SCALED) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) cs[e] = 1.0f;
+    if (a.cs && n > 0) ep_get8((const uint8_t*)a.cs, TG_F32, col, n, cs);
+  }
   // dZ may be dY or Z: each element is read by the thread that writes it, before it does
   ep_with_act(a.act, [&](auto act) {
     constexpr int ACT = decltype(act)::value;
@@ -75,6 +81,11 @@ __global__ __launch_bounds__(8 * RL) void act_grad(ActGradArgs a) {
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e) sum[e] += dy[e];
+          if constexpr (SCALED) {
+            const float rs = a.rs ? a.rs[r + RL * k] : 1.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dy[e] = dy[e] * rs * cs[e];
+          }
           if (a.dZ) ep_store8_16(a.dZ, (int64_t)(r + RL * k) * a.N + col, n, ep_pack8(a.t, dy));
         }
     }
@@ -128,8 +139,14 @@ hipError_t launch_ep_join(const EpArgs& g, hipStream_t s) {
 hipError_t launch_act_grad(const ActGradArgs& a, int groups, hipStream_t s) {
   // columns over x, and z where x would pass its threads; rows over y
   const dim3 cols = wide_grid(((int64_t)a.N + 63) / 64), grid(cols.x, (unsigned)groups, cols.y);
-  if (groups == 1) hipLaunchKernelGGL((act_grad<128, 2>), grid, dim3(1024), 0, s, a);
-  else hipLaunchKernelGGL((act_grad<32, 4>), grid, dim3(256), 0, s, a);
+  const bool scaled = a.rs || a.cs;
+  if (groups == 1) {
+    if (scaled) hipLaunchKernelGGL((act_grad<128, 2, true>), grid, dim3(1024), 0, s, a);
+    else hipLaunchKernelGGL((act_grad<128, 2, false>), grid, dim3(1024), 0, s, a);
+  } else {
+    if (scaled) hipLaunchKernelGGL((act_grad<32, 4, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((act_grad<32, 4, false>), grid, dim3(256), 0, s, a);
+  }
   return hipGetLastError();
 }
 

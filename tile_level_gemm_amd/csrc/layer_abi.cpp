@@ -363,6 +363,15 @@ int tile_gemm_ep_bwd(const void* dY, const void* Z, const void* A, const void* B
                      void* dB, float* dbias, int64_t M, int64_t N, int64_t K, int64_t ld_dy, int64_t ld_z,
                      int64_t lda, int64_t ldb, int transA, int transB, int dtype, int act, void* workspace,
                      int64_t workspace_bytes, void* stream) {
+  return tile_gemm_ep_bwd_scaled(dY, Z, A, B, nullptr, nullptr, dZ, dA, dB, dbias, M, N, K, ld_dy, ld_z, lda, ldb,
+                                 transA, transB, dtype, act, workspace, workspace_bytes, stream);
+}
+
+int tile_gemm_ep_bwd_scaled(const void* dY, const void* Z, const void* A, const void* B, const float* row_scale,
+                            const float* col_scale, void* dZ, void* dA, void* dB, float* dbias, int64_t M,
+                            int64_t N, int64_t K, int64_t ld_dy, int64_t ld_z, int64_t lda, int64_t ldb,
+                            int transA, int transB, int dtype, int act, void* workspace, int64_t workspace_bytes,
+                            void* stream) {
   clear_error();
   int st = check_extents(M, N, K);
   if (st) return st;
@@ -374,21 +383,24 @@ int tile_gemm_ep_bwd(const void* dY, const void* Z, const void* A, const void* B
       (st = resolve_ld("lda", &lda, transA ? M : K)) || (st = resolve_ld("ldb", &ldb, transB ? K : N)))
     return st;
   if ((st = check_workspace(workspace, workspace_bytes))) return st;
-  const bool outs = M > 0 && N > 0;
+  const bool outs = M > 0 && N > 0, scaled = row_scale || col_scale;
   if (outs && !dY) return fail(TG_E_NULL, "dY is NULL");
   if (outs && act != TG_ACT_NONE && (!Z || !dZ)) return fail(TG_E_NULL, "an activation's gradient needs Z and dZ");
+  if (outs && scaled && !dZ) return fail(TG_E_NULL, "a scaled product's gradient needs dZ");
   if ((dA && outs && K > 0 && !B) || (dB && outs && K > 0 && !A))
     return fail(TG_E_NULL, "dA needs B, dB needs A");
   const void* all2[] = {dY, Z, A, B, dZ, dA, dB};
   for (const void* p : all2)
     if (misaligned(p, 2)) return fail(TG_E_ALIGN, "a pointer is not aligned to its element");
-  if (misaligned(dbias, 4)) return fail(TG_E_ALIGN, "dbias must be 4-byte aligned");
+  if (misaligned(dbias, 4) || misaligned(row_scale, 4) || misaligned(col_scale, 4))
+    return fail(TG_E_ALIGN, "dbias, row_scale and col_scale must be 4-byte aligned");
   const Mat my = mat(dY, M, N, ld_dy, 2), mz = mat(act != TG_ACT_NONE ? Z : nullptr, M, N, ld_z, 2);
   const Mat ma = mat(dB ? A : nullptr, transA ? K : M, transA ? M : K, lda, 2);
   const Mat mb = mat(dA ? B : nullptr, transB ? N : K, transB ? K : N, ldb, 2);
   const Mat mdz = mat(dZ, M, N, N, 2), mda = mat(dA, 1, M * K, M * K, 2), mdb = mat(dB, 1, K * N, K * N, 2);
   const Mat mbias = vec(dbias, N, 4), mw = vec(workspace, workspace_bytes, 1);
-  const Mat ins[] = {my, mz, ma, mb}, results[] = {mda, mdb, mbias, mw};
+  const Mat mrs = vec(row_scale, M, 4), mcs = vec(col_scale, N, 4);
+  const Mat ins[] = {my, mz, ma, mb, mrs, mcs}, results[] = {mda, mdb, mbias, mw};
   for (const Mat& o : results) {
     for (const Mat& in : ins)
       if (overlaps(o, in)) return fail(TG_E_ALIAS, "an output or the workspace overlaps an input");
@@ -398,7 +410,7 @@ int tile_gemm_ep_bwd(const void* dY, const void* Z, const void* A, const void* B
     for (int j = i + 1; j < 4; ++j)
       if (overlaps(results[i], results[j])) return fail(TG_E_ALIAS, "outputs and the workspace must not overlap");
   if ((overlaps(mdz, my) && !same(mdz, my)) || (overlaps(mdz, mz) && !same(mdz, mz)) || overlaps(mdz, ma) ||
-      overlaps(mdz, mb))
+      overlaps(mdz, mb) || overlaps(mdz, mrs) || overlaps(mdz, mcs))
     return fail(TG_E_ALIAS, "dZ overlaps an input without being exactly dY or Z");
 
   // both products are planned before anything is launched
@@ -432,7 +444,9 @@ int tile_gemm_ep_bwd(const void* dY, const void* Z, const void* A, const void* B
     a.dY = (const uint8_t*)dY;
     a.Z = (const uint8_t*)Z;
     // an unchanged dZ = dY in place is not rewritten
-    a.dZ = dZ == dY && act == TG_ACT_NONE ? nullptr : (uint8_t*)dZ;
+    a.dZ = dZ == dY && act == TG_ACT_NONE && !scaled ? nullptr : (uint8_t*)dZ;
+    a.rs = row_scale;
+    a.cs = col_scale;
     a.ldy = ld_dy;
     a.ldz = ld_z;
     a.M = (int32_t)M;

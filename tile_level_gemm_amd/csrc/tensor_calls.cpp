@@ -215,10 +215,10 @@ PyObject* gemm_ep(PyObject* const* a) {
   return Py_BuildValue("(NN)", wrap(out), wrap(Z));
 }
 
-// dY, A, B, Z, act, trans_a, trans_b, need_dA, need_dB, need_dbias
+// dY, A, B, Z, act, trans_a, trans_b, need_dA, need_dB, need_dbias, row_scale, col_scale
 PyObject* gemm_ep_backward(PyObject* const* a) {
   const Tensor &dY = *tensor("dY", a[0]), &A = *tensor("A", a[1]), &B = *tensor("B", a[2]);
-  const Tensor* Z = tensor("Z", a[3], true);
+  const Tensor *Z = tensor("Z", a[3], true), *rs = tensor("row_scale", a[10], true), *cs = tensor("col_scale", a[11], true);
   const int act = (int)integer(a[4]);
   const bool ta = truth(a[5]), tb = truth(a[6]);
   const Extents e = extents(A, B, ta, tb);
@@ -230,17 +230,20 @@ PyObject* gemm_ep_backward(PyObject* const* a) {
   if (act == TG_ACT_NONE) Z = nullptr;
   else if (!Z) refuse(TG_E_NULL, "an activation's gradient needs Z");
   else ldz = matrix("Z", *Z, e.M, e.N, st);
-  const at::Device dev = one_gpu({&dY, &A, &B, Z});
+  if (rs) f32_vector("row_scale", *rs, e.M);
+  if (cs) f32_vector("col_scale", *cs, e.N);
+  const at::Device dev = one_gpu({&dY, &A, &B, Z, rs, cs});
   Tensor dZ, dA, dB, dbias, ws;
-  if (act != TG_ACT_NONE) dZ = make({e.M, e.N}, st, dev);
+  if (act != TG_ACT_NONE || rs || cs) dZ = make({e.M, e.N}, st, dev);
   if (truth(a[7])) dA = make(A.sizes(), st, dev);
   if (truth(a[8])) dB = make(B.sizes(), st, dev);
   if (truth(a[9])) dbias = make({e.N}, at::kFloat, dev);
   const int64_t nb = tile_gemm_ep_bwd_workspace(e.M, e.N, e.K, ta, tb, t);
   if (nb) ws = make({nb}, at::kByte, dev);
-  check(tile_gemm_ep_bwd(address(&dY), address(Z), address(&A), address(&B), address(dZ), address(dA), address(dB),
-                         (float*)address(dbias), e.M, e.N, e.K, ldy, ldz, e.lda, e.ldb, ta, tb, t, act, address(ws),
-                         nb, stream_of(dev)));
+  check(tile_gemm_ep_bwd_scaled(address(&dY), address(Z), address(&A), address(&B), (const float*)address(rs),
+                                (const float*)address(cs), address(dZ), address(dA), address(dB),
+                                (float*)address(dbias), e.M, e.N, e.K, ldy, ldz, e.lda, e.ldb, ta, tb, t, act,
+                                address(ws), nb, stream_of(dev)));
   PyObject* z;
   if (dZ.defined()) {
     z = wrap(dZ);
@@ -343,7 +346,7 @@ PyObject* set_error_class(PyObject*, PyObject* c) {
 }
 
 #define TG_METHOD(f, n) {#f, (PyCFunction)(void (*)(void))(entry<f, n>), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {TG_METHOD(gemm_ep, 12), TG_METHOD(gemm_ep_backward, 10), TG_METHOD(rms_norm, 7),
+PyMethodDef methods[] = {TG_METHOD(gemm_ep, 12), TG_METHOD(gemm_ep_backward, 12), TG_METHOD(rms_norm, 7),
                          TG_METHOD(rms_norm_backward, 6),
                          {"set_error_class", set_error_class, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
