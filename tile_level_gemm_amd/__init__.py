@@ -541,9 +541,10 @@ def _room(t):
     return (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
 
 
-def _ptr(name, x, esize, nbytes, dev):
-    """Address of a tensor argument after the checks of _checked; a view may have gaps (its leading
-    dimension says so).  Returns (address, device)."""
+def _ptr(name, x, esize, nbytes, dev, ld):
+    """Address of a tensor argument after the checks of _checked.  The library sees an address and, for a
+    matrix, a leading dimension `ld` (None: packed): a view with gaps has to have those very rows.
+    Returns (address, device)."""
     if x is None or isinstance(x, int):
         return x, dev
     if not isinstance(x, torch.Tensor):
@@ -557,16 +558,36 @@ def _ptr(name, x, esize, nbytes, dev):
                                     f"{esize}-byte elements")
     if _room(x) < nbytes:
         raise TileError(TG_E_SHAPE, f"{name} holds {_room(x)} bytes, the sizes need {nbytes}")
+    if x.numel() and not x.is_contiguous():
+        if ld is None:
+            raise TileError(TG_E_LAYOUT, f"{name} must be contiguous, its strides are {tuple(x.stride())}")
+        if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1) or (x.shape[0] > 1 and x.stride(0) != ld):
+            raise TileError(TG_E_LAYOUT, f"{name} has strides {tuple(x.stride())}, its rows are read {ld} elements apart")
     return x.data_ptr() or None, x.device
 
 
 def _ptrs(*args):
-    """Addresses of several tensor arguments: (name, value, element bytes or None, bytes)."""
+    """Addresses of several tensor arguments: (name, value, element bytes or None, bytes) of packed ones,
+    and the leading dimension behind them of matrices."""
     dev, out = None, []
-    for name, x, esize, nbytes in args:
-        p, dev = _ptr(name, x, esize, nbytes, dev)
+    for name, x, esize, nbytes, *ld in args:
+        p, dev = _ptr(name, x, esize, nbytes, dev, ld[0] if ld else None)
         out.append(p)
     return out
+
+
+def _matrix(name, x, rows, cols, ld, esize):
+    """_ptrs argument of a matrix with leading dimension `ld` (0: packed)."""
+    return name, x, esize, _span(rows, cols, ld, esize), int(ld) or int(cols)
+
+
+def _workspace_bytes(workspace, nbytes):
+    """Size of a workspace: all of a tensor unless the caller says less."""
+    if workspace is not None and nbytes is None:
+        if not isinstance(workspace, torch.Tensor):
+            raise TileError(TG_E_ARG, "a workspace given by address needs workspace_bytes")
+        nbytes = _room(workspace)
+    return int(nbytes or 0)
 
 
 def _ep_args(A, B, D, M, N, K, lda, ldb, ldd, transA, transB, a_dtype, b_dtype, d_dtype, bias, bias_dtype,
@@ -574,17 +595,13 @@ def _ep_args(A, B, D, M, N, K, lda, ldb, ldd, transA, transB, a_dtype, b_dtype, 
     ea, eb, ed = ELEM_BYTES.get(int(a_dtype), 1), ELEM_BYTES.get(int(b_dtype), 1), ELEM_BYTES.get(int(d_dtype), 1)
     if bias_dtype is None:
         bias_dtype = TORCH_DTYPES.get(bias.dtype, 0) if isinstance(bias, torch.Tensor) else 0
-    if workspace is not None and workspace_bytes is None:
-        if not isinstance(workspace, torch.Tensor):
-            raise TileError(TG_E_ARG, "a workspace given by address needs workspace_bytes")
-        workspace_bytes = _room(workspace)
-    nb = int(workspace_bytes or 0)
+    ebias, nb = ELEM_BYTES.get(int(bias_dtype)), _workspace_bytes(workspace, workspace_bytes)
     pa, pb, pd, pbias, pres, pz, prs, pcs, pws = _ptrs(
-        ("A", A, ea, _span(K if transA else M, M if transA else K, lda, ea)),
-        ("B", B, eb, _span(N if transB else K, K if transB else N, ldb, eb)),
-        ("D", D, ed, _span(M, N, ldd, ed)),
-        ("bias", bias, None, max(int(N), 0) * ELEM_BYTES.get(int(bias_dtype), 1)),
-        ("residual", residual, ed, _span(M, N, ld_residual, ed)), ("Z", Z, ed, _span(M, N, ld_z, ed)),
+        _matrix("A", A, K if transA else M, M if transA else K, lda, ea),
+        _matrix("B", B, N if transB else K, K if transB else N, ldb, eb),
+        _matrix("D", D, M, N, ldd, ed),
+        ("bias", bias, ebias, max(int(N), 0) * (ebias or 1)),
+        _matrix("residual", residual, M, N, ld_residual, ed), _matrix("Z", Z, M, N, ld_z, ed),
         ("row_scale", row_scale, 4, max(int(M), 0) * 4), ("col_scale", col_scale, 4, max(int(N), 0) * 4),
         ("workspace", workspace, None, nb))
     ep = Epilogue(pbias, pres, pz, prs, pcs, int(ld_residual), int(ld_z), int(bias_dtype), int(act))
@@ -624,12 +641,10 @@ def tile_gemm_ep_bwd(dY, Z, A, B, dZ, dA, dB, dbias, M, N, K, transA, transB, dt
     """Gradients of tile_gemm_ep for 16-bit operands, scaled or not (see include/tilegemm.h)."""
     e = ELEM_BYTES.get(int(dtype), 1)
     m, n, k = max(int(M), 0), max(int(N), 0), max(int(K), 0)
-    if workspace is not None and workspace_bytes is None:
-        workspace_bytes = _room(workspace)
-    nb = int(workspace_bytes or 0)
-    p = _ptrs(("dY", dY, e, _span(m, n, ld_dy, e)), ("Z", Z, e, _span(m, n, ld_z, e)),
-              ("A", A, e, _span(k if transA else m, m if transA else k, lda, e)),
-              ("B", B, e, _span(n if transB else k, k if transB else n, ldb, e)),
+    nb = _workspace_bytes(workspace, workspace_bytes)
+    p = _ptrs(_matrix("dY", dY, m, n, ld_dy, e), _matrix("Z", Z, m, n, ld_z, e),
+              _matrix("A", A, k if transA else m, m if transA else k, lda, e),
+              _matrix("B", B, n if transB else k, k if transB else n, ldb, e),
               ("dZ", dZ, e, m * n * e), ("dA", dA, e, m * k * e), ("dB", dB, e, k * n * e),
               ("dbias", dbias, 4, n * 4), ("workspace", workspace, None, nb), ("row_scale", row_scale, 4, m * 4),
               ("col_scale", col_scale, 4, n * 4))
@@ -651,8 +666,8 @@ def tile_rmsnorm(X, R, W, H, Y, S, rstd, rows, cols, eps, dtype, w_dtype, y_dtyp
     e, ew, ey = ELEM_BYTES.get(int(dtype), 1), ELEM_BYTES.get(int(w_dtype), 1), ELEM_BYTES.get(int(y_dtype), 1)
     m, n = max(int(rows), 0), max(int(cols), 0)
     sb = m * 4 if int(scale_kind) == TG_SCALE_ROW else m * (n // 32) if int(scale_kind) == TG_SCALE_BLOCK else 0
-    p = _ptrs(("X", X, e, _span(m, n, ld_x, e)), ("R", R, e, _span(m, n, ld_r, e)), ("W", W, ew, n * ew),
-              ("H", H, e, _span(m, n, ld_h, e)), ("Y", Y, ey, _span(m, n, ld_y, ey)), ("S", S, None, sb),
+    p = _ptrs(_matrix("X", X, m, n, ld_x, e), _matrix("R", R, m, n, ld_r, e), ("W", W, ew, n * ew),
+              _matrix("H", H, m, n, ld_h, e), _matrix("Y", Y, m, n, ld_y, ey), ("S", S, None, sb),
               ("rstd", rstd, 4, m * 4))
     _check(lib().tile_rmsnorm(*p, rows, cols, int(ld_x), int(ld_r), int(ld_h), int(ld_y), float(eps),
                               int(dtype), int(w_dtype), int(y_dtype), int(scale_kind), _stream(stream)))
@@ -663,12 +678,10 @@ def tile_rmsnorm_bwd(dY, H, W, rstd, dH, dX, dW, rows, cols, dtype, w_dtype, *, 
     """Gradients of tile_rmsnorm (see include/tilegemm.h)."""
     e, ew = ELEM_BYTES.get(int(dtype), 1), ELEM_BYTES.get(int(w_dtype), 1)
     m, n = max(int(rows), 0), max(int(cols), 0)
-    if workspace is not None and workspace_bytes is None:
-        workspace_bytes = _room(workspace)
-    nb = int(workspace_bytes or 0)
-    p = _ptrs(("dY", dY, e, _span(m, n, ld_dy, e)), ("H", H, e, _span(m, n, ld_h, e)), ("W", W, ew, n * ew),
-              ("rstd", rstd, 4, m * 4), ("dH", dH, e, _span(m, n, ld_dh, e)),
-              ("dX", dX, e, _span(m, n, ld_dx, e)), ("dW", dW, 4, n * 4), ("workspace", workspace, None, nb))
+    nb = _workspace_bytes(workspace, workspace_bytes)
+    p = _ptrs(_matrix("dY", dY, m, n, ld_dy, e), _matrix("H", H, m, n, ld_h, e), ("W", W, ew, n * ew),
+              ("rstd", rstd, 4, m * 4), _matrix("dH", dH, m, n, ld_dh, e), _matrix("dX", dX, m, n, ld_dx, e),
+              ("dW", dW, 4, n * 4), ("workspace", workspace, None, nb))
     _check(lib().tile_rmsnorm_bwd(*p[:7], rows, cols, int(ld_dy), int(ld_h), int(ld_dh), int(ld_dx),
                                   int(dtype), int(w_dtype), p[7], nb, _stream(stream)))
 
