@@ -521,7 +521,9 @@ def tile_gemm_atom_select(M, N, K, dtype, transA, transB):
 # The tile_* functions take the C ABI's arguments (leading dimensions given, so operands may be
 # slices of wider tensors); gemm_ep, gemm_ep_backward, rms_norm and rms_norm_backward take
 # tensors, allocate the results and the workspace on the call's stream and are what a model calls:
-# their checks and allocations are native (csrc/tensor_calls.cpp).
+# their checks and allocations are native (csrc/tensor_calls.cpp).  Their results carry no autograd
+# history: the backward calls give the gradients.  An input that requires one gets a warning while
+# gradients are recorded, and tensors they write (out, h_out) count as changed.
 
 ACTS = {"none": TG_ACT_NONE, "relu": TG_ACT_RELU, "gelu": TG_ACT_GELU,
         "gelu_tanh": TG_ACT_GELU_TANH, "silu": TG_ACT_SILU}

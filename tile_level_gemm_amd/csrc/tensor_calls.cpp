@@ -8,6 +8,7 @@
 // Positional arguments only: the documented functions with their defaults are in __init__.py.
 #include <Python.h>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
@@ -124,6 +125,22 @@ PyObject* wrap(const Tensor& t) {
   return THPVariable_Wrap(t);
 }
 
+// A tensor of the caller's that the call writes: autograd sees that saved tensors have changed.
+void written(const Tensor* t) {
+  if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+// The results carry no history (the backward calls give the gradients): said once where a gradient would
+// be lost without a word.
+void no_history(const char* call, std::initializer_list<const Tensor*> inputs) {
+  if (!at::GradMode::is_enabled()) return;
+  for (const Tensor* t : inputs)
+    if (t && t->requires_grad()) {
+      TORCH_WARN_ONCE(call, ": an input requires a gradient, but results of the layer operators carry no autograd "
+                      "history; use gemm_ep_backward and rms_norm_backward (and torch.no_grad() around the calls)");
+      return;
+    }
+}
+
 void check(int status) {
   if (status != TG_OK) refuse(status, tile_last_error());
 }
@@ -207,6 +224,8 @@ PyObject* gemm_ep(PyObject* const* a) {
   if (nb) ws = make({nb}, at::kByte, dev);
   check(tile_gemm_ep(address(&A), address(&B), address(out), e.M, e.N, e.K, e.lda, e.ldb, ldd, ta, tb, at, bt, dt,
                      &ep, address(ws), nb, stream_of(dev)));
+  written(given);
+  no_history("gemm_ep", {&A, &B, bias, res, rs, cs});
   if (given && !keep_z) {
     Py_INCREF(a[11]);
     return a[11];
@@ -284,6 +303,8 @@ PyObject* rms_norm(PyObject* const* a) {
   check(tile_rmsnorm(address(&X), address(res), address(&W), address(h), address(y), address(S),
                      (float*)address(rstd), rows, cols, ldx, ldr, ldh, 0, (float)eps, t, code_of(W.scalar_type()), yt,
                      kind, stream_of(dev)));
+  written(given);
+  no_history("rms_norm", {&X, &W, res});
   PyObject* ph;
   if (given || !res) {
     ph = given ? a[6] : a[0];
