@@ -524,7 +524,8 @@ int tile_gemm_atom_select(int64_t M, int64_t N, int64_t K, int dtype, int transA
  * activation and residual in its epilogue, its backward pass, the root-mean-square norm with
  * the residual's addition (16-bit result, or 8 bits with scales for the products above and
  * below) and its backward pass.  Conventions as for every entry point; in addition:
- *   - leading dimensions count elements, 0 means packed; at least the row length, at most 2^40;
+ *   - leading dimensions count elements, 0 means packed; at least the row length, at most 2^40, and at
+ *     most 2^60 elements over all rows;
  *   - pointers need only their element's alignment (16-byte aligned operands whose rows are
  *     multiples of 16 bytes take the faster loads);
  *   - outputs must not overlap inputs or each other except where a line below allows exactly the

@@ -46,3 +46,25 @@ def test_the_join_alone_covers_any_extent():
     with pytest.raises(tg.TileError) as e:
         plan(1 << 21, 1 << 21, 0)
     assert e.value.status == tg.TG_E_SHAPE
+
+
+@pytest.mark.parametrize("K", [(1 << 23) - 512, (1 << 23) + 1, 1 << 30])
+def test_matrices_past_any_address_space_are_refused(K):
+    # K rows 2^41 bytes apart: 64-bit spans wrap (K + 512 = 2^23 rows: to nothing)
+    with pytest.raises(tg.TileError) as e:
+        tg.tile_gemm_ep_plan(A, B, D, 64, 64, K, 1, 1, BF, BF, BF, lda=1 << 40)
+    assert e.value.status == tg.TG_E_LAYOUT and "lda" in e.value.reason
+
+
+def test_rows_past_any_address_space_are_refused_everywhere():
+    L, far, rows = tg.lib(), 1 << 40, 1 << 29
+    S, W, R = (1 << 44) * 4, (1 << 44) * 5, (1 << 44) * 6
+    for ld in ((far, 0, 0, 0), (0, far, 0, 0), (0, 0, far, 0), (0, 0, 0, far)):
+        assert L.tile_rmsnorm(A, B, W, R, D, None, S, rows, 8, *ld, 1e-5, BF, BF, BF, 0, None) == tg.TG_E_LAYOUT
+        assert L.tile_rmsnorm_bwd(A, B, W, S, R, D, None, rows, 8, *ld, BF, BF, None, 0, None) == tg.TG_E_LAYOUT
+        if ld[3] == 0:   # B has 8 rows only
+            assert L.tile_gemm_ep_bwd(A, B, W, R, D, None, None, S, rows, 8, 8, *ld, 0, 0, BF, 1, None, 0, None) == tg.TG_E_LAYOUT
+    for kw in (dict(ldd=far), dict(residual=R, ld_residual=far), dict(Z=R, ld_z=far)):
+        with pytest.raises(tg.TileError) as e:
+            tg.tile_gemm_ep_plan(A, B, D, rows, 64, 64, 0, 1, BF, BF, BF, **kw)
+        assert e.value.status == tg.TG_E_LAYOUT

@@ -15,6 +15,7 @@ namespace {
 
 const int64_t kMaxDim = (int64_t)1 << 30;
 const int64_t kMaxLd = (int64_t)1 << 40;
+const int64_t kMaxSpan = (int64_t)1 << 60;      // elements from a matrix's first row to its last
 const int64_t kDirectSpan = (int64_t)1 << 31;   // buffer offsets of the direct loads stay below
 
 std::string fmt(const char* f, long long a = 0, long long b = 0, long long c = 0) {
@@ -52,11 +53,13 @@ bool overlaps(const Mat& a, const Mat& b) {
 }
 bool same(const Mat& a, const Mat& b) { return a.p == b.p && a.pitch == b.pitch; }
 
-// ld 0 = packed; must cover the row
-int resolve_ld(const char* name, int64_t* ld, int64_t cols) {
+// ld 0 = packed; must cover the row, and the rows must lie in an address space: byte spans stay below 2^63
+int resolve_ld(const char* name, int64_t* ld, int64_t cols, int64_t rows) {
   if (*ld == 0) *ld = std::max<int64_t>(cols, 1);
   if (*ld < cols || *ld > kMaxLd)
     return fail(TG_E_LAYOUT, std::string(name) + fmt(" %lld must be 0 (packed) or %lld .. 2^40", *ld, cols));
+  if (rows > kMaxSpan / *ld)
+    return fail(TG_E_LAYOUT, std::string(name) + fmt(" %lld puts %lld rows past any address space", *ld, rows));
   return TG_OK;
 }
 bool misaligned(const void* p, int eb) { return (uintptr_t)p % (uintptr_t)eb != 0; }
@@ -195,9 +198,10 @@ int plan_ep(const void* A, const void* B, const void* D, int64_t M, int64_t N, i
   if (is8(a_dtype) && (transA || !transB))
     return fail(TG_E_LAYOUT, "fp8 operands are stored A [M,K], B [N,K] (transA 0, transB 1)");
   int64_t ldr = ep->ld_residual, ldz = ep->ld_z;
-  if ((st = resolve_ld("lda", &lda, transA ? M : K)) || (st = resolve_ld("ldb", &ldb, transB ? K : N)) ||
-      (st = resolve_ld("ldd", &ldd, N)) || (ep->residual && (st = resolve_ld("ld_residual", &ldr, N))) ||
-      (ep->Z && (st = resolve_ld("ld_z", &ldz, N))))
+  if ((st = resolve_ld("lda", &lda, transA ? M : K, transA ? K : M)) ||
+      (st = resolve_ld("ldb", &ldb, transB ? K : N, transB ? N : K)) ||
+      (st = resolve_ld("ldd", &ldd, N, M)) || (ep->residual && (st = resolve_ld("ld_residual", &ldr, N, M))) ||
+      (ep->Z && (st = resolve_ld("ld_z", &ldz, N, M))))
     return st;
   if ((st = check_workspace(ws, ws_bytes))) return st;
   *plan = tg_ep_plan{};
@@ -379,8 +383,9 @@ int tile_gemm_ep_bwd_scaled(const void* dY, const void* Z, const void* A, const 
   if (transA != 0 && transA != 1) return fail(TG_E_ARG, "transA must be 0 or 1");
   if (transB != 0 && transB != 1) return fail(TG_E_ARG, "transB must be 0 or 1");
   if (act < TG_ACT_NONE || act > TG_ACT_SILU) return fail(TG_E_ARG, fmt("unknown activation %lld", act));
-  if ((st = resolve_ld("ld_dy", &ld_dy, N)) || (st = resolve_ld("ld_z", &ld_z, N)) ||
-      (st = resolve_ld("lda", &lda, transA ? M : K)) || (st = resolve_ld("ldb", &ldb, transB ? K : N)))
+  if ((st = resolve_ld("ld_dy", &ld_dy, N, M)) || (st = resolve_ld("ld_z", &ld_z, N, M)) ||
+      (st = resolve_ld("lda", &lda, transA ? M : K, transA ? K : M)) ||
+      (st = resolve_ld("ldb", &ldb, transB ? K : N, transB ? N : K)))
     return st;
   if ((st = check_workspace(workspace, workspace_bytes))) return st;
   const bool outs = M > 0 && N > 0, scaled = row_scale || col_scale;
@@ -485,8 +490,8 @@ int tile_rmsnorm(const void* X, const void* R, const void* W, void* H, void* Y, 
   if (!(eps >= 0.0f) || std::isinf(eps)) return fail(TG_E_ARG, "eps must be finite and not negative");
   if (H && !R) return fail(TG_E_ARG, "H is the sum X + R: it needs R");
   int st;
-  if ((st = resolve_ld("ld_x", &ld_x, cols)) || (st = resolve_ld("ld_r", &ld_r, cols)) ||
-      (st = resolve_ld("ld_h", &ld_h, cols)) || (st = resolve_ld("ld_y", &ld_y, cols)))
+  if ((st = resolve_ld("ld_x", &ld_x, cols, rows)) || (st = resolve_ld("ld_r", &ld_r, cols, rows)) ||
+      (st = resolve_ld("ld_h", &ld_h, cols, rows)) || (st = resolve_ld("ld_y", &ld_y, cols, rows)))
     return st;
   if (rows == 0) return TG_OK;
   if (!X || !W || !Y) return fail(TG_E_NULL, "X, W or Y is NULL");
@@ -545,8 +550,8 @@ int tile_rmsnorm_bwd(const void* dY, const void* H, const void* W, const float* 
   if (!is_float(dtype)) return fail(TG_E_DTYPE, fmt("dtype must be TG_F16, TG_BF16 or TG_F32 (got %lld)", dtype));
   if (w_dtype != dtype && w_dtype != TG_F32) return fail(TG_E_DTYPE, "w_dtype must be dtype or TG_F32");
   int st;
-  if ((st = resolve_ld("ld_dy", &ld_dy, cols)) || (st = resolve_ld("ld_h", &ld_h, cols)) ||
-      (st = resolve_ld("ld_dh", &ld_dh, cols)) || (st = resolve_ld("ld_dx", &ld_dx, cols)))
+  if ((st = resolve_ld("ld_dy", &ld_dy, cols, rows)) || (st = resolve_ld("ld_h", &ld_h, cols, rows)) ||
+      (st = resolve_ld("ld_dh", &ld_dh, cols, rows)) || (st = resolve_ld("ld_dx", &ld_dx, cols, rows)))
     return st;
   if ((st = check_workspace(workspace, workspace_bytes))) return st;
   hipStream_t s = (hipStream_t)stream;
