@@ -37,7 +37,7 @@ struct EpArgs {
 };
 
 // Kernel families of tile_gemm_ep (tg_ep_plan.kernel).
-struct EpKernel {   // block kernels: block size 64 (staged and ring), 128 or 256 (direct)
+struct EpKernel {   // block kernels: block size 64 or 128 (staged, ring), 128 or 256 (direct)
   int bs;
   bool staged, ring;
 };

@@ -513,8 +513,8 @@ __global__ __launch_bounds__(ep_threads(BS)) void gemm_ep_ring(EpArgs g) {
   ep_store<BS, WN, TM, TN>(g, t, acc, wave, lane, wm, wn, s0, s1, s2, s3);
 }
 
-// Operands through registers, D stages ahead of the one computed: four on 64-wide blocks (a CU holds one
-// or two and waits for memory), two on 128-wide ones (four would leave one workgroup a CU).
+// Operands through registers, two stages ahead of the one computed: one register set each for the even
+// and the odd stage.
 template <bool A_MN, bool B_MN, int DT, int BS>
 __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_staged(EpArgs g) {
   constexpr int WGM = 2, WGN = ep_threads(BS) / 128;
@@ -557,9 +557,8 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_sta
   const uint8_t* pb = g.B + (B_MN ? (int64_t)t.k0 * g.ldb + t.n0 : (int64_t)t.n0 * g.ldb + t.k0) * E;
   const int ra = g.M - t.m0, rb = g.N - t.n0;   // rows / columns from here to the end
   const int KT = (t.kl + EL::kBK - 1) / EL::kBK;   // >= 1
-  constexpr int D = 2;
-  StagedFetch<A_MN, PER, DT, BS> fa[D];
-  StagedFetch<B_MN, PER, DT, BS> fb[D];
+  StagedFetch<A_MN, PER, DT, BS> fa[2];
+  StagedFetch<B_MN, PER, DT, BS> fb[2];
   auto compute = [&](const uint8_t* xa, const uint8_t* xb) {
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
@@ -599,46 +598,24 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_sta
     };
     constexpr std::integral_constant<int, 0> S0{};
     constexpr std::integral_constant<int, 1> S1{};
-    constexpr std::integral_constant<int, D == 4 ? 2 : 0> S2{};
-    constexpr std::integral_constant<int, D == 4 ? 3 : 1> S3{};
     get(S0, 0);
     get(S1, 1);
-    if constexpr (D == 4) {
-      get(S2, 2);
-      get(S3, 3);
-    }
     put(S0, 0, sa0, sb0);
     __syncthreads();
-    // stage kt from (ca, cb); its registers, set `q`, take stage kt + D, and stage kt + 1, loaded
-    // D - 1 stages ago, goes to (na, nb) after it
+    // stage kt from (ca, cb); its registers, set `q`, take stage kt + 2, and stage kt + 1, loaded a stage
+    // ago, goes to (na, nb) after it
     auto stage = [&](const uint8_t* ca, const uint8_t* cb, uint8_t* na, uint8_t* nb, int kt, auto q, auto next) {
-      get(q, kt + D);
+      get(q, kt + 2);
       compute(ca, cb);
       put(next, kt + 1, na, nb);
       __syncthreads();
     };
     int kt = 0;
-    if constexpr (D == 4) {
-      for (; kt + 4 <= KT; kt += 4) {
-        stage(sa0, sb0, sa1, sb1, kt, S0, S1);
-        stage(sa1, sb1, sa0, sb0, kt + 1, S1, S2);
-        stage(sa0, sb0, sa1, sb1, kt + 2, S2, S3);
-        stage(sa1, sb1, sa0, sb0, kt + 3, S3, S0);
-      }
-      if (kt < KT) {
-        stage(sa0, sb0, sa1, sb1, kt, S0, S1);
-        if (kt + 1 < KT) {
-          stage(sa1, sb1, sa0, sb0, kt + 1, S1, S2);
-          if (kt + 2 < KT) stage(sa0, sb0, sa1, sb1, kt + 2, S2, S3);
-        }
-      }
-    } else {
-      for (; kt + 2 <= KT; kt += 2) {
-        stage(sa0, sb0, sa1, sb1, kt, S0, S1);
-        stage(sa1, sb1, sa0, sb0, kt + 1, S1, S0);
-      }
-      if (kt < KT) stage(sa0, sb0, sa1, sb1, kt, S0, S1);
+    for (; kt + 2 <= KT; kt += 2) {
+      stage(sa0, sb0, sa1, sb1, kt, S0, S1);
+      stage(sa1, sb1, sa0, sb0, kt + 1, S1, S0);
     }
+    if (kt < KT) stage(sa0, sb0, sa1, sb1, kt, S0, S1);
   }
   ep_store<BS, WN, TM, TN>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
 }

@@ -215,8 +215,6 @@ __global__ __launch_bounds__(1024) void gemm_ep_tokens(EpArgs g) {
     s += NB * W;
   };
   while (s + (U - 1) * W < full) batch(std::integral_constant<int, U>{}, F_{});
-  if constexpr (U > 4)
-    if (s + 3 * W < full) batch(std::integral_constant<int, 4>{}, F_{});
   if (s + W < full) batch(std::integral_constant<int, 2>{}, F_{});
   if (s < full) batch(std::integral_constant<int, 1>{}, F_{});
   if (s < T) batch(std::integral_constant<int, 1>{}, T_{});   // the partial step, if it is this wave's

@@ -16,8 +16,9 @@
 // 8192 x 8192 bf16 with dH 100 us and 4 for the sum of dw's shares (5.2 TB/s of 537 MB); one row of
 // 4096 2.9 us, launch and latency.
 // Rows whose length is not a multiple of 8 end in a chunk moved back to the row's last 8
-// columns: every load is a whole vector, the columns another chunk owns (`dup` of them) are left
-// out of the sums, and both owners store the same values.
+// columns: every load is a whole vector, and the columns another chunk owns (`dup` of them) are left
+// out of the sums.  Forward both owners store the same values; backward, where dX may be dH, a moved
+// chunk stores its own columns only.
 #include "ep.h"
 #include "norm.h"
 
