@@ -28,6 +28,7 @@
 
 #include "direct_gemm.h"
 #include "ep.h"
+#include "staged.h"
 
 namespace tg {
 namespace {
@@ -61,47 +62,35 @@ struct StagedFetch {
   static constexpr int E = EL::kBytes, VE = 16 / E;   // elements per chunk
   u32x4 r[PER];
 
-  // instruction i's chunk of a stage: its row (K-major) or k (M/N-major) and its first k or column
-  __device__ __forceinline__ static void where(int i, int stage, int wave, int lane, int& line, int& first) {
+  // instruction i's chunk of a stage
+  __device__ __forceinline__ static StagedPlace where(int i, int stage, int wave, int lane) {
     const uint32_t blk = (uint32_t)(PER * wave + i);
     if constexpr (MN) {
       constexpr uint32_t ROWB = BS * E, CH = ROWB / 16, RPB = 1024 / ROWB;
       const uint32_t k = RPB * blk + (uint32_t)lane / CH;
-      line = stage * EL::kBK + (int)k;
-      first = (int)(((uint32_t)lane % CH) ^ sm_row<SMV, ROWB>(k)) * VE;
+      return staged_place<true>(stage, EL::kBK, VE, (int)k, (int)(((uint32_t)lane % CH) ^ sm_row<SMV, ROWB>(k)));
     } else {
       const uint32_t row = 8u * blk + ((uint32_t)lane >> 3);
-      line = (int)row;
-      first = stage * EL::kBK + (int)(((uint32_t)lane & 7u) ^ sk<SKV>(row)) * VE;
+      return staged_place<false>(stage, EL::kBK, VE, (int)row, (int)(((uint32_t)lane & 7u) ^ sk<SKV>(row)));
     }
   }
   // base: the block's first element at k = 0 of the block's part of K; rows: rows (K-major) or columns
   // (M/N-major) from there to the operand's end; kl: k of this part.
-  // Every load is 16 whole bytes inside the operand, whatever the edge: a chunk that would pass the end
-  // of its line is moved back to the line's last 16 bytes (the line holds as many), a line past the end
-  // repeats the last one.  So the loads of all stages are alike, no branch hides how many are in
-  // flight, and fix() puts the moved chunks right once they are here.
+  // Every load is 16 whole bytes inside the operand (staged.h), so the loads of all stages are alike, no
+  // branch hides how many are in flight, and fix() puts the moved chunks right once they are here.
   __device__ __forceinline__ void get(const uint8_t* base, int64_t ld, int rows, int kl, int stage, int wave,
                                       int lane) {
     const int lines = MN ? kl : rows, width = MN ? rows : kl;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      int line, first;
-      where(i, stage, wave, lane, line, first);
-      r[i] = load16(base + ((int64_t)min(line, lines - 1) * ld + min(first, width - VE)) * E);
-    }
+    for (int i = 0; i < PER; ++i)
+      r[i] = load16(base + staged_offset(where(i, stage, wave, lane), ld, lines, width, VE) * E);
   }
-  // Moved chunks down to their place, zeros for k past the end (a row or column past the end feeds
-  // only outputs that are not stored).
+  // Moved chunks down to their place, zeros for k past the end.
   __device__ __forceinline__ void fix(int rows, int kl, int stage, int wave, int lane) {
     const int width = MN ? rows : kl;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      int line, first;
-      where(i, stage, wave, lane, line, first);
-      const int back = MN && line >= kl ? VE : max(0, first - (width - VE));
-      r[i] = shift_down(r[i], 8u * E * (uint32_t)min(back, VE));
-    }
+    for (int i = 0; i < PER; ++i)
+      r[i] = shift_down(r[i], 8u * E * (uint32_t)staged_back<MN>(where(i, stage, wave, lane), kl, width, VE));
   }
   // Element by element: lines shorter than 16 bytes.
   __device__ __forceinline__ void get_each(const uint8_t* base, int64_t ld, int rows, int kl, int stage, int wave,
@@ -109,10 +98,9 @@ struct StagedFetch {
     const int lines = MN ? kl : rows, width = MN ? rows : kl;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      int line, first;
-      where(i, stage, wave, lane, line, first);
-      const uint8_t* p = base + ((int64_t)line * ld + first) * E;
-      const int n = line < lines ? width - first : 0;
+      const StagedPlace at = where(i, stage, wave, lane);
+      const uint8_t* p = base + ((int64_t)at.line * ld + at.first) * E;
+      const int n = at.line < lines ? width - at.first : 0;
       u32x4 v = {0, 0, 0, 0};
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
