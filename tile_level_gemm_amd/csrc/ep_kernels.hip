@@ -49,7 +49,7 @@ template <int RL, int K, bool SCALED>
 __global__ __launch_bounds__(8 * RL) void act_grad(ActGradArgs a) {
   __shared__ float red[RL][64 + 1];
   const int lane = (int)threadIdx.x & 7, rl = (int)threadIdx.x >> 3;
-  const int first = ((int)blockIdx.z * (int)gridDim.x + (int)blockIdx.x) * 64;   // of the workgroup's columns
+  const int first = ((int)blockIdx.z * kWideRow + (int)blockIdx.x) * 64;   // of the workgroup's columns
   const int col = first + lane * 8, n = a.N - col;
   const int r0 = (int)blockIdx.y * a.rows_per, r1 = min(a.M, r0 + a.rows_per);
   float sum[8] = {}, cs[8];
@@ -137,7 +137,7 @@ hipError_t launch_ep_join(const EpArgs& g, hipStream_t s) {
 }
 
 hipError_t launch_act_grad(const ActGradArgs& a, int groups, hipStream_t s) {
-  // columns over x, and z where x would pass its threads; rows over y
+  // columns over x and z, rows over y
   const dim3 cols = wide_grid(((int64_t)a.N + 63) / 64), grid(cols.x, (unsigned)groups, cols.y);
   const bool scaled = a.rs || a.cs;
   if (groups == 1) {

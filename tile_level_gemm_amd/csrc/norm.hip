@@ -19,6 +19,8 @@
 // columns: every load is a whole vector, and the columns another chunk owns (`dup` of them) are left
 // out of the sums.  Forward both owners store the same values; backward, where dX may be dH, a moved
 // chunk stores its own columns only.
+#include <algorithm>
+
 #include "ep.h"
 #include "norm.h"
 
@@ -126,8 +128,8 @@ __global__ __launch_bounds__(MAXT) void rmsnorm(NormArgs a) {
   __shared__ float red[WAVE ? 1 : kMaxWaves][2];
   const int TPR = WAVE ? 64 : (int)blockDim.x;
   const int t = WAVE ? (int)threadIdx.x & 63 : (int)threadIdx.x;
-  const int64_t row = WAVE ? wide_block() * 4 + (threadIdx.x >> 6) : wide_block();
-  if (row >= a.rows) return;
+  const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
+  if (WAVE && row >= a.rows) return;
   const int cols = (int)a.cols;
   float h[NV][8], w[NV][8];
 #pragma unroll
@@ -218,8 +220,7 @@ __global__ __launch_bounds__(MAXT) void rmsnorm(NormArgs a) {
 template <int DT, int SC>
 __global__ __launch_bounds__(1024) void rmsnorm_long(NormArgs a) {
   __shared__ float red[16][2];
-  const int64_t row = wide_block();
-  if (row >= a.rows) return;
+  const int64_t row = blockIdx.x;
   auto get = [&](int64_t col, int n, float (&h)[8], float (&w)[8]) {
     ep_get8(a.X, DT, row * a.ldx + col, n, h);
     if (a.R) {
@@ -437,8 +438,7 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_bwd(NormBwdArgs a) {
 template <int DT>
 __global__ __launch_bounds__(1024) void rmsnorm_bwd_dot(NormBwdArgs a) {
   __shared__ float red[16][2];
-  const int64_t row = wide_block();
-  if (row >= a.rows) return;
+  const int64_t row = blockIdx.x;
   const float rstd = a.rstd[row];
   float dot = 0.0f, none = 0.0f;
   for (int64_t col = (int64_t)threadIdx.x * 8; col < a.cols; col += 8192) {
@@ -454,11 +454,12 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_dot(NormBwdArgs a) {
   row_reduce<false>(dot, none, false, red);
   if (threadIdx.x == 0) a.dot[row] = dot / (float)a.cols;
 }
-// ... then dX and dw by panels of 2048 columns (blockIdx.y, and z past 2^15 of them), rows shared over
+// ... then dX and dw by panels of 2048 columns (blockIdx.y, and z past kPanels of them), rows shared over
 // blockIdx.x.
+constexpr int kPanels = 1 << 15;
 template <int DT>
 __global__ __launch_bounds__(256) void rmsnorm_bwd_panel(NormBwdArgs a) {
-  const int64_t col = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * 2048 + threadIdx.x * 8;
+  const int64_t col = ((int64_t)blockIdx.z * kPanels + blockIdx.y) * 2048 + threadIdx.x * 8;
   if (col >= a.cols) return;
   const int n = (int)min((int64_t)8, a.cols - col);
   float w[8], dw[8] = {};
@@ -486,9 +487,22 @@ unsigned row_threads(int64_t cols, int nv) { return (unsigned)((cols + 512 * nv 
 // threads of a two-pass kernel's workgroup: rows of fewer than 8 columns are one thread's
 dim3 long_threads(int64_t cols) { return dim3(cols < 8 ? 64 : 1024); }
 
+// A launch holds fewer than 2^32 threads: more rows than these are cut into launches (each of a
+// millisecond or more).  The same over x and y in one launch cost short calls 0.15 us.
+constexpr int64_t kLaunchRows = 1 << 21;
+// f(first row, number of rows) until an error
+template <class F>
+hipError_t over_rows(int64_t rows, F f) {
+  for (int64_t r = 0; r < rows; r += kLaunchRows) {
+    const hipError_t e = f(r, std::min(rows - r, kLaunchRows));
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 template <int DT, int SC>
 hipError_t go_fwd(const NormArgs& a, hipStream_t s) {
-  const dim3 rows = wide_grid(a.rows), waves = wide_grid((a.rows + 3) / 4);
+  const dim3 rows((unsigned)a.rows), waves((unsigned)((a.rows + 3) / 4));
   const dim3 one(row_threads(a.cols, 1)), two(row_threads(a.cols, 2));
   if (!norm_in_registers(a.cols)) hipLaunchKernelGGL((rmsnorm_long<DT, SC>), rows, long_threads(a.cols), 0, s, a);
   else if (a.cols <= 512) hipLaunchKernelGGL((rmsnorm<DT, 1, SC, true, 256>), waves, dim3(256), 0, s, a);
@@ -508,12 +522,20 @@ template <int DT>
 hipError_t go_bwd(const NormBwdArgs& a, int64_t groups, hipStream_t s) {
   const dim3 g((unsigned)groups);
   if (!norm_in_registers(a.cols)) {
-    hipLaunchKernelGGL((rmsnorm_bwd_dot<DT>), wide_grid(a.rows), long_threads(a.cols), 0, s, a);
-    const hipError_t e = hipGetLastError();   // without the dot products there is nothing to read
-    if (e != hipSuccess) return e;
-    const int64_t panels = (a.cols + 2047) / 2048, z = (panels + 32767) / 32768;
-    hipLaunchKernelGGL((rmsnorm_bwd_panel<DT>), dim3((unsigned)groups, (unsigned)((panels + z - 1) / z), (unsigned)z),
-                       dim3(256), 0, s, a);
+    const int64_t eb = DT == TG_F32 ? 4 : 2;
+    const hipError_t e = over_rows(a.rows, [&](int64_t r, int64_t n) {
+      NormBwdArgs b = a;
+      b.dY += r * a.ldy * eb;
+      b.H += r * a.ldh * eb;
+      b.rstd += r;
+      b.dot += r;
+      hipLaunchKernelGGL((rmsnorm_bwd_dot<DT>), dim3((unsigned)n), long_threads(a.cols), 0, s, b);
+      return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;   // without the dot products there is nothing to read
+    const int64_t panels = (a.cols + 2047) / 2048;
+    const dim3 over((unsigned)groups, (unsigned)std::min<int64_t>(panels, kPanels), (unsigned)((panels + kPanels - 1) / kPanels));
+    hipLaunchKernelGGL((rmsnorm_bwd_panel<DT>), over, dim3(256), 0, s, a);
   } else if (a.cols <= 512) hipLaunchKernelGGL((rmsnorm_bwd<DT, 1, true, 256>), g, dim3(256), 0, s, a);
   else if (a.cols <= 1024) hipLaunchKernelGGL((rmsnorm_bwd<DT, 2, true, 256>), g, dim3(256), 0, s, a);
   else if (a.cols <= 4096) hipLaunchKernelGGL((rmsnorm_bwd<DT, 1, false, 512>), g, dim3(row_threads(a.cols, 1)), 0, s, a);
@@ -524,10 +546,22 @@ hipError_t go_bwd(const NormBwdArgs& a, int64_t groups, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_rmsnorm(const NormArgs& a, int dtype, int scale_kind, hipStream_t s) {
-  if (dtype == TG_F32) return go_fwd<TG_F32>(a, scale_kind, s);
-  if (dtype == TG_F16) return go_fwd<TG_F16>(a, scale_kind, s);
-  return go_fwd<TG_BF16>(a, scale_kind, s);
+hipError_t launch_rmsnorm(const NormArgs& all, int dtype, int scale_kind, hipStream_t s) {
+  const int64_t eb = dtype == TG_F32 ? 4 : 2, yb = scale_kind == TG_SCALE_NONE ? eb : 1;
+  const int64_t sb = scale_kind == TG_SCALE_ROW ? 4 : scale_kind == TG_SCALE_BLOCK ? all.cols / 32 : 0;
+  return over_rows(all.rows, [&](int64_t r, int64_t n) {
+    NormArgs a = all;
+    a.rows = n;
+    a.X += r * a.ldx * eb;
+    if (a.R) a.R += r * a.ldr * eb;
+    if (a.H) a.H += r * a.ldh * eb;
+    a.Y += r * a.ldy * yb;
+    if (a.S) a.S += r * sb;
+    if (a.rstd) a.rstd += r;
+    if (dtype == TG_F32) return go_fwd<TG_F32>(a, scale_kind, s);
+    if (dtype == TG_F16) return go_fwd<TG_F16>(a, scale_kind, s);
+    return go_fwd<TG_BF16>(a, scale_kind, s);
+  });
 }
 
 hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int dtype, int64_t groups, hipStream_t s) {

@@ -40,14 +40,15 @@ bool tile_steps_aligned(const Side& s, int64_t tile_rows, int64_t tile_cols, int
 
 // ------------------------------------------------------------ launch size ---
 // A launch holds fewer than 2^32 threads in each dimension: `blocks` workgroups of up to 1024 threads
-// (0 .. 2^37 of them) lie over x and y.  The last few may lie past the end; a kernel finds its place
-// with wide_block().
+// (at most 2^31 of them) lie over x and y, rows of 2^16.  The last row's end lies past them; a kernel finds
+// its place with wide_block().  The row length is a constant: reading the grid's size would be one more
+// wait at the start of kernels of a few microseconds.
+constexpr int kWideRow = 1 << 16;
 inline dim3 wide_grid(int64_t blocks) {
-  const int64_t most = (int64_t)1 << 21, y = (blocks + most - 1) / most;
-  return y <= 1 ? dim3((unsigned)blocks) : dim3((unsigned)((blocks + y - 1) / y), (unsigned)y);
+  return blocks <= kWideRow ? dim3((unsigned)blocks) : dim3(kWideRow, (unsigned)((blocks + kWideRow - 1) / kWideRow));
 }
 #ifdef __HIP__
-__device__ __forceinline__ int64_t wide_block() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+__device__ __forceinline__ int64_t wide_block() { return (int64_t)blockIdx.y * kWideRow + blockIdx.x; }
 #endif
 
 // --------------------------------------------------------- launch structs ---
