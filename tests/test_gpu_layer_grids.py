@@ -136,3 +136,22 @@ def test_epilogue_of_a_zero_product_past_two_to_the_35_results():
         assert bool((D[at:at + (1 << 14)] == want).all()), at
     del D
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("rows", [1, 3, 5])
+@pytest.mark.parametrize("cols", [1, 7, 16385])
+def test_norm_backward_with_the_least_documented_workspace(rows, cols):
+    """4 bytes a row, whatever the alignment of the shares behind them."""
+    say(f"norm backward least workspace rows={rows} cols={cols}")
+    H, W, dY = filled(1, (rows, cols), "bf16", 3.0), filled(2, (cols,), "bf16"), filled(3, (rows, cols), "bf16")
+    rstd = torch.rsqrt(H.float().square().mean(dim=1) + 1e-5)
+    dX, dw = torch.empty_like(H), torch.empty(cols, device=dev())
+    ws = torch.full((64,), 255, dtype=torch.uint8, device=dev())
+    bf = tg.TG_BF16
+    with pytest.raises(tg.TileError):
+        tg.tile_rmsnorm_bwd(dY, H, W, rstd, None, dX, dw, rows, cols, bf, bf, workspace=ws, workspace_bytes=4 * rows - 1)
+    tg.tile_rmsnorm_bwd(dY, H, W, rstd, None, dX, dw, rows, cols, bf, bf, workspace=ws, workspace_bytes=4 * rows)
+    ref, bound, wref, wbound = ol.norm_backward(host(dY), host(H), host(W), host(rstd), None, "bf16")
+    check(dX, ref, bound, "dX")
+    check(dw, wref, wbound, "dw")
+    assert bool((ws[4 * rows:] == 255).all())

@@ -572,8 +572,9 @@ int tile_rmsnorm_bwd(const void* dY, const void* H, const void* W, const float* 
   if (overlaps(mdx, mdw) || overlaps(mdx, mws) || overlaps(mdw, mws))
     return fail(TG_E_ALIAS, "dX, dW and the workspace must not overlap");
   const int64_t dots = norm_in_registers(cols) ? 0 : (rows * 4 + 15) / 16 * 16;
-  if (workspace_bytes < dots)
-    return fail(TG_E_ARG, fmt("rows of %lld columns need a workspace of at least %lld bytes", cols, dots));
+  const int64_t least = dots ? rows * 4 : 0;   // `dots` is rounded up for the shares of dW behind it
+  if (workspace_bytes < least)
+    return fail(TG_E_ARG, fmt("rows of %lld columns need a workspace of at least %lld bytes", cols, least));
   if (rows == 0) return dW ? hip_status("tile_rmsnorm_bwd", launch_sum_rows(dW, 0, cols, dW, s)) : TG_OK;
   NormBwdArgs a{};
   a.dY = (const uint8_t*)dY;
