@@ -524,6 +524,9 @@ def tile_gemm_atom_select(M, N, K, dtype, transA, transB):
 # their checks and allocations are native (csrc/tensor_calls.cpp).  Their results carry no autograd
 # history: the backward calls give the gradients.  An input that requires one gets a warning while
 # gradients are recorded, and tensors they write (out, h_out) count as changed.
+# stream (a stream or its handle; the current one by default): the results and the workspace belong to it.
+# As with every call of this package the caller orders it after the streams that write the inputs, and
+# keeps inputs of other streams alive until it has read them (Tensor.record_stream).
 
 ACTS = {"none": TG_ACT_NONE, "relu": TG_ACT_RELU, "gelu": TG_ACT_GELU,
         "gelu_tanh": TG_ACT_GELU_TANH, "silu": TG_ACT_SILU}
