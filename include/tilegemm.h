@@ -577,11 +577,12 @@ typedef struct tg_ep_plan {
  * tile_gemm_ep — D = act(Z) + residual,  Z[m][n] = row_scale[m]·col_scale[n]·(A·B)[m][n] + bias[n].
  *
  *   A, B    device, stored as tile_gemm's (transA, transB) with leading dimensions lda, ldb.
- *           16-bit: a_dtype == b_dtype, TG_F16 or TG_BF16, any orientation.  fp8: each
- *           TG_FP8_E4M3 or TG_FP8_E5M2, transA == 0 and transB == 1 (else TG_E_LAYOUT).
+ *           16-bit: a_dtype == b_dtype, TG_F16 or TG_BF16, any orientation.  8-bit integers: both
+ *           TG_I8; fp8: each TG_FP8_E4M3 or TG_FP8_E5M2; both with transA == 0 and transB == 1 (else
+ *           TG_E_LAYOUT).
  *   D       device [M,N] of d_dtype (TG_F16, TG_BF16 or TG_F32), leading dimension ldd.
- *   M,N,K   any, 0 .. 2^30.  M == 0 or N == 0 is a no-op; K == 0 has A·B = 0.  TG_E_SHAPE above 2^41
- *           results, and where the plan's workgroups would hold 2^32 threads: 2^23 blocks of 128 x 128
+ *   M,N,K   any, 0 .. 2^30 (K of integers at most 131071: 128·128·K < 2^31).  M == 0 or N == 0 is a
+ *           no-op; K == 0 has A·B = 0.  TG_E_SHAPE above 2^41 results, and where the plan's workgroups would hold 2^32 threads: 2^23 blocks of 128 x 128
  *           or 256 x 256 (an extent within 128 of 2^30 where rows are no multiples of 16 bytes, an extent
  *           above 2^29 with more than 128 of the other, ...).
  *   ep      the epilogue, or NULL for none of it.
@@ -589,8 +590,8 @@ typedef struct tg_ep_plan {
  *           tiles and a long K sum parts of K in different workgroups when the parts' fp32
  *           sums fit here.  tile_gemm_ep_workspace says how much the best plan uses; with
  *           less, fewer parts are made.
- * The sum over K is held in fp32 (fp8: in the groups tile_gemm_fp8 describes), parts are added
- * in their order, and Z and D are each rounded once from the fp32 value, so a call gives the same
+ * The sum over K is held in fp32 (fp8: in the groups tile_gemm_fp8 describes; integers: exactly, in
+ * 32-bit integers that are rounded to fp32 once), parts are added in their order, and Z and D are each rounded once from the fp32 value, so a call gives the same
  * bits every time.  Returns TG_OK or a tg_status; asynchronous on `stream`.
  */
 int tile_gemm_ep(const void* A, const void* B, void* D, int64_t M, int64_t N, int64_t K,

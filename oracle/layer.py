@@ -68,10 +68,11 @@ def product_bound(A, B, eight):
 
 
 def product(A, B, kind="none", bias=None, residual=None, row_scale=None, col_scale=None, out="bf16",
-            eight=False):
-    """(D, Z, bound of D, bound of Z) for A [M][K], B [K][N]."""
+            eight=False, ints=False):
+    """(D, Z, bound of D, bound of Z) for A [M][K], B [K][N].  ints: operands of 8-bit integers, whose sums
+    are exact and rounded to fp32 once."""
     P = A @ B
-    err = product_bound(A, B, eight)
+    err = U32 * np.abs(P) if ints else product_bound(A, B, eight)
     scale = np.ones((A.shape[0], B.shape[1]))
     if row_scale is not None:
         scale = scale * row_scale[:, None]

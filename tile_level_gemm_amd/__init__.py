@@ -744,8 +744,9 @@ def gemm_ep(A, B, bias=None, act="none", residual=None, row_scale=None, col_scal
     """D = act(row_scale·col_scale·A·B + bias) + residual; returns D, or (D, Z) with keep_z.
 
     A is [M, K] ([K, M] with trans_a), B [N, K] as a linear layer's weight ([K, N] without trans_b);
-    rows may be slices of wider tensors.  out_dtype: the operands' type by default, bfloat16 for
-    fp8 operands.  residual and out have out_dtype; they may be the same tensor."""
+    rows may be slices of wider tensors.  float16 or bfloat16; float8 or int8 (exact sums) with A
+    [M, K] and B [N, K].  out_dtype: the operands' type by default, bfloat16 for 8-bit operands.
+    residual and out have out_dtype; they may be the same tensor."""
     if stream is not None:
         with _On(stream):
             return gemm_ep(A, B, bias, act, residual, row_scale, col_scale, trans_a, trans_b, out_dtype, keep_z, out)

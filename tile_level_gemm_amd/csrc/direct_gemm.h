@@ -57,6 +57,8 @@ namespace {
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 typedef __attribute__((ext_vector_type(16))) float f32x16;
+typedef __attribute__((ext_vector_type(16))) int i32x16;
+typedef __attribute__((ext_vector_type(4))) int i32x4;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 typedef __attribute__((ext_vector_type(8))) uint32_t u32x8;
@@ -82,15 +84,17 @@ constexpr int p6_code(int a_fmt, int b_fmt) { return kP6 + 2 * (a_fmt - 2) + (b_
 constexpr int fp8_code(int a_fmt, int b_fmt) { return kF8 + 2 * a_fmt + b_fmt; }
 constexpr int mx_code(int a_fmt, int b_fmt) { return kMX + 2 * a_fmt + b_fmt; }
 
-// Addressing unit: one element of a 16-bit or fp8 operand, one byte of a packed operand.
-// kFp8: the two-step (64-K) stage schedule, which 6-bit operands share.
+// Addressing unit: one element of a 16-bit, fp8 or int8 operand, one byte of a packed operand.
+// kFp8: the two-step (64-K) stage schedule, which 6-bit operands share.  kI8 (DT TG_I8): four steps of
+// 32 K whose lanes carry 16 bytes, read as 16-bit fragments are; sums in 32-bit integers.
 template <int DT>
 struct Elem {
   static constexpr bool kFp4 = DT == kP4;
   static constexpr bool kFp6 = DT >= kP6;
   static constexpr bool kFp8 = DT >= kF8 && !kFp4;
+  static constexpr bool kI8 = DT == TG_I8;
   static constexpr bool kScaled = DT >= kMX;      // E8M0 scale per 32 K of each row / column
-  static constexpr int kBytes = kFp8 || kFp4 ? 1 : 2;   // bytes per addressing unit
+  static constexpr int kBytes = kFp8 || kFp4 || kI8 ? 1 : 2;   // bytes per addressing unit
   static constexpr int kPer = kFp4 ? 2 : 1;        // K values per addressing unit (not 6-bit)
   static constexpr int kBK = kRowBytes / kBytes;   // addressing units per stage
   static constexpr int kStageBytes = kFp6 ? 96 : kRowBytes;   // bytes of a K row per stage

@@ -1,6 +1,6 @@
 // Matrix product with an epilogue: launch arguments and the epilogue's device functions.
 //
-//   P = A·B (fp32 sums)   Z = row_scale[m]·col_scale[n]·P + bias[n]   D = act(Z) + residual
+//   P = A·B (fp32 sums; int8 operands: exact 32-bit integers, then fp32)   Z = row_scale[m]·col_scale[n]·P + bias[n]   D = act(Z) + residual
 //
 // Every kernel that finishes an output element (the block kernels, the token kernels and the join
 // of a split sum) goes through ep_finish8, its 16-bit form or ep_finish1, so all of them round once: Z and D are each
@@ -25,7 +25,7 @@ struct EpArgs {
   int32_t waves, cn;           // few rows: waves and columns of a workgroup
   int32_t ring;                // direct blocks: four stages in flight (128 and 64 wide)
   int32_t splits, k_per_split; // the sum over K in `splits` parts of k_per_split (the last one shorter)
-  float* part;                 // splits > 1: fp32 sums [splits][M][part_ld]
+  float* part;                 // splits > 1: fp32 (or 32-bit integer) sums [splits][M][part_ld]
   int64_t part_ld;             // N rounded up to 8: rows stay 32-byte aligned
   const uint8_t* bias;
   const uint8_t* res;
@@ -34,6 +34,7 @@ struct EpArgs {
   const float* cs;
   int64_t ldr, ldz;
   int32_t bias_t, d_t, act;    // tg_dtype, tg_dtype, tg_act
+  int32_t ints;                // parts hold integers
 };
 
 // Kernel families of tile_gemm_ep (tg_ep_plan.kernel).
@@ -72,6 +73,7 @@ hipError_t launch_ep_km(const EpArgs& g, int dtype, const EpKernel& k, hipStream
 hipError_t launch_ep_mk(const EpArgs& g, int dtype, const EpKernel& k, hipStream_t s);
 hipError_t launch_ep_mm(const EpArgs& g, int dtype, const EpKernel& k, hipStream_t s);
 hipError_t launch_ep_fp8(const EpArgs& g, int a_dtype, int b_dtype, const EpKernel& k, hipStream_t s);
+hipError_t launch_ep_i8(const EpArgs& g, const EpKernel& k, hipStream_t s);
 
 #ifdef __HIP__
 namespace {

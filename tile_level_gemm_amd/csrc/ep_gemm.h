@@ -38,6 +38,9 @@ template <int DT, class F>
 __device__ __forceinline__ f32x16 mfma32t(F b, F a, f32x16 c) {
   if constexpr (DT == TG_F16 || DT == TG_BF16)
     return mfma32<DT>(b, a, c);
+  else if constexpr (DT == TG_I8)   // integer sums, held as the bits of c's floats
+    return __builtin_bit_cast(f32x16, __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, b), __builtin_bit_cast(i32x4, a),
+                                                                            __builtin_bit_cast(i32x16, c), 0, 0, 0));
   else
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
         __builtin_bit_cast(i32x8, b), __builtin_bit_cast(i32x8, a), c, DT & 1, (DT & 3) >> 1, 0, 0, 0,
@@ -149,7 +152,8 @@ __device__ __forceinline__ EpTile ep_tile(const EpArgs& g) {
 // Epilogue, one 32-row band of the wave's tile at a time.  No wave reads or fills a stage buffer any
 // more, so the bands live there: s0 .. s3 are four stage arrays.
 // Accumulator element r of tile (i, j): row 32i + lane%32, column 32j + 8(r/4) + 4(lane/32) + r%4.
-template <int BS, int WN, int TM, int TN>
+// INT: the accumulators hold integers; parts of a sum stay integers, so that ep_join adds them exactly.
+template <int BS, int WN, int TM, int TN, bool INT>
 __device__ __forceinline__ void ep_store(const EpArgs& g, const EpTile& t, f32x16 (&acc)[TM][TN], int wave,
                                          int lane, int wm, int wn, uint8_t* s0, uint8_t* s1, uint8_t* s2,
                                          uint8_t* s3) {
@@ -168,6 +172,13 @@ __device__ __forceinline__ void ep_store(const EpArgs& g, const EpTile& t, f32x1
     const float4 lo = *(const float4*)src, hi = *(const float4*)(src + 4);
     v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
     v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+  };
+  auto sums = [&](int p, float (&v)[8]) {
+    from_band(p, v);
+    if constexpr (INT) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (float)__builtin_bit_cast(int, v[e]);
+    }
   };
   constexpr int NP = 32 / RPP;
   const bool in = col < g.N, half = g.d_t != TG_F32;   // half: 16-bit results
@@ -218,7 +229,7 @@ __device__ __forceinline__ void ep_store(const EpArgs& g, const EpTile& t, f32x1
       ep_with_act(g.act, [&](auto act) {
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          from_band(p, v);
+          sums(p, v);
           const int row = row0 + p * RPP;
           if (in && row < g.M) ep_finish8_16<decltype(act)::value>(g, row, col, cols, rows[p], v);
         }
@@ -226,7 +237,7 @@ __device__ __forceinline__ void ep_store(const EpArgs& g, const EpTile& t, f32x1
     } else {
 #pragma unroll 1
       for (int p = 0; p < NP; ++p) {
-        from_band(p, v);
+        sums(p, v);
         const int row = row0 + p * RPP;
         if (in && row < g.M) ep_finish8(g, row, col, cols, v);   // the L2 joins a row's 16-byte pieces
       }
@@ -282,8 +293,8 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_dir
   constexpr int WM = BS / WGM, WN = BS / WGN, TM = WM / 32, TN = WN / 32;
   constexpr int PER = BS / 8 / NW;
   constexpr int NS = EL::kSteps;
-  static_assert(DT == TG_F16 || DT == TG_BF16 || (DT >= kF8 && DT < kMX), "16-bit or fp8 operands");
-  static_assert(!EL::kFp8 || (!A_MN && !B_MN), "fp8 operands are K-contiguous");
+  static_assert(DT == TG_F16 || DT == TG_BF16 || DT == TG_I8 || (DT >= kF8 && DT < kMX), "16-bit, int8 or fp8 operands");
+  static_assert(EL::kBytes == 2 || (!A_MN && !B_MN), "8-bit operands are K-contiguous");
   const EpTile t = ep_tile<BS>(g);
   const int tid = (int)threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -389,7 +400,7 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_dir
   }
   stage(sa0, sb0, sa1, sb1, kt, F_{}, T_{});
   stage(sa1, sb1, sa0, sb0, kt + 1, F_{}, F_{});
-  ep_store<BS, WN, TM, TN>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
+  ep_store<BS, WN, TM, TN, EL::kI8>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
 }
 
 // s_waitcnt: at most n vector memory instructions outstanding (n < 64), no LDS read
@@ -420,8 +431,8 @@ __global__ __launch_bounds__(ep_threads(BS)) void gemm_ep_ring(EpArgs g) {
   constexpr int WM = BS / WGM, WN = BS / WGN, TM = WM / 32, TN = WN / 32;
   constexpr int PER = BS / 8 / NW;
   constexpr int NS = EL::kSteps;
-  static_assert(DT == TG_F16 || DT == TG_BF16 || (DT >= kF8 && DT < kMX), "16-bit or fp8 operands");
-  static_assert(!EL::kFp8 || (!A_MN && !B_MN), "fp8 operands are K-contiguous");
+  static_assert(DT == TG_F16 || DT == TG_BF16 || DT == TG_I8 || (DT >= kF8 && DT < kMX), "16-bit, int8 or fp8 operands");
+  static_assert(EL::kBytes == 2 || (!A_MN && !B_MN), "8-bit operands are K-contiguous");
   const EpTile t = ep_tile<BS>(g);
   const int tid = (int)threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -498,7 +509,7 @@ __global__ __launch_bounds__(ep_threads(BS)) void gemm_ep_ring(EpArgs g) {
   }
   // the zero stages still on their way must land before the epilogue takes the buffers
   meet(std::integral_constant<int, 0>{});
-  ep_store<BS, WN, TM, TN>(g, t, acc, wave, lane, wm, wn, s0, s1, s2, s3);
+  ep_store<BS, WN, TM, TN, EL::kI8>(g, t, acc, wave, lane, wm, wn, s0, s1, s2, s3);
 }
 
 // Operands through registers, two stages ahead of the one computed: one register set each for the even
@@ -516,8 +527,8 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_sta
   constexpr int WM = BS / WGM, WN = BS / WGN, TM = WM / 32, TN = WN / 32;
   constexpr int PER = BS / 8 / NW;
   constexpr int NS = EL::kSteps;
-  static_assert(DT == TG_F16 || DT == TG_BF16 || (DT >= kF8 && DT < kMX), "16-bit or fp8 operands");
-  static_assert(!EL::kFp8 || (!A_MN && !B_MN), "fp8 operands are K-contiguous");
+  static_assert(DT == TG_F16 || DT == TG_BF16 || DT == TG_I8 || (DT >= kF8 && DT < kMX), "16-bit, int8 or fp8 operands");
+  static_assert(EL::kBytes == 2 || (!A_MN && !B_MN), "8-bit operands are K-contiguous");
   const EpTile t = ep_tile<BS>(g);
   const int tid = (int)threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -605,7 +616,7 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_sta
     }
     if (kt < KT) stage(sa0, sb0, sa1, sb1, kt, S0, S1);
   }
-  ep_store<BS, WN, TM, TN>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
+  ep_store<BS, WN, TM, TN, EL::kI8>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
 }
 
 template <bool A_MN, bool B_MN, int DT>

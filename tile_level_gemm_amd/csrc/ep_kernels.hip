@@ -9,6 +9,8 @@ namespace {
 // 8 columns per thread; bound by the partial sums' bytes, which the block kernels have just
 // written: two parts of 4096 x 2048, 84 MB, 15.5 us (5.4 TB/s).  Four parts' loads are in flight
 // together: one at a time, 16 parts of one row took 7.9 us, nearly all of it waiting.
+// INT: parts of a product of integers, added as integers and rounded to fp32 once.
+template <bool INT>
 __global__ __launch_bounds__(256) void ep_join(EpArgs g, int64_t chunks) {
   const int64_t i = wide_block() * 256 + threadIdx.x;
   if (i >= chunks) return;
@@ -19,9 +21,13 @@ __global__ __launch_bounds__(256) void ep_join(EpArgs g, int64_t chunks) {
   float v[8] = {};
   const float* p = g.part + (int64_t)row * g.part_ld + col;
   const int64_t step = (int64_t)g.M * g.part_ld;
+  auto plus = [](float& x, float y) {
+    if constexpr (INT) x = __builtin_bit_cast(float, __builtin_bit_cast(int, x) + __builtin_bit_cast(int, y));
+    else x += y;
+  };
   auto add = [&](float4 a, float4 b) {
-    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    plus(v[0], a.x); plus(v[1], a.y); plus(v[2], a.z); plus(v[3], a.w);
+    plus(v[4], b.x); plus(v[5], b.y); plus(v[6], b.z); plus(v[7], b.w);
   };
   int s = 0;
   for (; s + 4 <= g.splits; s += 4, p += 4 * step) {
@@ -35,6 +41,10 @@ __global__ __launch_bounds__(256) void ep_join(EpArgs g, int64_t chunks) {
     for (int k = 0; k < 4; ++k) add(a[k], b[k]);
   }
   for (; s < g.splits; ++s, p += step) add(*(const float4*)p, *(const float4*)(p + 4));
+  if constexpr (INT) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (float)__builtin_bit_cast(int, v[e]);
+  }
   ep_finish8(g, row, col, cols, v);
 }
 
@@ -132,7 +142,9 @@ __global__ __launch_bounds__(1024) void sum_rows(const float* part, int64_t G, i
 
 hipError_t launch_ep_join(const EpArgs& g, hipStream_t s) {
   const int64_t chunks = (int64_t)g.M * ((g.N + 7) / 8);
-  hipLaunchKernelGGL(ep_join, wide_grid((chunks + 255) / 256), dim3(256), 0, s, g, chunks);
+  const dim3 grid = wide_grid((chunks + 255) / 256);
+  if (g.ints) hipLaunchKernelGGL(ep_join<true>, grid, dim3(256), 0, s, g, chunks);
+  else hipLaunchKernelGGL(ep_join<false>, grid, dim3(256), 0, s, g, chunks);
   return hipGetLastError();
 }
 
@@ -158,6 +170,7 @@ hipError_t launch_sum_rows(const float* part, int64_t G, int64_t N, float* out, 
 hipError_t launch_ep_block(const EpArgs& g, int trans_a, int trans_b, int a_dtype, int b_dtype,
                            const EpKernel& k, hipStream_t s) {
   if (a_dtype == TG_FP8_E4M3 || a_dtype == TG_FP8_E5M2) return launch_ep_fp8(g, a_dtype, b_dtype, k, s);
+  if (a_dtype == TG_I8) return launch_ep_i8(g, k, s);
   if (trans_a) return trans_b ? launch_ep_mk(g, a_dtype, k, s) : launch_ep_mm(g, a_dtype, k, s);
   return trans_b ? launch_ep_kk(g, a_dtype, k, s) : launch_ep_km(g, a_dtype, k, s);
 }

@@ -8,7 +8,7 @@
 //
 //   B [N][K] (K-major): a step is 128 bytes of K of 16 columns (32 for N >= 8192: A is read half as
 //     often).  Lane (n = l%16, g = l/16) loads bytes 32g .. 32g+31 of its column, so four lanes read one
-//     whole line; the matrix instruction (16x16x32 for 16-bit, 16x16x128 for fp8) takes K in that order,
+//     whole line; the matrix instruction (16x16x32 for 16-bit, 16x16x64 for int8, 16x16x128 for fp8) takes K in that order,
 //     for A and B alike (a sum does not care).  For small N the workgroup owns 8 or 4 columns and the
 //     other lanes load nothing: more CUs, no parts to join.
 //   B [K][N]: a step is 32 k-rows of 32 columns.  Where that leaves CUs without work and a workgroup
@@ -36,6 +36,9 @@ __device__ __forceinline__ f32x4 mfma16t(F b, F a, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), c, 0, 0, 0);
   else if constexpr (DT == TG_BF16)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), c, 0, 0, 0);
+  else if constexpr (DT == TG_I8)   // integer sums, held as the bits of c's floats
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, b), __builtin_bit_cast(i32x4, a),
+                                                                           __builtin_bit_cast(i32x4, c), 0, 0, 0));
   else
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(i32x8, b), __builtin_bit_cast(i32x8, a),
                                                             c, DT & 1, (DT & 3) >> 1, 0, 0, 0, 0);
@@ -76,10 +79,10 @@ __global__ __launch_bounds__(1024) void gemm_ep_tokens(EpArgs g) {
   static_assert(!B_MN || NI == 2, "a lane's two columns");
   constexpr int CN = 16 * NI;                   // most columns of a workgroup
   constexpr int KS = B_MN ? 32 : 128 / E;       // K of a step
-  constexpr int KI = E == 2 ? 32 : 128;         // K of an instruction
+  constexpr int KI = EL::kFp8 ? 128 : 64 / E;   // K of an instruction
   constexpr int NF = KS / KI;                   // instructions of a step along K
   constexpr int U = MT == 1 && (B_MN || NI == 1) ? 4 : 2;   // steps in flight
-  using Frag = typename EL::Frag;               // one instruction's operand: 8 16-bit values, 32 fp8
+  using Frag = typename EL::Frag;               // one instruction's operand: 8 16-bit values, 16 int8, 32 fp8
   constexpr int LD = CN + 1;
   __shared__ float red[16][MT * 16][LD];
 
@@ -147,7 +150,7 @@ __global__ __launch_bounds__(1024) void gemm_ep_tokens(EpArgs g) {
       const uint32_t sel = c ? 0x07060302u : 0x05040100u;   // high or low halves of two k-rows
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = __builtin_amdgcn_perm(x.r[2 * e + 1], x.r[2 * e], sel);
-    } else if constexpr (E == 2) {
+    } else if constexpr (!EL::kFp8) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = x.r[8 * c + 4 * f + e];
     } else {
@@ -159,14 +162,14 @@ __global__ __launch_bounds__(1024) void gemm_ep_tokens(EpArgs g) {
   // A's fragment of row tile i, instruction f of a step: K in the same order as B's
   auto frag_a = [&](int step, int i, int f, auto partial) {
     constexpr bool kPartial = decltype(partial)::value;
-    const int row = 16 * i + li, k = step * KS + kl + (E == 2 ? 8 * f : 0), left = K - k;
+    const int row = 16 * i + li, k = step * KS + kl + (EL::kFp8 ? 0 : 16 / E * f), left = K - k;
     Frag o = {};
     if (row < g.M) {
       if constexpr (A_MN) {
         o = k_gather((const uint16_t*)pa + (int64_t)k * g.lda + row, g.lda, kPartial ? left : 8);
       } else {
         const uint8_t* p = pa + ((int64_t)row * g.lda + k) * E;
-        if constexpr (E == 2) {
+        if constexpr (!EL::kFp8) {
           o = kPartial ? k_chunk<E>(p, left) : load16(p);
         } else {
           const u32x4 a = kPartial ? k_chunk<E>(p, left) : load16(p);
@@ -228,15 +231,19 @@ __global__ __launch_bounds__(1024) void gemm_ep_tokens(EpArgs g) {
       for (int r = 0; r < 4; ++r)
         red[wave][16 * i + li][B_MN ? 2 * (4 * lg + r) + c : 16 * c + 4 * lg + r] = acc[i][c][r];
   __syncthreads();
+  auto add = [](float a, float b) {
+    if constexpr (EL::kI8) return __builtin_bit_cast(float, __builtin_bit_cast(int, a) + __builtin_bit_cast(int, b));
+    else return a + b;
+  };
   auto sum = [&](int row, int n) {
     float v = red[0][row][n];
     if (W == 16) {
 #pragma unroll
-      for (int w = 1; w < 16; ++w) v += red[w][row][n];
+      for (int w = 1; w < 16; ++w) v = add(v, red[w][row][n]);
     } else {
-      for (int w = 1; w < W; ++w) v += red[w][row][n];
+      for (int w = 1; w < W; ++w) v = add(v, red[w][row][n]);
     }
-    return v;
+    return EL::kI8 ? (float)__builtin_bit_cast(int, v) : v;
   };
   for (int o = (int)threadIdx.x; o < MT * 16 * CN; o += (int)blockDim.x) {
     const int row = o / CN, col_o = n0 + o % CN;
@@ -276,6 +283,7 @@ hipError_t go16(const EpArgs& g, int ta, int tb, int waves, hipStream_t s) {
 hipError_t launch_ep_tokens(const EpArgs& g, int trans_a, int trans_b, int a_dtype, int b_dtype, int waves,
                             hipStream_t s) {
   if (a_dtype == TG_F16) return go16<TG_F16>(g, trans_a, trans_b, waves, s);
+  if (a_dtype == TG_I8) return go<false, false, TG_I8>(g, waves, s);
   if (a_dtype == TG_BF16) return go16<TG_BF16>(g, trans_a, trans_b, waves, s);
   const bool a5 = a_dtype == TG_FP8_E5M2, b5 = b_dtype == TG_FP8_E5M2;
   if (a5 && b5) return go<false, false, fp8_code(1, 1)>(g, waves, s);

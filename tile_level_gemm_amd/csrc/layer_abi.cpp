@@ -14,6 +14,7 @@ using namespace tg;
 namespace {
 
 const int64_t kMaxDim = (int64_t)1 << 30;
+const int64_t kMaxIntK = 131071;                 // 128·128·K stays below 2^31
 const int64_t kMaxLd = (int64_t)1 << 40;
 const int64_t kMaxSpan = (int64_t)1 << 60;      // elements from a matrix's first row to its last
 const int64_t kDirectSpan = (int64_t)1 << 31;   // buffer offsets of the direct loads stay below
@@ -25,7 +26,8 @@ std::string fmt(const char* f, long long a = 0, long long b = 0, long long c = 0
 }
 
 bool is16(int t) { return t == TG_F16 || t == TG_BF16; }
-bool is8(int t) { return t == TG_FP8_E4M3 || t == TG_FP8_E5M2; }
+bool isf8(int t) { return t == TG_FP8_E4M3 || t == TG_FP8_E5M2; }
+bool is8(int t) { return isf8(t) || t == TG_I8; }
 bool is_float(int t) { return is16(t) || t == TG_F32; }
 int bytes_of(int t) { return t == TG_F32 ? 4 : is16(t) ? 2 : 1; }
 
@@ -186,9 +188,11 @@ int plan_ep(const void* A, const void* B, const void* D, int64_t M, int64_t N, i
   if (!ep) ep = &kNone;
   int st = check_extents(M, N, K);
   if (st) return st;
-  if (!(is16(a_dtype) && a_dtype == b_dtype) && !(is8(a_dtype) && is8(b_dtype)))
-    return fail(TG_E_DTYPE, fmt("operands must both be TG_F16, both TG_BF16, or both fp8 (got %lld, %lld)",
+  if (!((is16(a_dtype) || a_dtype == TG_I8) && a_dtype == b_dtype) && !(isf8(a_dtype) && isf8(b_dtype)))
+    return fail(TG_E_DTYPE, fmt("operands must both be TG_F16, both TG_BF16, both TG_I8, or both fp8 (got %lld, %lld)",
                                 a_dtype, b_dtype));
+  if (a_dtype == TG_I8 && K > kMaxIntK)
+    return fail(TG_E_SHAPE, fmt("K %lld: sums of 8-bit integers are held in 32 bits, K is at most %lld", K, kMaxIntK));
   if (!is_float(d_dtype)) return fail(TG_E_DTYPE, fmt("d_dtype must be TG_F16, TG_BF16 or TG_F32 (got %lld)", d_dtype));
   if (ep->bias && !is_float(ep->bias_dtype))
     return fail(TG_E_DTYPE, fmt("bias_dtype must be TG_F16, TG_BF16 or TG_F32 (got %lld)", ep->bias_dtype));
@@ -196,7 +200,7 @@ int plan_ep(const void* A, const void* B, const void* D, int64_t M, int64_t N, i
   if (transB != 0 && transB != 1) return fail(TG_E_ARG, "transB must be 0 or 1");
   if (ep->act < TG_ACT_NONE || ep->act > TG_ACT_SILU) return fail(TG_E_ARG, fmt("unknown activation %lld", ep->act));
   if (is8(a_dtype) && (transA || !transB))
-    return fail(TG_E_LAYOUT, "fp8 operands are stored A [M,K], B [N,K] (transA 0, transB 1)");
+    return fail(TG_E_LAYOUT, "8-bit operands are stored A [M,K], B [N,K] (transA 0, transB 1)");
   int64_t ldr = ep->ld_residual, ldz = ep->ld_z;
   if ((st = resolve_ld("lda", &lda, transA ? M : K, transA ? K : M)) ||
       (st = resolve_ld("ldb", &ldb, transB ? K : N, transB ? N : K)) ||
@@ -281,6 +285,7 @@ int plan_ep(const void* A, const void* B, const void* D, int64_t M, int64_t N, i
   g->bias_t = ep->bias_dtype;
   g->d_t = d_dtype;
   g->act = ep->act;
+  g->ints = a_dtype == TG_I8;
   return TG_OK;
 }
 
@@ -483,7 +488,7 @@ int tile_rmsnorm(const void* X, const void* R, const void* W, void* H, void* Y, 
   if (w_dtype != dtype && w_dtype != TG_F32) return fail(TG_E_DTYPE, "w_dtype must be dtype or TG_F32");
   if (scale_kind < TG_SCALE_NONE || scale_kind > TG_SCALE_BLOCK)
     return fail(TG_E_ARG, fmt("unknown scale kind %lld", scale_kind));
-  if (scale_kind == TG_SCALE_NONE ? y_dtype != dtype : !is8(y_dtype))
+  if (scale_kind == TG_SCALE_NONE ? y_dtype != dtype : !isf8(y_dtype))
     return fail(TG_E_DTYPE, "y_dtype must be dtype without scales, TG_FP8_E4M3 or TG_FP8_E5M2 with them");
   if (scale_kind == TG_SCALE_BLOCK && cols % 32)
     return fail(TG_E_SHAPE, fmt("block scales need cols %% 32 == 0 (got %lld)", cols));

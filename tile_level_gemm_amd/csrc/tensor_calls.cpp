@@ -47,6 +47,7 @@ int code_of(at::ScalarType t) {
     case at::kFloat: return TG_F32;
     case at::kFloat8_e4m3fn: return TG_FP8_E4M3;
     case at::kFloat8_e5m2: return TG_FP8_E5M2;
+    case at::kChar: return TG_I8;
     default: return 0;
   }
 }
@@ -189,7 +190,7 @@ PyObject* gemm_ep(PyObject* const* a) {
   const bool ta = truth(a[7]), tb = truth(a[8]), keep_z = truth(a[10]);
   const Extents e = extents(A, B, ta, tb);
   const int at = dtype_code("A", A.scalar_type()), bt = dtype_code("B", B.scalar_type());
-  const bool eight = at == TG_FP8_E4M3 || at == TG_FP8_E5M2;
+  const bool eight = at == TG_FP8_E4M3 || at == TG_FP8_E5M2 || at == TG_I8;
   const at::ScalarType out_t = a[9] != Py_None ? scalar_type("out_dtype", a[9])
                                : given         ? given->scalar_type()
                                : eight         ? at::kBFloat16
