@@ -523,7 +523,7 @@ int tile_gemm_atom_select(int64_t M, int64_t N, int64_t K, int dtype, int transA
  * Operators of a transformer layer around the products: the product with scales, bias,
  * activation and residual in its epilogue, its backward pass, the root-mean-square norm with
  * the residual's addition (16-bit result, or 8 bits with scales for the products above and
- * below) and its backward pass.  Conventions as for every entry point; in addition:
+ * below), the layer norm likewise, their backward passes, and the quantisation of rows.  Conventions as for every entry point; in addition:
  *   - leading dimensions count elements, 0 means packed; at least the row length, at most 2^40, and at
  *     most 2^60 elements over all rows;
  *   - pointers need only their element's alignment (16-byte aligned operands whose rows are
@@ -654,7 +654,8 @@ int64_t tile_gemm_ep_bwd_workspace(int64_t M, int64_t N, int64_t K, int transA, 
 
 typedef enum tg_scale_kind {
   TG_SCALE_NONE = 0,   /* Y in X's dtype */
-  TG_SCALE_ROW = 1,    /* Y in 8 bits, fp32 S[row] = max|Y[row]|/qmax: tile_gemm_ep's row_scale */
+  TG_SCALE_ROW = 1,    /* Y in 8 bits, fp32 S[row] = max|Y[row]|/qmax: tile_gemm_ep's row_scale (of
+                          weight rows: its col_scale) */
   TG_SCALE_BLOCK = 2   /* Y in 8 bits, E8M0 bytes S[row][col/32]: the smallest power of two with
                           max|Y of the 32 columns|/S <= qmax: tile_gemm_mx's SA */
 } tg_scale_kind;
@@ -669,9 +670,10 @@ typedef enum tg_scale_kind {
  *   H       device, as X with ld_h, or NULL; only with R.  May be exactly X or exactly R.
  *   Y       device [rows, cols] of y_dtype, leading dimension ld_y.  TG_SCALE_NONE: y_dtype ==
  *           dtype.  Otherwise TG_FP8_E4M3 or TG_FP8_E5M2 holding Y/S rounded once (qmax 448 or
- *           57344; nothing saturates), and max|Y| is taken as at least 2^-100.  A row or block
- *           whose Y holds a NaN or an infinity gets a NaN scale (from an infinite weight too, or a
- *           product past fp32).
+ *           57344; nothing saturates), or with TG_SCALE_ROW TG_I8 (qmax 127, rounded to nearest, ties
+ *           to even), and max|Y| is taken as at least 2^-100.  A row or block whose Y holds a NaN or
+ *           an infinity gets a NaN scale (from an infinite weight too, or a product past fp32); its
+ *           codes are NaN, as integers 0.
  *   S       device scales, packed (see tg_scale_kind), or NULL for TG_SCALE_NONE.  TG_SCALE_BLOCK
  *           needs cols % 32 == 0 (TG_E_SHAPE).
  *   rstd    device fp32 [rows], or NULL: for the backward pass.  The mean of squares is taken in
@@ -703,6 +705,52 @@ int tile_rmsnorm_bwd(const void* dY, const void* H, const void* W, const float* 
 /* tile_rmsnorm_bwd_workspace — host-only. */
 int64_t tile_rmsnorm_bwd_workspace(int64_t rows, int64_t cols, int dtype);
 
+/*
+ * tile_layernorm — H = X + R,  mean and rstd = 1/sqrt(mean((H - mean)^2) + eps) per row,
+ * Y = (H - mean)·rstd·W + bias.
+ *
+ *   bias    device [cols] of w_dtype, or NULL.
+ *   mean    device fp32 [rows], or NULL: for the backward pass, as rstd.  The squares are taken about
+ *           the mean, in fp32: a row far from zero keeps its variance, deviations above about 2^63
+ *           overflow it (rstd 0).
+ * Everything else as for tile_rmsnorm.
+ */
+int tile_layernorm(const void* X, const void* R, const void* W, const void* bias, void* H, void* Y, void* S,
+                   float* mean, float* rstd, int64_t rows, int64_t cols, int64_t ld_x, int64_t ld_r,
+                   int64_t ld_h, int64_t ld_y, float eps, int dtype, int w_dtype, int y_dtype, int scale_kind,
+                   void* stream);
+
+/*
+ * tile_layernorm_bwd — gradients of tile_layernorm for the gradient dY of Y, with xh = (H - mean)·rstd and
+ * g = dY·W:
+ *
+ *   dX = rstd·(g - mean(g) - xh·mean(g·xh)) + dH    dW[c] = sum_rows dY·xh    dbias[c] = sum_rows dY
+ *
+ *   mean, rstd  device fp32 [rows], what tile_layernorm stored;  dW, dbias  device fp32 [cols], each or NULL.
+ *   workspace   as for tile_rmsnorm_bwd (tile_layernorm_bwd_workspace); rows of fewer than 8 or more than
+ *           16384 columns need at least 8·rows bytes.
+ * Everything else as for tile_rmsnorm_bwd.
+ */
+int tile_layernorm_bwd(const void* dY, const void* H, const void* W, const float* mean, const float* rstd,
+                       const void* dH, void* dX, float* dW, float* dbias, int64_t rows, int64_t cols,
+                       int64_t ld_dy, int64_t ld_h, int64_t ld_dh, int64_t ld_dx, int dtype, int w_dtype,
+                       void* workspace, int64_t workspace_bytes, void* stream);
+
+/* tile_layernorm_bwd_workspace — host-only. */
+int64_t tile_layernorm_bwd_workspace(int64_t rows, int64_t cols, int dtype);
+
+/*
+ * tile_quantize_rows — X in 8 bits with scales, Y = X/S: the operand of an 8-bit product (an activation, or
+ * a weight's rows with one scale per output column) that no norm has just written.
+ *
+ *   X       device [rows, cols] of dtype (TG_F16, TG_BF16 or TG_F32), leading dimension ld_x.
+ *   Y, S    as tile_rmsnorm's with TG_SCALE_ROW (y_dtype TG_I8, TG_FP8_E4M3 or TG_FP8_E5M2) or
+ *           TG_SCALE_BLOCK (fp8, cols % 32 == 0); TG_SCALE_NONE is refused (TG_E_ARG).
+ *   rows, cols   rows 0 .. 2^30 (0: a no-op), cols 1 .. 2^30.
+ */
+int tile_quantize_rows(const void* X, void* Y, void* S, int64_t rows, int64_t cols, int64_t ld_x, int64_t ld_y,
+                       int dtype, int y_dtype, int scale_kind, void* stream);
+
 /* Reason for the last failure on the calling thread ("" after a success): the readable
  * reason a call was refused, as the dispatcher reports why no variant accepts a call
  * ([SYNC-GEMM] 二, the failure reasons of the dispatch; [VEC-AUTO] 接受什么输入).  The
@@ -712,8 +760,8 @@ const char* tile_last_error(void);
 /* Library ABI version (this header: 7; 2 added tile_gemm_fp8 and tile_gemm_fp8_plan, 3 added
  * tile_gemm_mx and tile_gemm_mx_plan, 4 the register fragment calls tile_frag_*, 5
  * tile_copy_async and tile_copy_async_plan, 6 the K = 8 / 16 atoms and tile_mma_select, 7
- * tile_gemm_atom_select and tg_gemm_plan.atom; tile_gemm_ep*, tile_rmsnorm* were added without
- * changing any earlier call, and are found by their symbols). */
+ * tile_gemm_atom_select and tg_gemm_plan.atom; tile_gemm_ep*, tile_rmsnorm*, tile_layernorm* and
+ * tile_quantize_rows were added without changing any earlier call, and are found by their symbols). */
 int tile_abi_version(void);
 
 #ifdef __cplusplus

@@ -1,8 +1,8 @@
 """Reference of the transformer-layer operators in float64 (numpy), with error bounds.
 
 Product with an epilogue: Z = row_scale·col_scale·(A·B) + bias, D = act(Z) + residual, and its
-gradients; RMS norm with the residual's addition, 8-bit results with row or block scales, and its
-gradients.  Inputs are float64 arrays holding the values the device buffers stand for.
+gradients; RMS norm and layer norm with the residual's addition, 8-bit results with row or block
+scales, and their gradients; quantised rows.  Inputs are float64 arrays holding the values the device buffers stand for.
 """
 
 import math
@@ -13,7 +13,7 @@ ACTS = ("none", "relu", "gelu", "gelu_tanh", "silu")
 HALF_STEP = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8, "f32": 2.0 ** -24, "e4m3": 2.0 ** -4, "e5m2": 2.0 ** -3}
 # half the spacing of the smallest numbers: what rounding costs however small the value is
 TINY = {"f16": 2.0 ** -25, "bf16": 2.0 ** -134, "f32": 2.0 ** -150, "e4m3": 2.0 ** -10, "e5m2": 2.0 ** -17}
-QMAX = {"e4m3": 448.0, "e5m2": 57344.0}
+QMAX = {"e4m3": 448.0, "e5m2": 57344.0, "i8": 127.0}
 AMAX_FLOOR = 2.0 ** -100
 U32 = 2.0 ** -24
 
@@ -153,3 +153,57 @@ def norm_backward(dY, H, w, rstd, dH, out):
     dw = (dY * xh).sum(axis=0)
     dwerr = (H.shape[0] + 8) * 2 * U32 * np.abs(dY * xh).sum(axis=0) + 2.0 ** -140
     return dX, err * (1 + h) + h * np.abs(dX) + TINY[out], dw, dwerr
+
+
+def layer_norm(H, w, b, eps):
+    """(Y, mean, rstd, bound of Y, bound of mean, relative bound of rstd) of the rows of H, in fp32.
+
+    The mean carries its sum's rounding: e = (cols+8)·2^-23 of the mean magnitude at most.  The deviations
+    carry e and their own rounding; their mean square, to first order, 2·(rounding) relative, the additions'
+    (cols+8)·2^-23 and e² (a shift of the centre adds its square), rstd half of it all and a root's and a
+    division's rounding."""
+    cols = H.shape[1]
+    mean = H.mean(axis=1)
+    d = H - mean[:, None]
+    var = np.mean(d * d, axis=1)
+    rstd = 1.0 / np.sqrt(var + eps)
+    merr = (cols + 8) * 2 * U32 * np.mean(np.abs(H), axis=1) + U32 * np.abs(mean)
+    # rounding of a deviation is relative to it; its root mean square bounds the mean's effect
+    rel = 0.5 * ((cols + 8) * 2 * U32 + 4 * U32) + 0.5 * (merr * rstd) ** 2 + U32 * merr * rstd + 6 * U32
+    xh = d * rstd[:, None]
+    Y = xh * w[None, :]
+    err = (merr * rstd)[:, None] * np.abs(w)[None, :] + (rel[:, None] + 4 * U32) * np.abs(Y)
+    if b is not None:
+        Y = Y + b[None, :]
+        err = err + U32 * (np.abs(Y) + err)
+    return Y, mean, rstd, err, merr, rel
+
+
+def layer_norm_backward(dY, H, w, mean, rstd, dH, out):
+    """(dX, bound, dw, bound, db, bound)."""
+    cols = H.shape[1]
+    d = H - mean[:, None]
+    xh = d * rstd[:, None]
+    xerr = 3 * U32 * np.abs(xh)
+    g = dY * w[None, :]
+    gm, c = np.mean(g, axis=1), np.mean(g * xh, axis=1)
+    s = (cols + 8) * 2 * U32
+    gmerr = s * np.mean(np.abs(g), axis=1)
+    cerr = (s + 4 * U32) * np.mean(np.abs(g * xh), axis=1)
+    dX = rstd[:, None] * (g - gm[:, None] - xh * c[:, None])
+    err = np.abs(rstd[:, None]) * (6 * U32 * (np.abs(g) + np.abs(gm[:, None]) + np.abs(xh * c[:, None])) + gmerr[:, None]
+                                   + np.abs(xh) * cerr[:, None] + xerr * np.abs(c[:, None]))
+    if dH is not None:
+        dX = dX + dH
+        err = err + U32 * (np.abs(dX) + err)
+    h = HALF_STEP[out]
+    rows = (H.shape[0] + 8) * 2 * U32
+    dw, db = (dY * xh).sum(axis=0), dY.sum(axis=0)
+    return (dX, err * (1 + h) + h * np.abs(dX) + TINY[out], dw, (rows + 4 * U32) * np.abs(dY * xh).sum(axis=0) + 2.0 ** -140,
+            db, rows * np.abs(dY).sum(axis=0) + 2.0 ** -140)
+
+
+def quantised_rows(X, fmt):
+    """(codes before their rounding, scales): the scale is an fp32 quotient, and the codes are X by it."""
+    s = (np.maximum(np.abs(X).max(axis=1), AMAX_FLOOR).astype(np.float32) / np.float32(QMAX[fmt])).astype(np.float64)
+    return X / s[:, None], s

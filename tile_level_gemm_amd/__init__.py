@@ -179,6 +179,10 @@ _SIGS = {
     "tile_rmsnorm_bwd": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _I64, _I64,
                                 _INT, _INT, _VP, _I64, _VP]),
     "tile_rmsnorm_bwd_workspace": (_I64, [_I64, _I64, _INT]),
+    "tile_layernorm": (_INT, [_VP] * 9 + [_I64] * 6 + [_F, _INT, _INT, _INT, _INT, _VP]),
+    "tile_layernorm_bwd": (_INT, [_VP] * 9 + [_I64] * 6 + [_INT, _INT, _VP, _I64, _VP]),
+    "tile_layernorm_bwd_workspace": (_I64, [_I64, _I64, _INT]),
+    "tile_quantize_rows": (_INT, [_VP] * 3 + [_I64] * 4 + [_INT, _INT, _INT, _VP]),
     "tile_last_error": (ctypes.c_char_p, []),
     "tile_abi_version": (_INT, []),
 }
@@ -665,14 +669,19 @@ def tile_gemm_ep_bwd_workspace(M, N, K, transA, transB, dtype):
     return lib().tile_gemm_ep_bwd_workspace(M, N, K, int(transA), int(transB), int(dtype))
 
 
+def _scale_bytes(rows, cols, kind):
+    """Bytes of the scales of 8-bit rows."""
+    return rows * 4 if int(kind) == TG_SCALE_ROW else rows * (cols // 32) if int(kind) == TG_SCALE_BLOCK else 0
+
+
 def tile_rmsnorm(X, R, W, H, Y, S, rstd, rows, cols, eps, dtype, w_dtype, y_dtype, scale_kind, *, ld_x=0,
                  ld_r=0, ld_h=0, ld_y=0, stream=None):
     """H = X + R, Y = H·rstd·W, optionally in 8 bits with scales S (see include/tilegemm.h)."""
     e, ew, ey = ELEM_BYTES.get(int(dtype), 1), ELEM_BYTES.get(int(w_dtype), 1), ELEM_BYTES.get(int(y_dtype), 1)
     m, n = max(int(rows), 0), max(int(cols), 0)
-    sb = m * 4 if int(scale_kind) == TG_SCALE_ROW else m * (n // 32) if int(scale_kind) == TG_SCALE_BLOCK else 0
     p = _ptrs(_matrix("X", X, m, n, ld_x, e), _matrix("R", R, m, n, ld_r, e), ("W", W, ew, n * ew),
-              _matrix("H", H, m, n, ld_h, e), _matrix("Y", Y, m, n, ld_y, ey), ("S", S, None, sb),
+              _matrix("H", H, m, n, ld_h, e), _matrix("Y", Y, m, n, ld_y, ey),
+              ("S", S, None, _scale_bytes(m, n, scale_kind)),
               ("rstd", rstd, 4, m * 4))
     _check(lib().tile_rmsnorm(*p, rows, cols, int(ld_x), int(ld_r), int(ld_h), int(ld_y), float(eps),
                               int(dtype), int(w_dtype), int(y_dtype), int(scale_kind), _stream(stream)))
@@ -693,6 +702,46 @@ def tile_rmsnorm_bwd(dY, H, W, rstd, dH, dX, dW, rows, cols, dtype, w_dtype, *, 
 
 def tile_rmsnorm_bwd_workspace(rows, cols, dtype):
     return lib().tile_rmsnorm_bwd_workspace(rows, cols, int(dtype))
+
+
+def tile_layernorm(X, R, W, bias, H, Y, S, mean, rstd, rows, cols, eps, dtype, w_dtype, y_dtype, scale_kind, *,
+                   ld_x=0, ld_r=0, ld_h=0, ld_y=0, stream=None):
+    """H = X + R, Y = (H - mean)·rstd·W + bias, optionally in 8 bits with scales S (see include/tilegemm.h)."""
+    e, ew, ey = ELEM_BYTES.get(int(dtype), 1), ELEM_BYTES.get(int(w_dtype), 1), ELEM_BYTES.get(int(y_dtype), 1)
+    m, n = max(int(rows), 0), max(int(cols), 0)
+    p = _ptrs(_matrix("X", X, m, n, ld_x, e), _matrix("R", R, m, n, ld_r, e), ("W", W, ew, n * ew),
+              ("bias", bias, ew, n * ew), _matrix("H", H, m, n, ld_h, e), _matrix("Y", Y, m, n, ld_y, ey),
+              ("S", S, None, _scale_bytes(m, n, scale_kind)), ("mean", mean, 4, m * 4), ("rstd", rstd, 4, m * 4))
+    _check(lib().tile_layernorm(*p, rows, cols, int(ld_x), int(ld_r), int(ld_h), int(ld_y), float(eps), int(dtype),
+                                int(w_dtype), int(y_dtype), int(scale_kind), _stream(stream)))
+
+
+def tile_layernorm_bwd(dY, H, W, mean, rstd, dH, dX, dW, dbias, rows, cols, dtype, w_dtype, *, ld_dy=0, ld_h=0,
+                       ld_dh=0, ld_dx=0, workspace=None, workspace_bytes=None, stream=None):
+    """Gradients of tile_layernorm (see include/tilegemm.h)."""
+    e, ew = ELEM_BYTES.get(int(dtype), 1), ELEM_BYTES.get(int(w_dtype), 1)
+    m, n = max(int(rows), 0), max(int(cols), 0)
+    nb = _workspace_bytes(workspace, workspace_bytes)
+    p = _ptrs(_matrix("dY", dY, m, n, ld_dy, e), _matrix("H", H, m, n, ld_h, e), ("W", W, ew, n * ew),
+              ("mean", mean, 4, m * 4), ("rstd", rstd, 4, m * 4), _matrix("dH", dH, m, n, ld_dh, e),
+              _matrix("dX", dX, m, n, ld_dx, e), ("dW", dW, 4, n * 4), ("dbias", dbias, 4, n * 4),
+              ("workspace", workspace, None, nb))
+    _check(lib().tile_layernorm_bwd(*p[:9], rows, cols, int(ld_dy), int(ld_h), int(ld_dh), int(ld_dx), int(dtype),
+                                    int(w_dtype), p[9], nb, _stream(stream)))
+
+
+def tile_layernorm_bwd_workspace(rows, cols, dtype):
+    return lib().tile_layernorm_bwd_workspace(rows, cols, int(dtype))
+
+
+def tile_quantize_rows(X, Y, S, rows, cols, dtype, y_dtype, scale_kind, *, ld_x=0, ld_y=0, stream=None):
+    """X in 8 bits with scales S (see include/tilegemm.h)."""
+    e, ey = ELEM_BYTES.get(int(dtype), 1), ELEM_BYTES.get(int(y_dtype), 1)
+    m, n = max(int(rows), 0), max(int(cols), 0)
+    p = _ptrs(_matrix("X", X, m, n, ld_x, e), _matrix("Y", Y, m, n, ld_y, ey),
+              ("S", S, None, _scale_bytes(m, n, scale_kind)))
+    _check(lib().tile_quantize_rows(*p, rows, cols, int(ld_x), int(ld_y), int(dtype), int(y_dtype), int(scale_kind),
+                                    _stream(stream)))
 
 
 class _On:
@@ -781,19 +830,23 @@ class Norm:
 _SCALES = {None: TG_SCALE_NONE, "row": TG_SCALE_ROW, "block": TG_SCALE_BLOCK}
 
 
-def rms_norm(X, weight, eps=1e-5, residual=None, out_dtype=None, scales=None, h_out=None, stream=None):
-    """h = X + residual, y = h·rstd·weight; returns a Norm.
-
-    scales None: y in X's dtype.  "row": y in 8 bits (out_dtype, float8_e4m3fn by default) with one
-    float32 scale a row, gemm_ep's row_scale.  "block": with an E8M0 scale per 32 columns,
-    tile_gemm_mx's SA.  h_out may be X or residual (in place)."""
-    if stream is not None:
-        with _On(stream):
-            return rms_norm(X, weight, eps, residual, out_dtype, scales, h_out)
+def _scale_kind(scales):
     kind = _SCALES.get(scales)
     if kind is None:
         raise TileError(TG_E_ARG, f"scales must be None, 'row' or 'block', got {scales!r}")
-    return Norm(*(_calls or _native()).rms_norm(X, weight, eps, residual, out_dtype, kind, h_out))
+    return kind
+
+
+def rms_norm(X, weight, eps=1e-5, residual=None, out_dtype=None, scales=None, h_out=None, stream=None):
+    """h = X + residual, y = h·rstd·weight; returns a Norm.
+
+    scales None: y in X's dtype.  "row": y in 8 bits (out_dtype: float8_e4m3fn by default, float8_e5m2
+    or int8) with one float32 scale a row, gemm_ep's row_scale.  "block": float8 with an E8M0 scale per
+    32 columns, tile_gemm_mx's SA.  h_out may be X or residual (in place)."""
+    if stream is not None:
+        with _On(stream):
+            return rms_norm(X, weight, eps, residual, out_dtype, scales, h_out)
+    return Norm(*(_calls or _native()).rms_norm(X, weight, eps, residual, out_dtype, _scale_kind(scales), h_out))
 
 
 def rms_norm_backward(dY, h, weight, rstd, dH=None, need_dw=True, stream=None):
@@ -803,3 +856,46 @@ def rms_norm_backward(dY, h, weight, rstd, dH=None, need_dw=True, stream=None):
         with _On(stream):
             return rms_norm_backward(dY, h, weight, rstd, dH, need_dw)
     return (_calls or _native()).rms_norm_backward(dY, h, weight, rstd, dH, need_dw)
+
+
+class LayerNorm(Norm):
+    """Result of layer_norm: a Norm with the rows' means."""
+    __slots__ = ("mean",)
+
+    def __init__(self, y, scale, mean, rstd, h):
+        super().__init__(y, scale, rstd, h)
+        self.mean = mean
+
+
+def layer_norm(X, weight, bias=None, eps=1e-5, residual=None, out_dtype=None, scales=None, h_out=None, stream=None):
+    """h = X + residual, y = (h - mean)·rstd·weight + bias; returns a LayerNorm.
+
+    weight and bias have one type, X's or float32.  out_dtype, scales and h_out as for rms_norm."""
+    if stream is not None:
+        with _On(stream):
+            return layer_norm(X, weight, bias, eps, residual, out_dtype, scales, h_out)
+    return LayerNorm(*(_calls or _native()).layer_norm(X, weight, bias, eps, residual, out_dtype, _scale_kind(scales), h_out))
+
+
+def layer_norm_backward(dY, h, weight, mean, rstd, dH=None, need_dw=True, need_dbias=True, stream=None):
+    """Gradients of layer_norm: (dX, dweight, dbias), None for what is not needed.  dX is the gradient of X
+    and of the residual; dH, if given, is the gradient that arrives at h by the residual stream.  dweight
+    and dbias are float32."""
+    if stream is not None:
+        with _On(stream):
+            return layer_norm_backward(dY, h, weight, mean, rstd, dH, need_dw, need_dbias)
+    return (_calls or _native()).layer_norm_backward(dY, h, weight, mean, rstd, dH, need_dw, need_dbias)
+
+
+def quantize_rows(X, out_dtype=torch.int8, scales="row", stream=None):
+    """X in 8 bits: (q, scale) with X ~ q·scale, for the 8-bit products.
+
+    scales "row": int8, float8_e4m3fn or float8_e5m2 with one float32 scale a row (gemm_ep's row_scale for
+    an activation, col_scale for a weight [N, K]).  "block": float8 with an E8M0 scale per 32 columns
+    (tile_gemm_mx's SA, SB)."""
+    if stream is not None:
+        with _On(stream):
+            return quantize_rows(X, out_dtype, scales)
+    if scales is None:
+        raise TileError(TG_E_ARG, "scales must be 'row' or 'block', got None")
+    return (_calls or _native()).quantize_rows(X, out_dtype, _scale_kind(scales))

@@ -64,8 +64,9 @@ struct ActGradArgs {
   int32_t t, act;
 };
 hipError_t launch_act_grad(const ActGradArgs& a, int groups, hipStream_t s);
-// out[n] = sum_g part[g][n]
-hipError_t launch_sum_rows(const float* part, int64_t G, int64_t N, float* out, hipStream_t s);
+// out[n] = sum_g part[g][n]; columns from `split` on go to rest[n - split]
+hipError_t launch_sum_rows(const float* part, int64_t G, int64_t N, float* out, hipStream_t s,
+                           float* rest = nullptr, int64_t split = INT64_MAX);
 
 // one orientation per translation unit (ep_gemm_*.hip)
 hipError_t launch_ep_kk(const EpArgs& g, int dtype, const EpKernel& k, hipStream_t s);

@@ -118,7 +118,7 @@ __global__ __launch_bounds__(8 * RL) void act_grad(ActGradArgs a) {
 // out[n] = sum over g of part[g][n]: 32 columns x 32 interleaved row lanes per workgroup, joined in
 // LDS, always in the same order.  Many lanes a column: the loads wait on memory, not on each other
 // (512 rows of 8192 columns: 16 loads a thread).
-__global__ __launch_bounds__(1024) void sum_rows(const float* part, int64_t G, int64_t N, float* out) {
+__global__ __launch_bounds__(1024) void sum_rows(const float* part, int64_t G, int64_t N, float* out, float* rest, int64_t split) {
   __shared__ float red[32][33];
   const int c = (int)threadIdx.x & 31, l = (int)threadIdx.x >> 5;
   const int64_t first = wide_block() * 32, n = first + c;
@@ -135,7 +135,7 @@ __global__ __launch_bounds__(1024) void sum_rows(const float* part, int64_t G, i
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) s += __shfl_xor(s, m);
   const int64_t o = first + l;
-  if (c == 0 && o < N) out[o] = s;
+  if (c == 0 && o < N) *(o < split ? out + o : rest + (o - split)) = s;
 }
 
 }  // namespace
@@ -162,8 +162,8 @@ hipError_t launch_act_grad(const ActGradArgs& a, int groups, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_sum_rows(const float* part, int64_t G, int64_t N, float* out, hipStream_t s) {
-  hipLaunchKernelGGL(sum_rows, wide_grid((N + 31) / 32), dim3(1024), 0, s, part, G, N, out);
+hipError_t launch_sum_rows(const float* part, int64_t G, int64_t N, float* out, hipStream_t s, float* rest, int64_t split) {
+  hipLaunchKernelGGL(sum_rows, wide_grid((N + 31) / 32), dim3(1024), 0, s, part, G, N, out, rest, split);
   return hipGetLastError();
 }
 

@@ -1,5 +1,5 @@
-// C-ABI entry points of the layer operators (product with an epilogue, RMS norm, their backward
-// passes): argument validation, planning and launch.  Every check runs before any HIP call.
+// C-ABI entry points of the layer operators (products with an epilogue, norms, their backward
+// passes, quantised rows): argument validation, planning and launch.  Every check runs before any HIP call.
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
@@ -322,6 +322,157 @@ int64_t norm_groups(int64_t rows, int64_t cols) {
   return std::max<int64_t>(1, std::min<int64_t>((rows + per - 1) / per, most));
 }
 
+// ---------------------------------------------------------------------------- the norms ----
+
+const char* const kNormName[] = {"tile_rmsnorm", "tile_layernorm", "tile_quantize_rows"};
+const char* const kNormBwdName[] = {"tile_rmsnorm_bwd", "tile_layernorm_bwd"};
+
+int run_norm(NormKind kind, const void* X, const void* R, const void* W, const void* B, void* H, void* Y, void* S,
+             float* mean, float* rstd, int64_t rows, int64_t cols, int64_t ld_x, int64_t ld_r, int64_t ld_h,
+             int64_t ld_y, float eps, int dtype, int w_dtype, int y_dtype, int scale_kind, void* stream) {
+  clear_error();
+  if (rows < 0 || rows > kMaxDim || cols < 1 || cols > kMaxDim)
+    return fail(TG_E_SHAPE, fmt("rows must be 0 .. 2^30 and cols 1 .. 2^30 (got %lld, %lld)", rows, cols));
+  if (!is_float(dtype)) return fail(TG_E_DTYPE, fmt("dtype must be TG_F16, TG_BF16 or TG_F32 (got %lld)", dtype));
+  if (w_dtype != dtype && w_dtype != TG_F32) return fail(TG_E_DTYPE, "w_dtype must be dtype or TG_F32");
+  if (scale_kind < TG_SCALE_NONE || scale_kind > TG_SCALE_BLOCK)
+    return fail(TG_E_ARG, fmt("unknown scale kind %lld", scale_kind));
+  if (kind == kRows && scale_kind == TG_SCALE_NONE) return fail(TG_E_ARG, "quantised rows need scales: TG_SCALE_ROW or TG_SCALE_BLOCK");
+  if (scale_kind == TG_SCALE_NONE    ? y_dtype != dtype
+      : scale_kind == TG_SCALE_BLOCK ? !isf8(y_dtype)
+                                     : !is8(y_dtype))
+    return fail(TG_E_DTYPE, "y_dtype must be dtype without scales, TG_FP8_E4M3 or TG_FP8_E5M2 with them, or TG_I8 with row scales");
+  if (scale_kind == TG_SCALE_BLOCK && cols % 32)
+    return fail(TG_E_SHAPE, fmt("block scales need cols %% 32 == 0 (got %lld)", cols));
+  if (!(eps >= 0.0f) || std::isinf(eps)) return fail(TG_E_ARG, "eps must be finite and not negative");
+  if (H && !R) return fail(TG_E_ARG, "H is the sum X + R: it needs R");
+  int st;
+  if ((st = resolve_ld("ld_x", &ld_x, cols, rows)) || (st = resolve_ld("ld_r", &ld_r, cols, rows)) ||
+      (st = resolve_ld("ld_h", &ld_h, cols, rows)) || (st = resolve_ld("ld_y", &ld_y, cols, rows)))
+    return st;
+  if (rows == 0) return TG_OK;
+  if (!X || (!W && kind != kRows) || !Y) return fail(TG_E_NULL, kind == kRows ? "X or Y is NULL" : "X, W or Y is NULL");
+  if (scale_kind != TG_SCALE_NONE && !S) return fail(TG_E_NULL, "scales need S");
+  const int eb = bytes_of(dtype), yb = bytes_of(y_dtype), wb = bytes_of(w_dtype);
+  if (misaligned(X, eb) || misaligned(R, eb) || misaligned(H, eb) || misaligned(Y, yb) || misaligned(W, wb) ||
+      misaligned(B, wb) || misaligned(mean, 4) || misaligned(rstd, 4) || (scale_kind == TG_SCALE_ROW && misaligned(S, 4)))
+    return fail(TG_E_ALIGN, "a pointer is not aligned to its element");
+  const Mat mx = mat(X, rows, cols, ld_x, eb), mr = mat(R, rows, cols, ld_r, eb), mh = mat(H, rows, cols, ld_h, eb);
+  const Mat outs[] = {mat(Y, rows, cols, ld_y, yb), vec(rstd, rows, 4),
+                      scale_kind == TG_SCALE_ROW ? vec(S, rows, 4)
+                      : scale_kind == TG_SCALE_BLOCK ? vec(S, rows * (cols / 32), 1) : Mat{}, vec(mean, rows, 4)};
+  const Mat mw = vec(W, cols, wb), mb = vec(B, cols, wb);
+  for (int i = 0; i < 4; ++i) {
+    if (overlaps(outs[i], mx) || overlaps(outs[i], mr) || overlaps(outs[i], mw) || overlaps(outs[i], mb) || overlaps(outs[i], mh))
+      return fail(TG_E_ALIAS, "an output overlaps an input or H");
+    for (int j = i + 1; j < 4; ++j)
+      if (overlaps(outs[i], outs[j])) return fail(TG_E_ALIAS, "outputs overlap each other");
+  }
+  if ((overlaps(mh, mx) && !same(mh, mx)) || (overlaps(mh, mr) && !same(mh, mr)) || overlaps(mh, mw) || overlaps(mh, mb))
+    return fail(TG_E_ALIAS, "H overlaps an input without being exactly X or R");
+  NormArgs a{};
+  a.X = (const uint8_t*)X;
+  a.R = (const uint8_t*)R;
+  a.W = (const uint8_t*)W;
+  a.B = (const uint8_t*)B;
+  a.H = (uint8_t*)H;
+  a.Y = (uint8_t*)Y;
+  a.S = (uint8_t*)S;
+  a.rstd = rstd;
+  a.mean = mean;
+  a.rows = rows;
+  a.cols = cols;
+  a.ldx = ld_x;
+  a.ldr = ld_r;
+  a.ldh = ld_h;
+  a.ldy = ld_y;
+  a.eps = eps;
+  a.w_t = w_dtype;
+  a.y_t = y_dtype;
+  hipStream_t s = (hipStream_t)stream;
+  return hip_status(kNormName[kind], kind == kRms     ? launch_rmsnorm(a, dtype, scale_kind, s)
+                                     : kind == kLayer ? launch_layernorm(a, dtype, scale_kind, s)
+                                                      : launch_quantize_rows(a, dtype, scale_kind, s));
+}
+
+// Two-pass rows: bytes that hold each row's means (kLayer has two), before the shares of the weights' gradients.
+int64_t norm_dots(NormKind kind, int64_t rows, int64_t cols) {
+  return norm_in_registers(cols) ? 0 : rows * (kind == kLayer ? 8 : 4);
+}
+
+int64_t norm_bwd_workspace(NormKind kind, int64_t rows, int64_t cols, int dtype) {
+  if (rows < 0 || rows > kMaxDim || cols < 1 || cols > kMaxDim || !is_float(dtype)) return 0;
+  const int64_t g = norm_groups(rows, cols);
+  return (norm_dots(kind, rows, cols) + 15) / 16 * 16 + (g > 1 ? g * cols * (kind == kLayer ? 8 : 4) : 0);
+}
+
+int run_norm_bwd(NormKind kind, const void* dY, const void* H, const void* W, const float* mean, const float* rstd,
+                 const void* dH, void* dX, float* dW, float* dB, int64_t rows, int64_t cols, int64_t ld_dy, int64_t ld_h,
+                 int64_t ld_dh, int64_t ld_dx, int dtype, int w_dtype, void* workspace, int64_t workspace_bytes,
+                 void* stream) {
+  clear_error();
+  if (rows < 0 || rows > kMaxDim || cols < 1 || cols > kMaxDim)
+    return fail(TG_E_SHAPE, fmt("rows must be 0 .. 2^30 and cols 1 .. 2^30 (got %lld, %lld)", rows, cols));
+  if (!is_float(dtype)) return fail(TG_E_DTYPE, fmt("dtype must be TG_F16, TG_BF16 or TG_F32 (got %lld)", dtype));
+  if (w_dtype != dtype && w_dtype != TG_F32) return fail(TG_E_DTYPE, "w_dtype must be dtype or TG_F32");
+  int st;
+  if ((st = resolve_ld("ld_dy", &ld_dy, cols, rows)) || (st = resolve_ld("ld_h", &ld_h, cols, rows)) ||
+      (st = resolve_ld("ld_dh", &ld_dh, cols, rows)) || (st = resolve_ld("ld_dx", &ld_dx, cols, rows)))
+    return st;
+  if ((st = check_workspace(workspace, workspace_bytes))) return st;
+  hipStream_t s = (hipStream_t)stream;
+  if (rows > 0 && (!dY || !H || !W || !rstd || !dX)) return fail(TG_E_NULL, "dY, H, W, rstd or dX is NULL");
+  if (rows > 0 && kind == kLayer && !mean) return fail(TG_E_NULL, "mean is NULL");
+  const int eb = bytes_of(dtype);
+  if (misaligned(dY, eb) || misaligned(H, eb) || misaligned(dH, eb) || misaligned(dX, eb) ||
+      misaligned(W, bytes_of(w_dtype)) || misaligned(mean, 4) || misaligned(rstd, 4) || misaligned(dW, 4) || misaligned(dB, 4))
+    return fail(TG_E_ALIGN, "a pointer is not aligned to its element");
+  const Mat my = mat(dY, rows, cols, ld_dy, eb), mdh = mat(dH, rows, cols, ld_dh, eb), mdx = mat(dX, rows, cols, ld_dx, eb);
+  const Mat mdw = vec(dW, cols, 4), mdb = vec(dB, cols, 4), mws = vec(workspace, workspace_bytes, 1);
+  const Mat ins[] = {my, mat(H, rows, cols, ld_h, eb), mdh, vec(W, cols, bytes_of(w_dtype)), vec(rstd, rows, 4), vec(mean, rows, 4)};
+  for (int i = 0; i < 6; ++i) {
+    if (overlaps(mdw, ins[i]) || overlaps(mdb, ins[i]) || overlaps(mws, ins[i]))
+      return fail(TG_E_ALIAS, "dW, dbias or the workspace overlaps an input");
+    if (overlaps(mdx, ins[i]) && !((i == 0 && same(mdx, my)) || (i == 2 && same(mdx, mdh))))
+      return fail(TG_E_ALIAS, "dX overlaps an input without being exactly dY or dH");
+  }
+  if (overlaps(mdx, mdw) || overlaps(mdx, mdb) || overlaps(mdx, mws) || overlaps(mdw, mws) || overlaps(mdb, mws) || overlaps(mdw, mdb))
+    return fail(TG_E_ALIAS, "dX, dW, dbias and the workspace must not overlap");
+  const int64_t least = norm_dots(kind, rows, cols), dots = (least + 15) / 16 * 16;   // rounded up for the shares behind it
+  if (workspace_bytes < least)
+    return fail(TG_E_ARG, fmt("rows of %lld columns need a workspace of at least %lld bytes", cols, least));
+  if (rows == 0) {   // sums of nothing
+    if (dW && (st = hip_status(kNormBwdName[kind], launch_sum_rows(dW, 0, cols, dW, s)))) return st;
+    return dB ? hip_status(kNormBwdName[kind], launch_sum_rows(dB, 0, cols, dB, s)) : TG_OK;
+  }
+  NormBwdArgs a{};
+  a.dY = (const uint8_t*)dY;
+  a.H = (const uint8_t*)H;
+  a.W = (const uint8_t*)W;
+  a.rstd = rstd;
+  a.mean = mean;
+  a.dH = (const uint8_t*)dH;
+  a.dX = (uint8_t*)dX;
+  a.rows = rows;
+  a.cols = cols;
+  a.ldy = ld_dy;
+  a.ldh = ld_h;
+  a.ldd = ld_dh;
+  a.ldx = ld_dx;
+  a.w_t = w_dtype;
+  a.dot = dots ? (float*)workspace : nullptr;
+  int64_t groups = norm_groups(rows, cols);
+  float* part = (float*)((uint8_t*)workspace + dots);
+  a.share_ld = cols * ((dW != nullptr) + (dB != nullptr));   // a workgroup's shares, dW's first
+  if (a.share_ld) groups = std::max<int64_t>(1, std::min(groups, (workspace_bytes - dots) / (4 * a.share_ld)));
+  a.dw = !dW ? nullptr : groups > 1 ? part : dW;
+  a.db = !dB ? nullptr : groups > 1 ? part + (dW ? cols : 0) : dB;
+  hipError_t e = kind == kRms ? launch_rmsnorm_bwd(a, dtype, groups, s) : launch_layernorm_bwd(a, dtype, groups, s);
+  if ((st = hip_status(kNormBwdName[kind], e)) || !a.share_ld || groups == 1) return st;
+  e = dW ? launch_sum_rows(part, groups, a.share_ld, dW, s, dB, cols) : launch_sum_rows(part, groups, cols, dB, s);
+  return hip_status(kNormBwdName[kind], e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -481,128 +632,45 @@ int tile_gemm_ep_bwd_scaled(const void* dY, const void* Z, const void* A, const 
 int tile_rmsnorm(const void* X, const void* R, const void* W, void* H, void* Y, void* S, float* rstd,
                  int64_t rows, int64_t cols, int64_t ld_x, int64_t ld_r, int64_t ld_h, int64_t ld_y, float eps,
                  int dtype, int w_dtype, int y_dtype, int scale_kind, void* stream) {
-  clear_error();
-  if (rows < 0 || rows > kMaxDim || cols < 1 || cols > kMaxDim)
-    return fail(TG_E_SHAPE, fmt("rows must be 0 .. 2^30 and cols 1 .. 2^30 (got %lld, %lld)", rows, cols));
-  if (!is_float(dtype)) return fail(TG_E_DTYPE, fmt("dtype must be TG_F16, TG_BF16 or TG_F32 (got %lld)", dtype));
-  if (w_dtype != dtype && w_dtype != TG_F32) return fail(TG_E_DTYPE, "w_dtype must be dtype or TG_F32");
-  if (scale_kind < TG_SCALE_NONE || scale_kind > TG_SCALE_BLOCK)
-    return fail(TG_E_ARG, fmt("unknown scale kind %lld", scale_kind));
-  if (scale_kind == TG_SCALE_NONE ? y_dtype != dtype : !isf8(y_dtype))
-    return fail(TG_E_DTYPE, "y_dtype must be dtype without scales, TG_FP8_E4M3 or TG_FP8_E5M2 with them");
-  if (scale_kind == TG_SCALE_BLOCK && cols % 32)
-    return fail(TG_E_SHAPE, fmt("block scales need cols %% 32 == 0 (got %lld)", cols));
-  if (!(eps >= 0.0f) || std::isinf(eps)) return fail(TG_E_ARG, "eps must be finite and not negative");
-  if (H && !R) return fail(TG_E_ARG, "H is the sum X + R: it needs R");
-  int st;
-  if ((st = resolve_ld("ld_x", &ld_x, cols, rows)) || (st = resolve_ld("ld_r", &ld_r, cols, rows)) ||
-      (st = resolve_ld("ld_h", &ld_h, cols, rows)) || (st = resolve_ld("ld_y", &ld_y, cols, rows)))
-    return st;
-  if (rows == 0) return TG_OK;
-  if (!X || !W || !Y) return fail(TG_E_NULL, "X, W or Y is NULL");
-  if (scale_kind != TG_SCALE_NONE && !S) return fail(TG_E_NULL, "scales need S");
-  const int eb = bytes_of(dtype), yb = bytes_of(y_dtype);
-  if (misaligned(X, eb) || misaligned(R, eb) || misaligned(H, eb) || misaligned(Y, yb) ||
-      misaligned(W, bytes_of(w_dtype)) || misaligned(rstd, 4) || (scale_kind == TG_SCALE_ROW && misaligned(S, 4)))
-    return fail(TG_E_ALIGN, "a pointer is not aligned to its element");
-  const Mat mx = mat(X, rows, cols, ld_x, eb), mr = mat(R, rows, cols, ld_r, eb), mh = mat(H, rows, cols, ld_h, eb);
-  const Mat outs[] = {mat(Y, rows, cols, ld_y, yb), vec(rstd, rows, 4),
-                      scale_kind == TG_SCALE_ROW ? vec(S, rows, 4)
-                      : scale_kind == TG_SCALE_BLOCK ? vec(S, rows * (cols / 32), 1) : Mat{}};
-  const Mat mw = vec(W, cols, bytes_of(w_dtype));
-  for (int i = 0; i < 3; ++i) {
-    if (overlaps(outs[i], mx) || overlaps(outs[i], mr) || overlaps(outs[i], mw) || overlaps(outs[i], mh))
-      return fail(TG_E_ALIAS, "an output overlaps an input or H");
-    for (int j = i + 1; j < 3; ++j)
-      if (overlaps(outs[i], outs[j])) return fail(TG_E_ALIAS, "outputs overlap each other");
-  }
-  if ((overlaps(mh, mx) && !same(mh, mx)) || (overlaps(mh, mr) && !same(mh, mr)) || overlaps(mh, mw))
-    return fail(TG_E_ALIAS, "H overlaps an input without being exactly X or R");
-  NormArgs a{};
-  a.X = (const uint8_t*)X;
-  a.R = (const uint8_t*)R;
-  a.W = (const uint8_t*)W;
-  a.H = (uint8_t*)H;
-  a.Y = (uint8_t*)Y;
-  a.S = (uint8_t*)S;
-  a.rstd = rstd;
-  a.rows = rows;
-  a.cols = cols;
-  a.ldx = ld_x;
-  a.ldr = ld_r;
-  a.ldh = ld_h;
-  a.ldy = ld_y;
-  a.eps = eps;
-  a.w_t = w_dtype;
-  a.y_t = y_dtype;
-  return hip_status("tile_rmsnorm", launch_rmsnorm(a, dtype, scale_kind, (hipStream_t)stream));
+  return run_norm(kRms, X, R, W, nullptr, H, Y, S, nullptr, rstd, rows, cols, ld_x, ld_r, ld_h, ld_y, eps, dtype,
+                  w_dtype, y_dtype, scale_kind, stream);
+}
+
+int tile_layernorm(const void* X, const void* R, const void* W, const void* bias, void* H, void* Y, void* S,
+                   float* mean, float* rstd, int64_t rows, int64_t cols, int64_t ld_x, int64_t ld_r, int64_t ld_h,
+                   int64_t ld_y, float eps, int dtype, int w_dtype, int y_dtype, int scale_kind, void* stream) {
+  return run_norm(kLayer, X, R, W, bias, H, Y, S, mean, rstd, rows, cols, ld_x, ld_r, ld_h, ld_y, eps, dtype, w_dtype,
+                  y_dtype, scale_kind, stream);
+}
+
+int tile_quantize_rows(const void* X, void* Y, void* S, int64_t rows, int64_t cols, int64_t ld_x, int64_t ld_y,
+                       int dtype, int y_dtype, int scale_kind, void* stream) {
+  return run_norm(kRows, X, nullptr, nullptr, nullptr, nullptr, Y, S, nullptr, nullptr, rows, cols, ld_x, 0, 0, ld_y,
+                  0.0f, dtype, dtype, y_dtype, scale_kind, stream);
 }
 
 int64_t tile_rmsnorm_bwd_workspace(int64_t rows, int64_t cols, int dtype) {
-  if (rows < 0 || rows > kMaxDim || cols < 1 || cols > kMaxDim || !is_float(dtype)) return 0;
-  const int64_t g = norm_groups(rows, cols);
-  const int64_t dots = norm_in_registers(cols) ? 0 : (rows * 4 + 15) / 16 * 16;
-  return dots + (g > 1 ? g * cols * 4 : 0);
+  return norm_bwd_workspace(kRms, rows, cols, dtype);
 }
 
 int tile_rmsnorm_bwd(const void* dY, const void* H, const void* W, const float* rstd, const void* dH, void* dX,
                      float* dW, int64_t rows, int64_t cols, int64_t ld_dy, int64_t ld_h, int64_t ld_dh,
                      int64_t ld_dx, int dtype, int w_dtype, void* workspace, int64_t workspace_bytes,
                      void* stream) {
-  clear_error();
-  if (rows < 0 || rows > kMaxDim || cols < 1 || cols > kMaxDim)
-    return fail(TG_E_SHAPE, fmt("rows must be 0 .. 2^30 and cols 1 .. 2^30 (got %lld, %lld)", rows, cols));
-  if (!is_float(dtype)) return fail(TG_E_DTYPE, fmt("dtype must be TG_F16, TG_BF16 or TG_F32 (got %lld)", dtype));
-  if (w_dtype != dtype && w_dtype != TG_F32) return fail(TG_E_DTYPE, "w_dtype must be dtype or TG_F32");
-  int st;
-  if ((st = resolve_ld("ld_dy", &ld_dy, cols, rows)) || (st = resolve_ld("ld_h", &ld_h, cols, rows)) ||
-      (st = resolve_ld("ld_dh", &ld_dh, cols, rows)) || (st = resolve_ld("ld_dx", &ld_dx, cols, rows)))
-    return st;
-  if ((st = check_workspace(workspace, workspace_bytes))) return st;
-  hipStream_t s = (hipStream_t)stream;
-  if (rows > 0 && (!dY || !H || !W || !rstd || !dX)) return fail(TG_E_NULL, "dY, H, W, rstd or dX is NULL");
-  const int eb = bytes_of(dtype);
-  if (misaligned(dY, eb) || misaligned(H, eb) || misaligned(dH, eb) || misaligned(dX, eb) ||
-      misaligned(W, bytes_of(w_dtype)) || misaligned(rstd, 4) || misaligned(dW, 4))
-    return fail(TG_E_ALIGN, "a pointer is not aligned to its element");
-  const Mat my = mat(dY, rows, cols, ld_dy, eb), mdh = mat(dH, rows, cols, ld_dh, eb), mdx = mat(dX, rows, cols, ld_dx, eb);
-  const Mat mdw = vec(dW, cols, 4), mws = vec(workspace, workspace_bytes, 1);
-  const Mat ins[] = {my, mat(H, rows, cols, ld_h, eb), mdh, vec(W, cols, bytes_of(w_dtype)), vec(rstd, rows, 4)};
-  for (int i = 0; i < 5; ++i) {
-    if (overlaps(mdw, ins[i]) || overlaps(mws, ins[i]))
-      return fail(TG_E_ALIAS, "dW or the workspace overlaps an input");
-    if (overlaps(mdx, ins[i]) && !((i == 0 && same(mdx, my)) || (i == 2 && same(mdx, mdh))))
-      return fail(TG_E_ALIAS, "dX overlaps an input without being exactly dY or dH");
-  }
-  if (overlaps(mdx, mdw) || overlaps(mdx, mws) || overlaps(mdw, mws))
-    return fail(TG_E_ALIAS, "dX, dW and the workspace must not overlap");
-  const int64_t dots = norm_in_registers(cols) ? 0 : (rows * 4 + 15) / 16 * 16;
-  const int64_t least = dots ? rows * 4 : 0;   // `dots` is rounded up for the shares of dW behind it
-  if (workspace_bytes < least)
-    return fail(TG_E_ARG, fmt("rows of %lld columns need a workspace of at least %lld bytes", cols, least));
-  if (rows == 0) return dW ? hip_status("tile_rmsnorm_bwd", launch_sum_rows(dW, 0, cols, dW, s)) : TG_OK;
-  NormBwdArgs a{};
-  a.dY = (const uint8_t*)dY;
-  a.H = (const uint8_t*)H;
-  a.W = (const uint8_t*)W;
-  a.rstd = rstd;
-  a.dH = (const uint8_t*)dH;
-  a.dX = (uint8_t*)dX;
-  a.rows = rows;
-  a.cols = cols;
-  a.ldy = ld_dy;
-  a.ldh = ld_h;
-  a.ldd = ld_dh;
-  a.ldx = ld_dx;
-  a.w_t = w_dtype;
-  a.dot = dots ? (float*)workspace : nullptr;
-  int64_t groups = norm_groups(rows, cols);
-  float* part = (float*)((uint8_t*)workspace + dots);
-  if (dW) groups = std::max<int64_t>(1, std::min(groups, (workspace_bytes - dots) / (4 * cols)));
-  a.dw = !dW ? nullptr : groups > 1 ? part : dW;
-  if ((st = hip_status("tile_rmsnorm_bwd", launch_rmsnorm_bwd(a, dtype, groups, s)))) return st;
-  if (dW && groups > 1) return hip_status("tile_rmsnorm_bwd", launch_sum_rows(part, groups, cols, dW, s));
-  return TG_OK;
+  return run_norm_bwd(kRms, dY, H, W, nullptr, rstd, dH, dX, dW, nullptr, rows, cols, ld_dy, ld_h, ld_dh, ld_dx, dtype,
+                      w_dtype, workspace, workspace_bytes, stream);
+}
+
+int64_t tile_layernorm_bwd_workspace(int64_t rows, int64_t cols, int dtype) {
+  return norm_bwd_workspace(kLayer, rows, cols, dtype);
+}
+
+int tile_layernorm_bwd(const void* dY, const void* H, const void* W, const float* mean, const float* rstd,
+                       const void* dH, void* dX, float* dW, float* dbias, int64_t rows, int64_t cols, int64_t ld_dy,
+                       int64_t ld_h, int64_t ld_dh, int64_t ld_dx, int dtype, int w_dtype, void* workspace,
+                       int64_t workspace_bytes, void* stream) {
+  return run_norm_bwd(kLayer, dY, H, W, mean, rstd, dH, dX, dW, dbias, rows, cols, ld_dy, ld_h, ld_dh, ld_dx, dtype,
+                      w_dtype, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

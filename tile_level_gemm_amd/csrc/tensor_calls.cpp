@@ -137,7 +137,7 @@ void no_history(const char* call, std::initializer_list<const Tensor*> inputs) {
   for (const Tensor* t : inputs)
     if (t && t->requires_grad()) {
       TORCH_WARN_ONCE(call, ": an input requires a gradient, but results of the layer operators carry no autograd "
-                      "history; use gemm_ep_backward and rms_norm_backward (and torch.no_grad() around the calls)");
+                      "history; use gemm_ep_backward, rms_norm_backward and their like (and torch.no_grad() around the calls)");
       return;
     }
 }
@@ -274,70 +274,149 @@ PyObject* gemm_ep_backward(PyObject* const* a) {
   return Py_BuildValue("(NNNN)", z, wrap(dA), wrap(dB), wrap(dbias));
 }
 
-// X, weight, eps, residual, out_dtype, scale kind, h_out -> (y, scale, rstd, h)
-PyObject* rms_norm(PyObject* const* a) {
-  const Tensor &X = *tensor("X", a[0]), &W = *tensor("weight", a[1]);
-  const Tensor *res = tensor("residual", a[3], true), *given = tensor("h_out", a[6], true);
-  const double eps = PyFloat_AsDouble(a[2]);
-  if (eps == -1.0 && PyErr_Occurred()) throw python_error();
-  const int kind = (int)integer(a[5]);
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw python_error();
+  return v;
+}
+
+// A norm's weight or bias: a vector of X's type or of float32.
+void per_column(const char* name, const Tensor& t, int64_t cols, at::ScalarType st) {
+  vector(name, t, cols);
+  if (t.scalar_type() != st && t.scalar_type() != at::kFloat)
+    refuse(TG_E_DTYPE, name, " must be ", st, " or float32, got ", t.scalar_type());
+}
+
+struct NormOut {
+  Tensor y, scale, mean, rstd;
+  PyObject* h;
+};
+// The forward pass of either norm.  B and `layer`: the layer norm's.
+NormOut norm(bool layer, const Tensor& X, const Tensor& W, const Tensor* B, double eps, const Tensor* res,
+             PyObject* out_dtype, int kind, const Tensor* given, PyObject* x_object, PyObject* given_object) {
   const int64_t ldx = matrix("X", X), rows = X.size(0), cols = X.size(1);
   const at::ScalarType st = X.scalar_type();
-  const at::ScalarType out_t = a[4] != Py_None          ? scalar_type("out_dtype", a[4])
+  const at::ScalarType out_t = out_dtype != Py_None    ? scalar_type("out_dtype", out_dtype)
                                : kind == TG_SCALE_NONE ? st
                                                        : at::kFloat8_e4m3fn;
   const int t = dtype_code("X", st), yt = dtype_code("out_dtype", out_t);
-  vector("weight", W, cols);
-  if (W.scalar_type() != st && W.scalar_type() != at::kFloat)
-    refuse(TG_E_DTYPE, "weight must be ", st, " or float32, got ", W.scalar_type());
+  per_column("weight", W, cols, st);
+  if (B) {
+    per_column("bias", *B, cols, st);
+    if (B->scalar_type() != W.scalar_type())
+      refuse(TG_E_DTYPE, "bias must be ", W.scalar_type(), " as weight, got ", B->scalar_type());
+  }
   int64_t ldr = 0, ldh = 0;
   if (res) ldr = matrix("residual", *res, rows, cols, st);
   else if (given) refuse(TG_E_ARG, "h_out is the sum X + residual: it needs a residual");
   if (given) ldh = matrix("h_out", *given, rows, cols, st);
-  const at::Device dev = one_gpu({&X, &W, res, given});
-  Tensor h, S;
+  const at::Device dev = one_gpu({&X, &W, B, res, given});
+  NormOut o;
+  Tensor h;
   if (given) h = *given;
   else if (res) h = make({rows, cols}, st, dev);
-  Tensor y = make({rows, cols}, out_t, dev), rstd = make({rows}, at::kFloat, dev);
-  if (kind == TG_SCALE_ROW) S = make({rows}, at::kFloat, dev);
-  else if (kind == TG_SCALE_BLOCK) S = make({rows, cols / 32}, at::kFloat8_e8m0fnu, dev);
-  check(tile_rmsnorm(address(&X), address(res), address(&W), address(h), address(y), address(S),
-                     (float*)address(rstd), rows, cols, ldx, ldr, ldh, 0, (float)eps, t, code_of(W.scalar_type()), yt,
-                     kind, stream_of(dev)));
+  o.y = make({rows, cols}, out_t, dev);
+  o.rstd = make({rows}, at::kFloat, dev);
+  if (layer) o.mean = make({rows}, at::kFloat, dev);
+  if (kind == TG_SCALE_ROW) o.scale = make({rows}, at::kFloat, dev);
+  else if (kind == TG_SCALE_BLOCK) o.scale = make({rows, cols / 32}, at::kFloat8_e8m0fnu, dev);
+  const int wt = code_of(W.scalar_type());
+  if (layer)
+    check(tile_layernorm(address(&X), address(res), address(&W), address(B), address(h), address(o.y), address(o.scale),
+                         (float*)address(o.mean), (float*)address(o.rstd), rows, cols, ldx, ldr, ldh, 0, (float)eps, t, wt,
+                         yt, kind, stream_of(dev)));
+  else
+    check(tile_rmsnorm(address(&X), address(res), address(&W), address(h), address(o.y), address(o.scale),
+                       (float*)address(o.rstd), rows, cols, ldx, ldr, ldh, 0, (float)eps, t, wt, yt, kind, stream_of(dev)));
   written(given);
-  no_history("rms_norm", {&X, &W, res});
-  PyObject* ph;
+  no_history(layer ? "layer_norm" : "rms_norm", {&X, &W, B, res});
   if (given || !res) {
-    ph = given ? a[6] : a[0];
-    Py_INCREF(ph);
+    o.h = given ? given_object : x_object;
+    Py_INCREF(o.h);
   } else {
-    ph = wrap(h);
+    o.h = wrap(h);
   }
-  return Py_BuildValue("(NNNN)", wrap(y), wrap(S), wrap(rstd), ph);
+  return o;
+}
+
+// X, weight, eps, residual, out_dtype, scale kind, h_out -> (y, scale, rstd, h)
+PyObject* rms_norm(PyObject* const* a) {
+  const Tensor &X = *tensor("X", a[0]), &W = *tensor("weight", a[1]);
+  const Tensor *res = tensor("residual", a[3], true), *given = tensor("h_out", a[6], true);
+  const NormOut o = norm(false, X, W, nullptr, number(a[2]), res, a[4], (int)integer(a[5]), given, a[0], a[6]);
+  return Py_BuildValue("(NNNN)", wrap(o.y), wrap(o.scale), wrap(o.rstd), o.h);
+}
+
+// X, weight, bias, eps, residual, out_dtype, scale kind, h_out -> (y, scale, mean, rstd, h)
+PyObject* layer_norm(PyObject* const* a) {
+  const Tensor &X = *tensor("X", a[0]), &W = *tensor("weight", a[1]), *B = tensor("bias", a[2], true);
+  const Tensor *res = tensor("residual", a[4], true), *given = tensor("h_out", a[7], true);
+  const NormOut o = norm(true, X, W, B, number(a[3]), res, a[5], (int)integer(a[6]), given, a[0], a[7]);
+  return Py_BuildValue("(NNNNN)", wrap(o.y), wrap(o.scale), wrap(o.mean), wrap(o.rstd), o.h);
+}
+
+struct NormGrads {
+  Tensor dX, dw, db;
+};
+// The backward pass of either norm; `mean`: the layer norm's.
+NormGrads norm_backward(const Tensor& dY, const Tensor& H, const Tensor& W, const Tensor* mean, const Tensor& rstd,
+                        const Tensor* dH, bool need_dw, bool need_db) {
+  const int64_t ldh = matrix("h", H), rows = H.size(0), cols = H.size(1);
+  const at::ScalarType st = H.scalar_type();
+  const int t = dtype_code("h", st), wt = code_of(W.scalar_type());
+  const int64_t ldy = matrix("dY", dY, rows, cols, st);
+  per_column("weight", W, cols, st);
+  f32_vector("rstd", rstd, rows);
+  if (mean) f32_vector("mean", *mean, rows);
+  const int64_t ldd = dH ? matrix("dH", *dH, rows, cols, st) : 0;
+  const at::Device dev = one_gpu({&dY, &H, &W, mean, &rstd, dH});
+  NormGrads g;
+  Tensor ws;
+  g.dX = make({rows, cols}, st, dev);
+  if (need_dw) g.dw = make({cols}, at::kFloat, dev);
+  if (need_db) g.db = make({cols}, at::kFloat, dev);
+  const int64_t nb = mean ? tile_layernorm_bwd_workspace(rows, cols, t) : tile_rmsnorm_bwd_workspace(rows, cols, t);
+  if (nb) ws = make({nb}, at::kByte, dev);
+  if (mean)
+    check(tile_layernorm_bwd(address(&dY), address(&H), address(&W), (const float*)address(mean), (const float*)address(&rstd),
+                             address(dH), address(g.dX), (float*)address(g.dw), (float*)address(g.db), rows, cols, ldy, ldh,
+                             ldd, 0, t, wt, address(ws), nb, stream_of(dev)));
+  else
+    check(tile_rmsnorm_bwd(address(&dY), address(&H), address(&W), (const float*)address(&rstd), address(dH), address(g.dX),
+                           (float*)address(g.dw), rows, cols, ldy, ldh, ldd, 0, t, wt, address(ws), nb, stream_of(dev)));
+  return g;
 }
 
 // dY, h, weight, rstd, dH, need_dw -> (dX, dweight)
 PyObject* rms_norm_backward(PyObject* const* a) {
   const Tensor &dY = *tensor("dY", a[0]), &H = *tensor("h", a[1]), &W = *tensor("weight", a[2]);
   const Tensor &rstd = *tensor("rstd", a[3]), *dH = tensor("dH", a[4], true);
-  const int64_t ldh = matrix("h", H), rows = H.size(0), cols = H.size(1);
-  const at::ScalarType st = H.scalar_type();
-  const int t = dtype_code("h", st);
-  const int64_t ldy = matrix("dY", dY, rows, cols, st);
-  vector("weight", W, cols);
-  if (W.scalar_type() != st && W.scalar_type() != at::kFloat)
-    refuse(TG_E_DTYPE, "weight must be ", st, " or float32, got ", W.scalar_type());
-  f32_vector("rstd", rstd, rows);
-  const int64_t ldd = dH ? matrix("dH", *dH, rows, cols, st) : 0;
-  const at::Device dev = one_gpu({&dY, &H, &W, &rstd, dH});
-  Tensor dX = make({rows, cols}, st, dev), dw, ws;
-  if (truth(a[5])) dw = make({cols}, at::kFloat, dev);
-  const int64_t nb = tile_rmsnorm_bwd_workspace(rows, cols, t);
-  if (nb) ws = make({nb}, at::kByte, dev);
-  check(tile_rmsnorm_bwd(address(&dY), address(&H), address(&W), (const float*)address(&rstd), address(dH), address(dX),
-                         (float*)address(dw), rows, cols, ldy, ldh, ldd, 0, t, code_of(W.scalar_type()), address(ws),
-                         nb, stream_of(dev)));
-  return Py_BuildValue("(NN)", wrap(dX), wrap(dw));
+  const NormGrads g = norm_backward(dY, H, W, nullptr, rstd, dH, truth(a[5]), false);
+  return Py_BuildValue("(NN)", wrap(g.dX), wrap(g.dw));
+}
+
+// dY, h, weight, mean, rstd, dH, need_dw, need_dbias -> (dX, dweight, dbias)
+PyObject* layer_norm_backward(PyObject* const* a) {
+  const Tensor &dY = *tensor("dY", a[0]), &H = *tensor("h", a[1]), &W = *tensor("weight", a[2]);
+  const Tensor &mean = *tensor("mean", a[3]), &rstd = *tensor("rstd", a[4]), *dH = tensor("dH", a[5], true);
+  const bool need_dw = truth(a[6]), need_db = truth(a[7]);
+  const NormGrads g = norm_backward(dY, H, W, &mean, rstd, dH, need_dw, need_db);
+  return Py_BuildValue("(NNN)", wrap(g.dX), wrap(g.dw), wrap(g.db));
+}
+
+// X, out_dtype, scale kind -> (q, scale)
+PyObject* quantize_rows(PyObject* const* a) {
+  const Tensor& X = *tensor("X", a[0]);
+  const int kind = (int)integer(a[2]);
+  const int64_t ldx = matrix("X", X), rows = X.size(0), cols = X.size(1);
+  const at::ScalarType out_t = scalar_type("out_dtype", a[1]);
+  const int t = dtype_code("X", X.scalar_type()), yt = dtype_code("out_dtype", out_t);
+  const at::Device dev = one_gpu({&X});
+  Tensor q = make({rows, cols}, out_t, dev);
+  Tensor S = kind == TG_SCALE_BLOCK ? make({rows, cols / 32}, at::kFloat8_e8m0fnu, dev) : make({rows}, at::kFloat, dev);
+  check(tile_quantize_rows(address(&X), address(q), address(S), rows, cols, ldx, 0, t, yt, kind, stream_of(dev)));
+  no_history("quantize_rows", {&X});
+  return Py_BuildValue("(NN)", wrap(q), wrap(S));
 }
 
 // Argument count, and C++ exceptions as Python ones.
@@ -369,7 +448,8 @@ PyObject* set_error_class(PyObject*, PyObject* c) {
 
 #define TG_METHOD(f, n) {#f, (PyCFunction)(void (*)(void))(entry<f, n>), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {TG_METHOD(gemm_ep, 12), TG_METHOD(gemm_ep_backward, 12), TG_METHOD(rms_norm, 7),
-                         TG_METHOD(rms_norm_backward, 6),
+                         TG_METHOD(rms_norm_backward, 6), TG_METHOD(layer_norm, 8),
+                         TG_METHOD(layer_norm_backward, 8), TG_METHOD(quantize_rows, 3),
                          {"set_error_class", set_error_class, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_calls", nullptr, -1, methods};
