@@ -521,7 +521,8 @@ int tile_gemm_atom_select(int64_t M, int64_t N, int64_t K, int dtype, int transA
 
 /* ---------------------------------------------------------------------------------------
  * Operators of a transformer layer around the products: the product with scales, bias,
- * activation and residual in its epilogue, its backward pass, the root-mean-square norm with
+ * activation and residual in its epilogue, the gated product of two projections, their backward
+ * passes, the root-mean-square norm with
  * the residual's addition (16-bit result, or 8 bits with scales for the products above and
  * below), the layer norm likewise, their backward passes, and the quantisation of rows.  Conventions as for every entry point; in addition:
  *   - leading dimensions count elements, 0 means packed; at least the row length, at most 2^40, and at
@@ -652,6 +653,61 @@ int tile_gemm_ep_bwd_scaled(const void* dY, const void* Z, const void* A, const 
 /* tile_gemm_ep_bwd_workspace — host-only: bytes of workspace tile_gemm_ep_bwd uses at most. */
 int64_t tile_gemm_ep_bwd_workspace(int64_t M, int64_t N, int64_t K, int transA, int transB, int dtype);
 
+/*
+ * tile_gemm_gated — both projections of a gated feed-forward layer, the activation and their product in one
+ * kernel: [G | U] = row_scale[m]·col_scale[n]·(A·B) + bias[n] of 2N columns, D = act(G)·U of N.
+ *
+ *   A       device [M,K], leading dimension lda.
+ *   B       device, the gate's weights and then the up projection's: [2N,K] with transB == 1, [K,2N] with
+ *           transB == 0 (16-bit operands only, else TG_E_LAYOUT), leading dimension ldb.  Operand types as for
+ *           tile_gemm_ep.
+ *   D       device [M,N] of d_dtype (TG_F16, TG_BF16 or TG_F32), leading dimension ldd.
+ *   ep      bias [2N], row_scale [M], col_scale [2N], act and Z [M,2N] (receives [G | U] of d_dtype, leading
+ *           dimension ld_z), each or NULL; residual must be NULL (TG_E_ARG).  NULL: D = G·U.
+ *   M,N,K   any, N at most 2^29 and M, K at most 2^30 (K of integers 131071); limits as for tile_gemm_ep's
+ *           [M,2N].  K == 0 has A·B = 0.
+ *   workspace   as for tile_gemm_ep (tile_gemm_gated_workspace).
+ * Z and D are each rounded once from fp32 values: D is of G and U before their rounding.
+ */
+int tile_gemm_gated(const void* A, const void* B, void* D, int64_t M, int64_t N, int64_t K, int64_t lda,
+                    int64_t ldb, int64_t ldd, int transB, int a_dtype, int b_dtype, int d_dtype,
+                    const tg_epilogue* ep, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* tile_gemm_gated_plan — host-only validation and kernel choice of tile_gemm_gated; block_n counts columns of
+ * B (of D: half), for TG_EP_TOKENS columns of D. */
+int tile_gemm_gated_plan(const void* A, const void* B, const void* D, int64_t M, int64_t N, int64_t K,
+                         int64_t lda, int64_t ldb, int64_t ldd, int transB, int a_dtype, int b_dtype,
+                         int d_dtype, const tg_epilogue* ep, const void* workspace, int64_t workspace_bytes,
+                         tg_ep_plan* out);
+
+/* tile_gemm_gated_workspace — host-only, as tile_gemm_ep_workspace. */
+int64_t tile_gemm_gated_workspace(int64_t M, int64_t N, int64_t K, int transB, int a_dtype);
+
+/*
+ * tile_gemm_gated_bwd — gradients of tile_gemm_gated for the gradient dY of D, with Z = [G | U]:
+ *
+ *   dZ = row_scale[m]·col_scale[n]·[dY·U·act'(G) | dY·act(G)]    dbias[n] = sum_m of that without the scales
+ *   dA = dZ·B^T    dB = A^T·dZ
+ *
+ *   dY      device [M,N] of dtype (TG_F16 or TG_BF16), leading dimension ld_dy.
+ *   Z       device [M,2N] of dtype, leading dimension ld_z: what tile_gemm_gated stored.
+ *   A, B    as given to tile_gemm_gated; A is read only for dB, B only for dA.  row_scale [M] and
+ *           col_scale [2N] device fp32 or NULL; they get no gradients.
+ *   dZ      device [M,2N] of dtype, packed: written, and the operand of both products (rounded to dtype).  May
+ *           be exactly Z when that is packed.
+ *   dA, dB  device, dtype, packed, in A's and B's stored orientation;  dbias  device fp32 [2N], the sums before
+ *           dZ's rounding;  each or NULL.
+ *   workspace   as for tile_gemm_ep_bwd (tile_gemm_gated_bwd_workspace).
+ */
+int tile_gemm_gated_bwd(const void* dY, const void* Z, const void* A, const void* B, const float* row_scale,
+                        const float* col_scale, void* dZ, void* dA, void* dB, float* dbias, int64_t M,
+                        int64_t N, int64_t K, int64_t ld_dy, int64_t ld_z, int64_t lda, int64_t ldb,
+                        int transB, int dtype, int act, void* workspace, int64_t workspace_bytes,
+                        void* stream);
+
+/* tile_gemm_gated_bwd_workspace — host-only: bytes of workspace tile_gemm_gated_bwd uses at most. */
+int64_t tile_gemm_gated_bwd_workspace(int64_t M, int64_t N, int64_t K, int transB, int dtype);
+
 typedef enum tg_scale_kind {
   TG_SCALE_NONE = 0,   /* Y in X's dtype */
   TG_SCALE_ROW = 1,    /* Y in 8 bits, fp32 S[row] = max|Y[row]|/qmax: tile_gemm_ep's row_scale (of
@@ -760,8 +816,8 @@ const char* tile_last_error(void);
 /* Library ABI version (this header: 7; 2 added tile_gemm_fp8 and tile_gemm_fp8_plan, 3 added
  * tile_gemm_mx and tile_gemm_mx_plan, 4 the register fragment calls tile_frag_*, 5
  * tile_copy_async and tile_copy_async_plan, 6 the K = 8 / 16 atoms and tile_mma_select, 7
- * tile_gemm_atom_select and tg_gemm_plan.atom; tile_gemm_ep*, tile_rmsnorm*, tile_layernorm* and
- * tile_quantize_rows were added without changing any earlier call, and are found by their symbols). */
+ * tile_gemm_atom_select and tg_gemm_plan.atom; tile_gemm_ep*, tile_gemm_gated*, tile_rmsnorm*,
+ * tile_layernorm* and tile_quantize_rows were added without changing any earlier call, and are found by their symbols). */
 int tile_abi_version(void);
 
 #ifdef __cplusplus

@@ -207,3 +207,66 @@ def quantised_rows(X, fmt):
     """(codes before their rounding, scales): the scale is an fp32 quotient, and the codes are X by it."""
     s = (np.maximum(np.abs(X).max(axis=1), AMAX_FLOOR).astype(np.float32) / np.float32(QMAX[fmt])).astype(np.float64)
     return X / s[:, None], s
+
+
+def gated(A, B, kind="silu", bias=None, row_scale=None, col_scale=None, out="bf16", eight=False, ints=False):
+    """(D, Z, bound of D, bound of Z) for A [M][K], B [K][2N]: Z = [G | U] = scales·A·B + bias, D = act(G)·U."""
+    N = B.shape[1] // 2
+    P = A @ B
+    scale = np.ones(P.shape)
+    if row_scale is not None:
+        scale = scale * row_scale[:, None]
+    if col_scale is not None:
+        scale = scale * col_scale[None, :]
+    Z = P * scale
+    err = (U32 * np.abs(P) if ints else product_bound(A, B, eight)) * np.abs(scale) + 3 * U32 * np.abs(Z)
+    if bias is not None:
+        Z = Z + bias[None, :]
+        err = err + U32 * (np.abs(Z) + err)
+    G, U, ge, ue = Z[:, :N], Z[:, N:], err[:, :N], err[:, N:]
+    a = act(G, kind)
+    # the activation's error as in product()
+    ae = ge if kind == "none" else 1.13 * ge + 16 * U32 * np.abs(G) + 2.0 ** -20 * np.abs(a)
+    D = a * U
+    derr = ae * np.abs(U) + np.abs(a) * ue + ae * ue + U32 * np.abs(D)
+    h, t = HALF_STEP[out], TINY[out]
+    return D, Z, derr * (1 + h) + h * np.abs(D) + t, err * (1 + h) + h * np.abs(Z) + t
+
+
+def act_grad_size(z, kind):
+    """What the fp32 evaluation of act_grad is accurate relative to.  The derivative is a sum of two terms,
+    gelu: Phi + z·phi, gelu_tanh and silu: s + (a multiple of) z·s·(1 - s), which cancel where it crosses zero
+    (z = -0.7518, -0.7524, -1.2785): each term is good to some units of fp32 relative to itself, so the sum is to
+    as many units of the terms' magnitudes, here |Phi| + |z·phi| and so on, however small it is."""
+    if kind == "gelu":
+        return _phi(z) + np.abs(z) * np.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
+    if kind in ("gelu_tanh", "silu"):
+        zc = np.clip(z, -100, 100) if kind == "gelu_tanh" else np.clip(z, -700, 700)
+        c = 2 * math.sqrt(2 / math.pi) if kind == "gelu_tanh" else 1.0
+        q = 0.044715 if kind == "gelu_tanh" else 0.0
+        s = _sigmoid(c * (zc + q * zc ** 3))
+        return s + np.abs(zc) * s * (1 - s) * c * (1 + 3 * q * zc ** 2)
+    return np.abs(act_grad(z, kind))
+
+
+def gated_backward(dY, Z, kind, out, row_scale=None, col_scale=None):
+    """(dZ, its bound, dbias, its bound) of D = act(G)·U: dbias sums before the scales and the rounding, in fp32."""
+    M, N = dY.shape
+    G, U = Z[:, :N], Z[:, N:]
+    g, a = act_grad(G, kind), act(G, kind)
+    exact = 0.0 if kind == "none" else 1.0
+    dG, dU = dY * U * g, dY * a
+    ge = np.abs(dY * U) * (exact * 32 * U32 * (1 + np.abs(G)) * (act_grad_size(G, kind) + 2.0 ** -20) + 2 * U32 * np.abs(g))
+    ue = np.abs(dY) * (exact * (16 * U32 * np.abs(G) + 2.0 ** -20 * np.abs(a)) + U32 * np.abs(a))
+    d, err = np.concatenate([dG, dU], axis=1), np.concatenate([ge, ue], axis=1)
+    s = d.sum(axis=0)
+    serr = err.sum(axis=0) + (M + 8) * 2 * U32 * np.abs(d).sum(axis=0) + 2.0 ** -140
+    if row_scale is not None or col_scale is not None:
+        scale = np.ones_like(d)
+        if row_scale is not None:
+            scale = scale * row_scale[:, None]
+        if col_scale is not None:
+            scale = scale * col_scale[None, :]
+        d, err = d * scale, err * np.abs(scale) + 3 * U32 * np.abs(d * scale)
+    h = HALF_STEP[out]
+    return d, err * (1 + h) + h * np.abs(d) + TINY[out], s, serr

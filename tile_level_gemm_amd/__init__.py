@@ -174,6 +174,12 @@ _SIGS = {
     "tile_gemm_ep_bwd_scaled": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64,
                                        _I64, _I64, _I64, _INT, _INT, _INT, _INT, _VP, _I64, _VP]),
     "tile_gemm_ep_bwd_workspace": (_I64, [_I64, _I64, _I64, _INT, _INT, _INT]),
+    "tile_gemm_gated": (_INT, [_VP] * 3 + [_I64] * 6 + [_INT] * 4 + [ctypes.POINTER(Epilogue), _VP, _I64, _VP]),
+    "tile_gemm_gated_plan": (_INT, [_VP] * 3 + [_I64] * 6 + [_INT] * 4 + [ctypes.POINTER(Epilogue), _VP, _I64,
+                                                                          ctypes.POINTER(EpPlan)]),
+    "tile_gemm_gated_workspace": (_I64, [_I64, _I64, _I64, _INT, _INT]),
+    "tile_gemm_gated_bwd": (_INT, [_VP] * 10 + [_I64] * 7 + [_INT, _INT, _INT, _VP, _I64, _VP]),
+    "tile_gemm_gated_bwd_workspace": (_I64, [_I64, _I64, _I64, _INT, _INT]),
     "tile_rmsnorm": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _I64, _I64, _F,
                             _INT, _INT, _INT, _INT, _VP]),
     "tile_rmsnorm_bwd": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _I64, _I64,
@@ -669,6 +675,65 @@ def tile_gemm_ep_bwd_workspace(M, N, K, transA, transB, dtype):
     return lib().tile_gemm_ep_bwd_workspace(M, N, K, int(transA), int(transB), int(dtype))
 
 
+def _gated_args(A, B, D, M, N, K, lda, ldb, ldd, transB, a_dtype, b_dtype, d_dtype, bias, bias_dtype, act, Z, ld_z,
+                row_scale, col_scale, workspace, workspace_bytes):
+    ea, eb, ed = ELEM_BYTES.get(int(a_dtype), 1), ELEM_BYTES.get(int(b_dtype), 1), ELEM_BYTES.get(int(d_dtype), 1)
+    if bias_dtype is None:
+        bias_dtype = TORCH_DTYPES.get(bias.dtype, 0) if isinstance(bias, torch.Tensor) else 0
+    ebias, nb, w = ELEM_BYTES.get(int(bias_dtype)), _workspace_bytes(workspace, workspace_bytes), 2 * int(N)
+    pa, pb, pd, pbias, pz, prs, pcs, pws = _ptrs(
+        _matrix("A", A, M, K, lda, ea), _matrix("B", B, w if transB else K, K if transB else w, ldb, eb),
+        _matrix("D", D, M, N, ldd, ed), ("bias", bias, ebias, max(w, 0) * (ebias or 1)), _matrix("Z", Z, M, w, ld_z, ed),
+        ("row_scale", row_scale, 4, max(int(M), 0) * 4), ("col_scale", col_scale, 4, max(w, 0) * 4),
+        ("workspace", workspace, None, nb))
+    ep = Epilogue(pbias, None, pz, prs, pcs, 0, int(ld_z), int(bias_dtype), int(act))
+    return (pa, pb, pd, M, N, K, int(lda), int(ldb), int(ldd), int(transB), int(a_dtype), int(b_dtype), int(d_dtype),
+            ctypes.byref(ep), pws, nb)
+
+
+def tile_gemm_gated(A, B, D, M, N, K, transB, a_dtype, b_dtype, d_dtype, *, lda=0, ldb=0, ldd=0, bias=None,
+                    bias_dtype=None, act=TG_ACT_NONE, Z=None, ld_z=0, row_scale=None, col_scale=None, workspace=None,
+                    workspace_bytes=None, stream=None):
+    """[G | U] = row_scale·col_scale·A·B + bias, D = act(G)·U (see include/tilegemm.h)."""
+    args = _gated_args(A, B, D, M, N, K, lda, ldb, ldd, transB, a_dtype, b_dtype, d_dtype, bias, bias_dtype, act, Z,
+                       ld_z, row_scale, col_scale, workspace, workspace_bytes)
+    _check(lib().tile_gemm_gated(*args, _stream(stream)))
+
+
+def tile_gemm_gated_plan(A, B, D, M, N, K, transB, a_dtype, b_dtype, d_dtype, *, lda=0, ldb=0, ldd=0, bias=None,
+                         bias_dtype=None, act=TG_ACT_NONE, Z=None, ld_z=0, row_scale=None, col_scale=None,
+                         workspace=None, workspace_bytes=None):
+    """Host-only: the kernel tile_gemm_gated would run."""
+    args = _gated_args(A, B, D, M, N, K, lda, ldb, ldd, transB, a_dtype, b_dtype, d_dtype, bias, bias_dtype, act, Z,
+                       ld_z, row_scale, col_scale, workspace, workspace_bytes)
+    out = EpPlan()
+    _check(lib().tile_gemm_gated_plan(*args, ctypes.byref(out)))
+    return out
+
+
+def tile_gemm_gated_workspace(M, N, K, transB, a_dtype):
+    """Workspace bytes of a problem's best plan."""
+    return lib().tile_gemm_gated_workspace(M, N, K, int(transB), int(a_dtype))
+
+
+def tile_gemm_gated_bwd(dY, Z, A, B, dZ, dA, dB, dbias, M, N, K, transB, dtype, act, *, ld_dy=0, ld_z=0, lda=0, ldb=0,
+                        row_scale=None, col_scale=None, workspace=None, workspace_bytes=None, stream=None):
+    """Gradients of tile_gemm_gated for 16-bit operands (see include/tilegemm.h)."""
+    e = ELEM_BYTES.get(int(dtype), 1)
+    m, n, k = max(int(M), 0), max(int(N), 0), max(int(K), 0)
+    nb = _workspace_bytes(workspace, workspace_bytes)
+    p = _ptrs(_matrix("dY", dY, m, n, ld_dy, e), _matrix("Z", Z, m, 2 * n, ld_z, e), _matrix("A", A, m, k, lda, e),
+              _matrix("B", B, 2 * n if transB else k, k if transB else 2 * n, ldb, e), ("row_scale", row_scale, 4, m * 4),
+              ("col_scale", col_scale, 4, n * 8), ("dZ", dZ, e, 2 * m * n * e), ("dA", dA, e, m * k * e),
+              ("dB", dB, e, 2 * k * n * e), ("dbias", dbias, 4, n * 8), ("workspace", workspace, None, nb))
+    _check(lib().tile_gemm_gated_bwd(*p[:10], M, N, K, int(ld_dy), int(ld_z), int(lda), int(ldb), int(transB), int(dtype),
+                                     int(act), p[10], nb, _stream(stream)))
+
+
+def tile_gemm_gated_bwd_workspace(M, N, K, transB, dtype):
+    return lib().tile_gemm_gated_bwd_workspace(M, N, K, int(transB), int(dtype))
+
+
 def _scale_bytes(rows, cols, kind):
     """Bytes of the scales of 8-bit rows."""
     return rows * 4 if int(kind) == TG_SCALE_ROW else rows * (cols // 32) if int(kind) == TG_SCALE_BLOCK else 0
@@ -817,6 +882,33 @@ def gemm_ep_backward(dY, A, B, Z=None, act="none", trans_a=False, trans_b=True, 
                                     col_scale)
     return (_calls or _native()).gemm_ep_backward(dY, A, B, Z, _act(act), trans_a, trans_b, need_dA, need_dB,
                                                   need_dbias, row_scale, col_scale)
+
+
+def gemm_gated(A, B, bias=None, act="silu", row_scale=None, col_scale=None, trans_b=True, out_dtype=None, keep_z=False,
+               out=None, stream=None):
+    """D = act(G)·U with [G | U] = row_scale·col_scale·A·B + bias; returns D, or (D, Z = [G | U]) with keep_z.
+
+    A is [M, K], B [2N, K] ([K, 2N] without trans_b, 16-bit types only): the gate's weights, then the up
+    projection's, as bias and col_scale are ([2N]).  Types, rows and out_dtype as for gemm_ep; D is taken of
+    G and U before Z rounds them."""
+    if stream is not None:
+        with _On(stream):
+            return gemm_gated(A, B, bias, act, row_scale, col_scale, trans_b, out_dtype, keep_z, out)
+    return (_calls or _native()).gemm_gated(A, B, bias, _act(act), row_scale, col_scale, trans_b, out_dtype, keep_z, out)
+
+
+def gemm_gated_backward(dY, A, B, Z, act="silu", trans_b=True, need_dA=True, need_dB=True, need_dbias=True, stream=None,
+                        row_scale=None, col_scale=None):
+    """Gradients of gemm_gated for 16-bit operands: (dZ, dA, dB, dbias), None for what is not needed.
+
+    Z is what gemm_gated returned with keep_z.  dZ [M, 2N] is the gradient of A·B (with scales it carries
+    them), dbias [2N] is float32, dA and dB have A's and B's shapes.  The products take dZ as it is held, in
+    16 bits; the scales get no gradients."""
+    if stream is not None:
+        with _On(stream):
+            return gemm_gated_backward(dY, A, B, Z, act, trans_b, need_dA, need_dB, need_dbias, None, row_scale, col_scale)
+    return (_calls or _native()).gemm_gated_backward(dY, A, B, Z, _act(act), trans_b, need_dA, need_dB, need_dbias,
+                                                     row_scale, col_scale)
 
 
 class Norm:

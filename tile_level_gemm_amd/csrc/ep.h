@@ -2,9 +2,12 @@
 //
 //   P = A·B (fp32 sums; int8 operands: exact 32-bit integers, then fp32)   Z = row_scale[m]·col_scale[n]·P + bias[n]   D = act(Z) + residual
 //
+// Gated: B has 2N columns, the gate's and the up projection's, Z = [G | U] has them too, and D = act(G)·U
+// has N.
+//
 // Every kernel that finishes an output element (the block kernels, the token kernels and the join
-// of a split sum) goes through ep_finish8, its 16-bit form or ep_finish1, so all of them round once: Z and D are each
-// rounded to d_dtype from the fp32 value.  Internal header.
+// of a split sum) goes through ep_finish8, its 16-bit form or ep_finish1, or the gated_* ones, so all of them
+// round once: Z and D are each rounded to d_dtype from the fp32 value.  Internal header.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -20,13 +23,13 @@ struct EpArgs {
   const uint8_t* B;
   uint8_t* D;
   int64_t lda, ldb, ldd;       // elements
-  int32_t M, N, K;
+  int32_t M, N, K;             // N: columns of D
   int32_t tiles_m, tiles_n;
   int32_t waves, cn;           // few rows: waves and columns of a workgroup
   int32_t ring;                // direct blocks: four stages in flight (128 and 64 wide)
   int32_t splits, k_per_split; // the sum over K in `splits` parts of k_per_split (the last one shorter)
   float* part;                 // splits > 1: fp32 (or 32-bit integer) sums [splits][M][part_ld]
-  int64_t part_ld;             // N rounded up to 8: rows stay 32-byte aligned
+  int64_t part_ld;             // N rounded up to 8: rows stay 32-byte aligned; gated: twice that, U in the second half
   const uint8_t* bias;
   const uint8_t* res;
   uint8_t* Z;
@@ -48,7 +51,11 @@ hipError_t launch_ep_block(const EpArgs& g, int trans_a, int trans_b, int a_dtyp
 constexpr int64_t kTokenRows = 32;
 hipError_t launch_ep_tokens(const EpArgs& g, int trans_a, int trans_b, int a_dtype, int b_dtype, int waves,
                             hipStream_t s);
-hipError_t launch_ep_join(const EpArgs& g, hipStream_t s);
+hipError_t launch_ep_join(const EpArgs& g, bool gated, hipStream_t s);
+// A [M,K]; B [2N,K] (trans_b) or [K,2N], the latter for 16-bit operands
+hipError_t launch_gated_block(const EpArgs& g, int trans_b, int a_dtype, int b_dtype, const EpKernel& k, hipStream_t s);
+// M <= kTokenRows, B [2N,K]
+hipError_t launch_gated_tokens(const EpArgs& g, int a_dtype, int b_dtype, int waves, hipStream_t s);
 
 // dZ = dY·act'(Z) ([M][N] packed, may be NULL) and column sums [groups][N] (may be NULL).  With scales the
 // sums are of that, and dZ receives row_scale·col_scale·dY·act'(Z).
@@ -64,6 +71,9 @@ struct ActGradArgs {
   int32_t t, act;
 };
 hipError_t launch_act_grad(const ActGradArgs& a, int groups, hipStream_t s);
+// The same of D = act(G)·U, Z = [G | U] and dZ [M][2N] = [dY·U·act'(G) | dY·act(G)], column scales, sums [groups][2N];
+// N: columns of D.
+hipError_t launch_gated_grad(const ActGradArgs& a, int groups, hipStream_t s);
 // out[n] = sum_g part[g][n]; columns from `split` on go to rest[n - split]
 hipError_t launch_sum_rows(const float* part, int64_t G, int64_t N, float* out, hipStream_t s,
                            float* rest = nullptr, int64_t split = INT64_MAX);
@@ -75,6 +85,7 @@ hipError_t launch_ep_mk(const EpArgs& g, int dtype, const EpKernel& k, hipStream
 hipError_t launch_ep_mm(const EpArgs& g, int dtype, const EpKernel& k, hipStream_t s);
 hipError_t launch_ep_fp8(const EpArgs& g, int a_dtype, int b_dtype, const EpKernel& k, hipStream_t s);
 hipError_t launch_ep_i8(const EpArgs& g, const EpKernel& k, hipStream_t s);
+hipError_t launch_gated_8(const EpArgs& g, int a_dtype, int b_dtype, const EpKernel& k, hipStream_t s);
 
 #ifdef __HIP__
 namespace {
@@ -273,7 +284,8 @@ __device__ __forceinline__ void ep_with_act(int act, F f) {
 struct EpCols {   // per-column values of the lane's 8 columns, loaded once
   float bias[8], cs[8];
 };
-__device__ __forceinline__ void ep_cols(const EpArgs& g, int col, EpCols& c) {
+// first: column 0 of those that the lane's are counted from (gated: N for the up projection's)
+__device__ __forceinline__ void ep_cols(const EpArgs& g, int col, EpCols& c, int first = 0) {
   const int n = g.N - col;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -281,8 +293,8 @@ __device__ __forceinline__ void ep_cols(const EpArgs& g, int col, EpCols& c) {
     c.cs[e] = 1.0f;
   }
   if (n <= 0) return;
-  if (g.bias) ep_get8(g.bias, g.bias_t, col, n, c.bias);
-  if (g.cs) ep_get8((const uint8_t*)g.cs, TG_F32, col, n, c.cs);
+  if (g.bias) ep_get8(g.bias, g.bias_t, (int64_t)first + col, n, c.bias);
+  if (g.cs) ep_get8((const uint8_t*)g.cs, TG_F32, (int64_t)first + col, n, c.cs);
 }
 // v: the sums P of row `row`, columns col .. col+7 (row < M, col < N); any type, any number of
 // columns left.
@@ -344,6 +356,74 @@ __device__ __forceinline__ void ep_finish8_16(const EpArgs& g, int row, int col,
     for (int e = 0; e < 8; ++e) v[e] += r[e];
   }
   ep_store8_16<true>(g.D, (int64_t)row * g.ldd + col, g.N - col, ep_pack8(g.d_t, v));
+}
+
+// ---- gated: 8 consecutive columns of the gate and of the up projection ---------------------------
+struct GatedCols {
+  EpCols gate, up;
+};
+__device__ __forceinline__ void gated_cols(const EpArgs& g, int col, GatedCols& c) {
+  ep_cols(g, col, c.gate);
+  ep_cols(g, col, c.up, g.N);
+}
+__device__ __forceinline__ void gated_z(const EpArgs& g, int row, const GatedCols& c, float (&v)[8], float (&u)[8]) {
+  const float rs = g.rs ? g.rs[row] : 1.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    v[e] = v[e] * rs * c.gate.cs[e] + c.gate.bias[e];
+    u[e] = u[e] * rs * c.up.cs[e] + c.up.bias[e];
+  }
+}
+// v, u: the sums of both projections; any type, any number of columns left
+__device__ __forceinline__ void gated_finish8(const EpArgs& g, int row, int col, const GatedCols& c, float (&v)[8],
+                                              float (&u)[8]) {
+  const int n = g.N - col;
+  gated_z(g, row, c, v, u);
+  if (g.Z) {
+    ep_put8(g.Z, g.d_t, (int64_t)row * g.ldz + col, n, v);
+    ep_put8(g.Z, g.d_t, (int64_t)row * g.ldz + g.N + col, n, u);
+  }
+  ep_with_act(g.act, [&](auto act) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = ep_act<decltype(act)::value>(v[e]) * u[e];
+  });
+  ep_put8(g.D, g.d_t, (int64_t)row * g.ldd + col, n, v);
+}
+template <int ACT>
+__device__ __forceinline__ void gated_finish8_16(const EpArgs& g, int row, int col, const GatedCols& c, float (&v)[8],
+                                                 float (&u)[8]) {
+  const int n = g.N - col;
+  gated_z(g, row, c, v, u);
+  if (g.Z) {
+    ep_store8_16<true>(g.Z, (int64_t)row * g.ldz + col, n, ep_pack8(g.d_t, v));
+    ep_store8_16<true>(g.Z, (int64_t)row * g.ldz + g.N + col, n, ep_pack8(g.d_t, u));
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = ep_act<ACT>(v[e]) * u[e];
+  ep_store8_16<true>(g.D, (int64_t)row * g.ldd + col, n, ep_pack8(g.d_t, v));
+}
+// one element
+struct GatedOne {
+  float rs, cs[2], bias[2];
+};
+__device__ __forceinline__ void gated_one(const EpArgs& g, int row, int col, GatedOne& x) {
+  x.rs = g.rs ? g.rs[row] : 1.0f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t at = (int64_t)h * g.N + col;
+    x.cs[h] = g.cs ? g.cs[at] : 1.0f;
+    x.bias[h] = g.bias ? ep_get(g.bias, g.bias_t, at) : 0.0f;
+  }
+}
+__device__ __forceinline__ void gated_finish1(const EpArgs& g, int row, int col, const GatedOne& x, float v, float u) {
+  v = v * x.rs * x.cs[0] + x.bias[0];
+  u = u * x.rs * x.cs[1] + x.bias[1];
+  if (g.Z) {
+    ep_put(g.Z, g.d_t, (int64_t)row * g.ldz + col, v);
+    ep_put(g.Z, g.d_t, (int64_t)row * g.ldz + g.N + col, u);
+  }
+  ep_with_act(g.act, [&](auto act) { v = ep_act<decltype(act)::value>(v); });
+  ep_put(g.D, g.d_t, (int64_t)row * g.ldd + col, v * u);
 }
 
 }  // namespace

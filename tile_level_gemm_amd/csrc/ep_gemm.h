@@ -17,6 +17,10 @@
 //    with 16-byte writes, and comes back as 8 consecutive columns per lane, where bias,
 //    activation and residual are applied and D is stored 16 bytes at a time (whole 128-byte
 //    lines per row on 256-wide blocks).  The band is wave-private: no workgroup barrier.
+//  * gated: a block is BS x BS/2 results of both projections.  Half of each wave's columns are the
+//    gate's and half the up projection's of the same results, so both meet in the wave's band, and the
+//    K loop is the plain one: only B's loads go by another map (gated_index), which is a base address a
+//    wave for [2N][K] weights, since a wave loads half a wave's columns, and an offset a lane for [K][2N].
 //
 // Bounds, measured on MI355X.  256-wide, 8192^3 bf16: 785 us (1400 TFLOP/s), of which the K loop takes
 // 725; with bias, gelu_tanh and Z 806 us; 8192 x 8192 x 4096 e4m3 with everything 217 us (2530 TFLOP/s),
@@ -59,14 +63,21 @@ __device__ __forceinline__ u32x4 shift_down(u32x4 v, uint32_t bits) {
 
 // Fills one operand's LDS stage through registers.  Slot mapping as Operand::load: instruction
 // i of wave w fills the 1 KiB block PER·w + i, lane l its bytes 16l .. 16l+15.
-template <bool MN, int PER, int DT, int BS>
+// R: of a gated block's weights, columns of a group (0: not gated); half: their N.
+template <bool MN, int PER, int DT, int BS, int R = 0>
 struct StagedFetch {
   using EL = Elem<DT>;
   static constexpr int E = EL::kBytes, VE = 16 / E;   // elements per chunk
   u32x4 r[PER];
+  int half = 0;
 
+  __device__ __forceinline__ StagedPlace where(int i, int stage, int wave, int lane) const {
+    const StagedPlace p = in_block(i, stage, wave, lane);
+    if constexpr (R) return gated_place<MN>(p, R, half);
+    else return p;
+  }
   // instruction i's chunk of a stage
-  __device__ __forceinline__ static StagedPlace where(int i, int stage, int wave, int lane) {
+  __device__ __forceinline__ static StagedPlace in_block(int i, int stage, int wave, int lane) {
     const uint32_t blk = (uint32_t)(PER * wave + i);
     if constexpr (MN) {
       constexpr uint32_t ROWB = BS * E, CH = ROWB / 16, RPB = 1024 / ROWB;
@@ -130,7 +141,7 @@ struct EpTile {
   int m0, n0, split, k0, kl;
 };
 // tile scheduler: contiguous ranges per XCD; parts of K outermost, then grouped tile-rows
-template <int BS>
+template <int BS, bool GATED>
 __device__ __forceinline__ EpTile ep_tile(const EpArgs& g) {
   const int nb = (int)gridDim.x;
   int bid = (int)blockIdx.x;
@@ -143,7 +154,7 @@ __device__ __forceinline__ EpTile ep_tile(const EpArgs& g) {
   const int first_m = (bid / group) * kGroupM;
   const int gsz = min(g.tiles_m - first_m, kGroupM);
   t.m0 = (first_m + (bid % group) % gsz) * BS;
-  t.n0 = ((bid % group) / gsz) * BS;
+  t.n0 = ((bid % group) / gsz) * (GATED ? BS / 2 : BS);
   t.k0 = t.split * g.k_per_split;
   t.kl = min(g.K - t.k0, g.k_per_split);
   return t;
@@ -248,11 +259,104 @@ __device__ __forceinline__ void ep_store(const EpArgs& g, const EpTile& t, f32x1
   }
 }
 
+// Epilogue of a gated block, as ep_store: the first half of a band's columns are the gate's.
+template <int BS, int WN, int TM, int TN, bool INT>
+__device__ __forceinline__ void gated_store(const EpArgs& g, const EpTile& t, f32x16 (&acc)[TM][TN], int wave,
+                                            int lane, int wm, int wn, uint8_t* s0, uint8_t* s1, uint8_t* s2,
+                                            uint8_t* s3) {
+  constexpr int LDF = WN + 4, R = WN / 2;
+  static_assert((BS == 64 ? 1 : 2) * 32 * LDF * 4 <= BS * kRowBytes, "two bands (four waves: one) per stage array");
+  float* band = (float*)((wave & 2) ? ((wave & 1) ? s3 : s2) : ((wave & 1) ? s1 : s0)) + (wave >> 2) * 32 * LDF;
+  constexpr int LPR = R / 8, RPP = 64 / LPR, NP = 32 / RPP;   // lanes per row, rows per pass
+  const int bcol = 8 * (lane % LPR), brow = lane / LPR;
+  const int col = t.n0 + wn / 2 + bcol;
+  const bool in = col < g.N;
+  GatedCols cols;
+  if (g.splits == 1) gated_cols(g, col, cols);
+  auto from_band = [&](int p, int at, float (&v)[8]) {
+    const float* src = band + (p * RPP + brow) * LDF + bcol + at;
+    const float4 lo = *(const float4*)src, hi = *(const float4*)(src + 4);
+    v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+    v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+  };
+  auto sums = [&](int p, int at, float (&v)[8]) {
+    from_band(p, at, v);
+    if constexpr (INT) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (float)__builtin_bit_cast(int, v[e]);
+    }
+  };
+#pragma unroll 1
+  for (int i = 0; i < TM; ++i) {
+    const int row0 = t.m0 + wm + 32 * i + brow;
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(float4*)(band + (lane & 31) * LDF + 32 * j + 8 * q + 4 * (lane >> 5)) =
+            float4{acc[0][j][4 * q], acc[0][j][4 * q + 1], acc[0][j][4 * q + 2], acc[0][j][4 * q + 3]};
+#pragma unroll
+    for (int k = 0; k + 1 < TM; ++k)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[k][j] = acc[k + 1][j];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    float v[8], u[8];
+    if (g.splits > 1) {
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        from_band(p, 0, v);
+        from_band(p, R, u);
+        const int row = row0 + p * RPP;
+        const int64_t at = ((int64_t)t.split * g.M + row) * g.part_ld + col;
+        if (in && row < g.M) {
+          ep_put8((uint8_t*)g.part, TG_F32, at, 8, v);
+          ep_put8((uint8_t*)g.part, TG_F32, at + g.part_ld / 2, 8, u);
+        }
+      }
+    } else if (g.d_t != TG_F32) {
+      ep_with_act(g.act, [&](auto act) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          sums(p, 0, v);
+          sums(p, R, u);
+          const int row = row0 + p * RPP;
+          if (in && row < g.M) gated_finish8_16<decltype(act)::value>(g, row, col, cols, v, u);
+        }
+      });
+    } else {
+#pragma unroll 1
+      for (int p = 0; p < NP; ++p) {
+        sums(p, 0, v);
+        sums(p, R, u);
+        const int row = row0 + p * RPP;
+        if (in && row < g.M) gated_finish8(g, row, col, cols, v, u);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+}
+
+// mn_dma_offsets of a gated block's [K][2N] weights: the chunk's columns by gated_index.
+template <int PER, int ROWB, int R>
+__device__ __forceinline__ void gated_mn_dma_offsets(int64_t ld, int n, int wave, int lane, uint32_t (&off)[2]) {
+  constexpr uint32_t CH = ROWB / 16, RPB = 1024 / ROWB;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const uint32_t k = RPB * (uint32_t)(PER * wave + p) + (uint32_t)lane / CH;
+    const uint32_t c = ((uint32_t)lane % CH) ^ sm_row<SMV, ROWB>(k);
+    off[p] = (k * (uint32_t)ld + (uint32_t)gated_index((int)c * 8, R, n)) * 2u;   // below the span of whole stages
+  }
+}
+
 // fills one stage's LDS images of both operands from memory
-template <bool A_MN, bool B_MN, int DT, int BS, class OA, class OB>
+template <bool A_MN, bool B_MN, int DT, int BS, bool GATED, class OA, class OB>
 struct DirectLoads {
   using EL = Elem<DT>;
-  static constexpr int E = EL::kBytes, BK = EL::kBK;
+  static constexpr int E = EL::kBytes, BK = EL::kBK, PER = BS / 8 / (ep_threads(BS) / 64);
   OA& oa;
   OB& ob;
   const EpArgs& g;
@@ -262,10 +366,19 @@ struct DirectLoads {
       : oa(a), ob(b), g(g_), kl(t.kl), wave(wave_) {
     const uint8_t* pa = g.A + (A_MN ? (int64_t)t.k0 * g.lda + t.m0 : (int64_t)t.m0 * g.lda + t.k0) * E;
     const uint8_t* pb = g.B + (B_MN ? (int64_t)t.k0 * g.ldb + t.n0 : (int64_t)t.n0 * g.ldb + t.k0) * E;
-    const int ra = g.M - t.m0, rb = g.N - t.n0;   // rows / columns from here to the end
+    // rows / columns from here to the end
+    const int ra = g.M - t.m0, rb = GATED ? 2 * g.N - t.n0 : g.N - t.n0;
     // records: from the panel's first element to the last one of this part of K
     oa.bind(pa, (A_MN ? (int64_t)(kl - 1) * g.lda + ra : (int64_t)(min(ra, BS) - 1) * g.lda + kl) * E);
-    ob.bind(pb, (B_MN ? (int64_t)(kl - 1) * g.ldb + rb : (int64_t)(min(rb, BS) - 1) * g.ldb + kl) * E);
+    if constexpr (GATED && !B_MN) {
+      // the wave's rows: a group of one projection
+      constexpr int R = 8 * PER;
+      const int first = t.n0 + (wave >> 1) * R, left = g.N - first;
+      const int64_t row = (int64_t)(wave & 1) * g.N + min(first, g.N - 1);
+      ob.bind(g.B + (row * g.ldb + t.k0) * E, left <= 0 ? 0 : ((int64_t)(min(left, R) - 1) * g.ldb + kl) * E);
+    } else {
+      ob.bind(pb, (B_MN ? (int64_t)(kl - 1) * g.ldb + rb : (int64_t)(min(rb, BS) - 1) * g.ldb + kl) * E);
+    }
     adv_a = A_MN ? (uint32_t)(BK * g.lda * E) : (uint32_t)kRowBytes;
     adv_b = B_MN ? (uint32_t)(BK * g.ldb * E) : (uint32_t)kRowBytes;
   }
@@ -279,7 +392,7 @@ struct DirectLoads {
 
 // Direct loads, two stages: 256-wide blocks (one workgroup per CU), and 128-wide ones where two
 // workgroups share a CU.
-template <bool A_MN, bool B_MN, int DT, int BS>
+template <bool A_MN, bool B_MN, int DT, int BS, bool GATED>
 __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_direct(EpArgs g) {
   constexpr int WGM = 2, WGN = ep_threads(BS) / 128;
   // four named stages: their addresses stay compile-time immediates
@@ -295,7 +408,8 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_dir
   constexpr int NS = EL::kSteps;
   static_assert(DT == TG_F16 || DT == TG_BF16 || DT == TG_I8 || (DT >= kF8 && DT < kMX), "16-bit, int8 or fp8 operands");
   static_assert(EL::kBytes == 2 || (!A_MN && !B_MN), "8-bit operands are K-contiguous");
-  const EpTile t = ep_tile<BS>(g);
+  static_assert(!GATED || !A_MN, "gated: A [M][K]");
+  const EpTile t = ep_tile<BS, GATED>(g);
   const int tid = (int)threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int wm = (wave / WGN) * WM, wn = (wave % WGN) * WN;
@@ -304,7 +418,8 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_dir
   OA oa;
   OB ob;
   oa.init(g.lda, wm, wave, lane);
-  ob.init(g.ldb, wn, wave, lane);
+  ob.init(g.ldb, wn, GATED && !B_MN ? 0 : wave, lane);   // gated: the wave's rows are in its base address
+  if constexpr (GATED && B_MN) gated_mn_dma_offsets<PER, BS * EL::kBytes, WN / 2>(g.ldb, g.N, wave, lane, ob.dma);
   f32x16 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -320,7 +435,7 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_dir
   constexpr int kReads = OA::kReads + OB::kReads, kMfma = TM * TN;
   using T_ = std::true_type;
   using F_ = std::false_type;
-  const DirectLoads<A_MN, B_MN, DT, BS, OA, OB> load_ab(oa, ob, g, t, wave);
+  const DirectLoads<A_MN, B_MN, DT, BS, GATED, OA, OB> load_ab(oa, ob, g, t, wave);
   const int KT = (t.kl + EL::kBK - 1) / EL::kBK;   // >= 1
   load_ab(0, sa0, sb0);
   __builtin_amdgcn_s_waitcnt(0);
@@ -400,7 +515,8 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_dir
   }
   stage(sa0, sb0, sa1, sb1, kt, F_{}, T_{});
   stage(sa1, sb1, sa0, sb0, kt + 1, F_{}, F_{});
-  ep_store<BS, WN, TM, TN, EL::kI8>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
+  if constexpr (GATED) gated_store<BS, WN, TM, TN, EL::kI8>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
+  else ep_store<BS, WN, TM, TN, EL::kI8>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
 }
 
 // s_waitcnt: at most n vector memory instructions outstanding (n < 64), no LDS read
@@ -416,7 +532,7 @@ constexpr int wait_vm(int n) { return (n & 15) | 7 << 4 | (n >> 4) << 14; }
 // kernel reads, every step of a 64-wide block waited for LDS: one wave per SIMD has 32 cycles of
 // products a step against about 130 of latency.
 // Stages past K read as zeros and touch no memory.
-template <bool A_MN, bool B_MN, int DT, int BS>
+template <bool A_MN, bool B_MN, int DT, int BS, bool GATED>
 __global__ __launch_bounds__(ep_threads(BS)) void gemm_ep_ring(EpArgs g) {
   constexpr int WGM = 2, WGN = ep_threads(BS) / 128;
   // one array a stage, A's image and then B's: the compiler tells the loads in flight apart by array
@@ -433,7 +549,8 @@ __global__ __launch_bounds__(ep_threads(BS)) void gemm_ep_ring(EpArgs g) {
   constexpr int NS = EL::kSteps;
   static_assert(DT == TG_F16 || DT == TG_BF16 || DT == TG_I8 || (DT >= kF8 && DT < kMX), "16-bit, int8 or fp8 operands");
   static_assert(EL::kBytes == 2 || (!A_MN && !B_MN), "8-bit operands are K-contiguous");
-  const EpTile t = ep_tile<BS>(g);
+  static_assert(!GATED || !A_MN, "gated: A [M][K]");
+  const EpTile t = ep_tile<BS, GATED>(g);
   const int tid = (int)threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int wm = (wave / WGN) * WM, wn = (wave % WGN) * WN;
@@ -442,7 +559,8 @@ __global__ __launch_bounds__(ep_threads(BS)) void gemm_ep_ring(EpArgs g) {
   OA oa;
   OB ob;
   oa.init(g.lda, wm, wave, lane);
-  ob.init(g.ldb, wn, wave, lane);
+  ob.init(g.ldb, wn, GATED && !B_MN ? 0 : wave, lane);   // gated: the wave's rows are in its base address
+  if constexpr (GATED && B_MN) gated_mn_dma_offsets<PER, BS * EL::kBytes, WN / 2>(g.ldb, g.N, wave, lane, ob.dma);
   f32x16 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -455,7 +573,7 @@ __global__ __launch_bounds__(ep_threads(BS)) void gemm_ep_ring(EpArgs g) {
       for (int j = 0; j < TN; ++j) acc[i][j] = mfma32t<DT>(b[j], a[i], acc[i][j]);
   };
   constexpr int kReads = OA::kReads + OB::kReads, kMfma = TM * TN, kDma = 2 * PER;
-  const DirectLoads<A_MN, B_MN, DT, BS, OA, OB> load_ab(oa, ob, g, t, wave);
+  const DirectLoads<A_MN, B_MN, DT, BS, GATED, OA, OB> load_ab(oa, ob, g, t, wave);
   const int KT = (t.kl + EL::kBK - 1) / EL::kBK;   // >= 1
   // the barrier alone: __syncthreads would wait for every load
   auto meet = [&](auto n) {
@@ -509,12 +627,13 @@ __global__ __launch_bounds__(ep_threads(BS)) void gemm_ep_ring(EpArgs g) {
   }
   // the zero stages still on their way must land before the epilogue takes the buffers
   meet(std::integral_constant<int, 0>{});
-  ep_store<BS, WN, TM, TN, EL::kI8>(g, t, acc, wave, lane, wm, wn, s0, s1, s2, s3);
+  if constexpr (GATED) gated_store<BS, WN, TM, TN, EL::kI8>(g, t, acc, wave, lane, wm, wn, s0, s1, s2, s3);
+  else ep_store<BS, WN, TM, TN, EL::kI8>(g, t, acc, wave, lane, wm, wn, s0, s1, s2, s3);
 }
 
 // Operands through registers, two stages ahead of the one computed: one register set each for the even
 // and the odd stage.
-template <bool A_MN, bool B_MN, int DT, int BS>
+template <bool A_MN, bool B_MN, int DT, int BS, bool GATED>
 __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_staged(EpArgs g) {
   constexpr int WGM = 2, WGN = ep_threads(BS) / 128;
   __shared__ __attribute__((aligned(1024))) uint8_t sa0[BS * kRowBytes];
@@ -529,7 +648,8 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_sta
   constexpr int NS = EL::kSteps;
   static_assert(DT == TG_F16 || DT == TG_BF16 || DT == TG_I8 || (DT >= kF8 && DT < kMX), "16-bit, int8 or fp8 operands");
   static_assert(EL::kBytes == 2 || (!A_MN && !B_MN), "8-bit operands are K-contiguous");
-  const EpTile t = ep_tile<BS>(g);
+  static_assert(!GATED || !A_MN, "gated: A [M][K]");
+  const EpTile t = ep_tile<BS, GATED>(g);
   const int tid = (int)threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int wm = (wave / WGN) * WM, wn = (wave % WGN) * WN;
@@ -538,7 +658,8 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_sta
   OA oa;
   OB ob;
   oa.init(g.lda, wm, wave, lane);
-  ob.init(g.ldb, wn, wave, lane);
+  ob.init(g.ldb, wn, GATED && !B_MN ? 0 : wave, lane);   // gated: the wave's rows are in its base address
+  if constexpr (GATED && B_MN) gated_mn_dma_offsets<PER, BS * EL::kBytes, WN / 2>(g.ldb, g.N, wave, lane, ob.dma);
   f32x16 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -554,10 +675,12 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_sta
   constexpr int E = EL::kBytes;
   const uint8_t* pa = g.A + (A_MN ? (int64_t)t.k0 * g.lda + t.m0 : (int64_t)t.m0 * g.lda + t.k0) * E;
   const uint8_t* pb = g.B + (B_MN ? (int64_t)t.k0 * g.ldb + t.n0 : (int64_t)t.n0 * g.ldb + t.k0) * E;
-  const int ra = g.M - t.m0, rb = g.N - t.n0;   // rows / columns from here to the end
+  const int bw = GATED ? 2 * g.N : g.N;   // rows or columns of B
+  const int ra = g.M - t.m0, rb = bw - t.n0;   // rows / columns from here to the end
   const int KT = (t.kl + EL::kBK - 1) / EL::kBK;   // >= 1
   StagedFetch<A_MN, PER, DT, BS> fa[2];
-  StagedFetch<B_MN, PER, DT, BS> fb[2];
+  StagedFetch<B_MN, PER, DT, BS, GATED ? WN / 2 : 0> fb[2];
+  if constexpr (GATED) fb[0].half = fb[1].half = g.N;
   auto compute = [&](const uint8_t* xa, const uint8_t* xb) {
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
@@ -567,7 +690,7 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_sta
     }
   };
   constexpr int VE = 16 / E;
-  if (g.K < VE || (A_MN && g.M < VE) || (B_MN && g.N < VE)) {
+  if (g.K < VE || (A_MN && g.M < VE) || (B_MN && bw < VE)) {
     // one stage after the other
     for (int kt = 0; kt < KT; ++kt) {
       fa[0].get_each(pa, g.lda, ra, t.kl, kt, wave, lane);
@@ -587,7 +710,7 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_sta
       fb[set].get(pb, g.ldb, rb, t.kl, s, wave, lane);
       __builtin_amdgcn_sched_barrier(0);   // on their way before the stage's products
     };
-    const bool edge_a = A_MN && ra < BS, edge_b = B_MN && rb < BS;
+    const bool edge_a = A_MN && ra < BS, edge_b = B_MN && (GATED ? 2 * (g.N - t.n0) : rb) < BS;
     auto put = [&](auto q, int s, uint8_t* xa, uint8_t* xb) {
       constexpr int set = decltype(q)::value;
       if (edge_a || s + 1 >= KT) fa[set].fix(ra, t.kl, s, wave, lane);
@@ -616,21 +739,22 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_sta
     }
     if (kt < KT) stage(sa0, sb0, sa1, sb1, kt, S0, S1);
   }
-  ep_store<BS, WN, TM, TN, EL::kI8>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
+  if constexpr (GATED) gated_store<BS, WN, TM, TN, EL::kI8>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
+  else ep_store<BS, WN, TM, TN, EL::kI8>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
 }
 
-template <bool A_MN, bool B_MN, int DT>
+template <bool A_MN, bool B_MN, int DT, bool GATED = false>
 hipError_t launch_ep_one(const EpArgs& g, const EpKernel& k, hipStream_t s) {
   const dim3 grid((unsigned)((int64_t)g.tiles_m * g.tiles_n * g.splits)), block(ep_threads(k.bs));
   if (k.staged) {
-    if (k.bs == 64) hipLaunchKernelGGL((gemm_ep_staged<A_MN, B_MN, DT, 64>), grid, block, 0, s, g);
-    else hipLaunchKernelGGL((gemm_ep_staged<A_MN, B_MN, DT, 128>), grid, block, 0, s, g);
+    if (k.bs == 64) hipLaunchKernelGGL((gemm_ep_staged<A_MN, B_MN, DT, 64, GATED>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((gemm_ep_staged<A_MN, B_MN, DT, 128, GATED>), grid, block, 0, s, g);
   } else if (k.ring) {
-    if (k.bs == 64) hipLaunchKernelGGL((gemm_ep_ring<A_MN, B_MN, DT, 64>), grid, block, 0, s, g);
-    else hipLaunchKernelGGL((gemm_ep_ring<A_MN, B_MN, DT, 128>), grid, block, 0, s, g);
+    if (k.bs == 64) hipLaunchKernelGGL((gemm_ep_ring<A_MN, B_MN, DT, 64, GATED>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((gemm_ep_ring<A_MN, B_MN, DT, 128, GATED>), grid, block, 0, s, g);
   } else {
-    if (k.bs == 256) hipLaunchKernelGGL((gemm_ep_direct<A_MN, B_MN, DT, 256>), grid, block, 0, s, g);
-    else hipLaunchKernelGGL((gemm_ep_direct<A_MN, B_MN, DT, 128>), grid, block, 0, s, g);
+    if (k.bs == 256) hipLaunchKernelGGL((gemm_ep_direct<A_MN, B_MN, DT, 256, GATED>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((gemm_ep_direct<A_MN, B_MN, DT, 128, GATED>), grid, block, 0, s, g);
   }
   return hipGetLastError();
 }

@@ -71,19 +71,20 @@ __device__ __forceinline__ u32x4 k_gather(const uint16_t* p, int64_t ld, int n) 
 struct __attribute__((packed, aligned(2))) Bytes4 { uint32_t v; };
 
 // MT: row tiles of 16.  blockDim.x / 64 waves.
-// NI: column tiles of 16.
-template <bool A_MN, bool B_MN, int DT, int MT, int NI>
+// NI: column tiles of 16.  GATED: the second tile is the up projection's, N rows of B further.
+template <bool A_MN, bool B_MN, int DT, int MT, int NI, bool GATED = false>
 __global__ __launch_bounds__(1024) void gemm_ep_tokens(EpArgs g) {
   using EL = Elem<DT>;
   constexpr int E = EL::kBytes;
   static_assert(!B_MN || NI == 2, "a lane's two columns");
-  constexpr int CN = 16 * NI;                   // most columns of a workgroup
+  static_assert(!GATED || (!B_MN && NI == 2), "a tile of each projection");
+  constexpr int CN = GATED ? 16 : 16 * NI;      // most results of a workgroup's row
   constexpr int KS = B_MN ? 32 : 128 / E;       // K of a step
   constexpr int KI = EL::kFp8 ? 128 : 64 / E;   // K of an instruction
   constexpr int NF = KS / KI;                   // instructions of a step along K
   constexpr int U = MT == 1 && (B_MN || NI == 1) ? 4 : 2;   // steps in flight
   using Frag = typename EL::Frag;               // one instruction's operand: 8 16-bit values, 16 int8, 32 fp8
-  constexpr int LD = CN + 1;
+  constexpr int LD = 16 * NI + 1;
   __shared__ float red[16][MT * 16][LD];
 
   const int nb = (int)gridDim.x;
@@ -101,8 +102,12 @@ __global__ __launch_bounds__(1024) void gemm_ep_tokens(EpArgs g) {
 
   // this thread's first output, and what its epilogue reads: on the way while the sum is taken
   const int orow = (int)threadIdx.x / CN, ocol = n0 + (int)threadIdx.x % CN;
-  EpOne pre{};
-  if (g.splits == 1 && orow < g.M && orow < 16 * MT && ocol < n1) ep_one(g, orow, ocol, pre);
+  typename std::conditional<GATED, GatedOne, EpOne>::type pre{};
+  auto look = [&](int row, int col) {
+    if constexpr (GATED) gated_one(g, row, col, pre);
+    else ep_one(g, row, col, pre);
+  };
+  if (g.splits == 1 && orow < g.M && orow < 16 * MT && ocol < n1) look(orow, ocol);
 
   // what a lane loads of B in a step, before it is made into fragments
   struct Raw {
@@ -129,11 +134,11 @@ __global__ __launch_bounds__(1024) void gemm_ep_tokens(EpArgs g) {
     } else {
 #pragma unroll
       for (int c = 0; c < NI; ++c) {
-        const uint8_t* p = pb + ((int64_t)16 * c * g.ldb + k0) * E;
+        const uint8_t* p = pb + ((int64_t)(GATED ? g.N : 16) * c * g.ldb + k0) * E;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           u32x4 v = {0, 0, 0, 0};
-          if (nc > 16 * c) {
+          if (nc > (GATED ? 0 : 16 * c)) {
             if constexpr (kPartial) v = k_chunk<E>(p + 16 * h, left - h * (16 / E));
             else v = load16(p + 16 * h);
           }
@@ -249,10 +254,14 @@ __global__ __launch_bounds__(1024) void gemm_ep_tokens(EpArgs g) {
     const int row = o / CN, col_o = n0 + o % CN;
     if (row >= g.M || col_o >= n1) continue;
     const float v = sum(row, o % CN);
-    if (g.splits > 1) {
+    if constexpr (GATED) {
+      const float u = sum(row, 16 + o % CN);
+      if (o != (int)threadIdx.x) look(row, col_o);
+      gated_finish1(g, row, col_o, pre, v, u);
+    } else if (g.splits > 1) {
       g.part[((int64_t)split * g.M + row) * g.part_ld + col_o] = v;
     } else {
-      if (o != (int)threadIdx.x) ep_one(g, row, col_o, pre);
+      if (o != (int)threadIdx.x) look(row, col_o);
       ep_finish1(g, row, col_o, pre, v);
     }
   }
@@ -278,7 +287,26 @@ hipError_t go16(const EpArgs& g, int ta, int tb, int waves, hipStream_t s) {
   return tb ? go<false, false, DT>(g, waves, s) : go<false, true, DT>(g, waves, s);
 }
 
+template <int DT>
+hipError_t go_gated(const EpArgs& g, int waves, hipStream_t s) {
+  const dim3 grid((unsigned)(((int64_t)g.N + g.cn - 1) / g.cn)), block(64 * (unsigned)waves);
+  if (g.M <= 16) hipLaunchKernelGGL((gemm_ep_tokens<false, false, DT, 1, 2, true>), grid, block, 0, s, g);
+  else hipLaunchKernelGGL((gemm_ep_tokens<false, false, DT, 2, 2, true>), grid, block, 0, s, g);
+  return hipGetLastError();
+}
+
 }  // namespace
+
+hipError_t launch_gated_tokens(const EpArgs& g, int a_dtype, int b_dtype, int waves, hipStream_t s) {
+  if (a_dtype == TG_F16) return go_gated<TG_F16>(g, waves, s);
+  if (a_dtype == TG_BF16) return go_gated<TG_BF16>(g, waves, s);
+  if (a_dtype == TG_I8) return go_gated<TG_I8>(g, waves, s);
+  const bool a5 = a_dtype == TG_FP8_E5M2, b5 = b_dtype == TG_FP8_E5M2;
+  if (a5 && b5) return go_gated<fp8_code(1, 1)>(g, waves, s);
+  if (a5) return go_gated<fp8_code(1, 0)>(g, waves, s);
+  if (b5) return go_gated<fp8_code(0, 1)>(g, waves, s);
+  return go_gated<fp8_code(0, 0)>(g, waves, s);
+}
 
 hipError_t launch_ep_tokens(const EpArgs& g, int trans_a, int trans_b, int a_dtype, int b_dtype, int waves,
                             hipStream_t s) {

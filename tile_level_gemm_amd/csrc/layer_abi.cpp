@@ -90,9 +90,11 @@ struct EpChoice {
   bool ring;       // direct blocks in the four-stage ring
 };
 
-int64_t part_ld(int64_t N) { return (N + 7) / 8 * 8; }
+// Floats of a row of partial sums: whole 32 bytes; gated (N columns of both projections together): for each of them.
+int64_t part_ld(int64_t N, bool gated) { return gated ? 2 * ((N / 2 + 7) / 8 * 8) : (N + 7) / 8 * 8; }
 
-EpChoice choose_ep(int64_t M, int64_t N, int64_t K, int transB, int eb, bool direct, int64_t budget) {
+// N: columns of B; gated: half as many of D, and blocks and workgroups take half as many of either projection.
+EpChoice choose_ep(int64_t M, int64_t N, int64_t K, int transB, int eb, bool direct, bool gated, int64_t budget) {
   EpChoice c{TG_EP_NONE, 0, 1, K, 0, 0, 0, false};
   if (M == 0 || N == 0) return c;
   if (K == 0) {
@@ -105,16 +107,18 @@ EpChoice choose_ep(int64_t M, int64_t N, int64_t K, int transB, int eb, bool dir
   // blocks 9.3); 17 to 32 rows of 16 bits read A twice over (24 x 4096 x 4096 13.2 us, blocks 11.1;
   // 32 x 1024 x 1024 5.4, blocks 6.0; fp8 32 x 8192 x 4096 11.6, blocks 12.9).
   const bool blocks_win = direct && (!transB ? N * K > (int64_t)1 << 23 : M > 16 && eb == 2 && N * K > (int64_t)1 << 22);
-  if (M <= kTokenRows && !blocks_win) {
+  // gated weights [K][2N]: blocks alone
+  if (M <= kTokenRows && !blocks_win && (transB || !gated)) {
     c.kernel = TG_EP_TOKENS;
     if (transB) {
       // a workgroup for every CU, and no more where N has them to spare
       c.cn = N >= 8192 ? 32 : N >= 4096 ? 16 : N >= 2048 ? 8 : 4;
+      if (gated) c.cn = std::max(4, c.cn / 2);
     } else {
       // 64 bytes of each k-row: parts of K of at least 1024 rows (64 KB, 2.5 us, where the join costs
       // 3 us) while there are fewer than 256 workgroups
       c.cn = 32;
-      const int64_t per = M * part_ld(N) * 4;
+      const int64_t per = M * part_ld(N, gated) * 4;
       int64_t s = std::min<int64_t>(256 / ((N + 31) / 32), K / 1024);
       if (budget >= 0) s = std::min(s, budget / per);
       if (s >= 2) {
@@ -157,7 +161,7 @@ EpChoice choose_ep(int64_t M, int64_t N, int64_t K, int transB, int eb, bool dir
     c.ring = direct;
     s = std::min(256 / blocks(64), steps / 16);
   }
-  const int64_t per = M * part_ld(N) * 4;
+  const int64_t per = M * part_ld(N, gated) * 4;
   if (budget >= 0) s = std::min(s, budget / per);
   if (s < 2) return c;
   int64_t each = (steps + s - 1) / s;
@@ -183,11 +187,14 @@ bool direct_operand(const void* p, int64_t ld, bool mn, int64_t extent, int64_t 
 
 int plan_ep(const void* A, const void* B, const void* D, int64_t M, int64_t N, int64_t K, int64_t lda,
             int64_t ldb, int64_t ldd, int transA, int transB, int a_dtype, int b_dtype, int d_dtype,
-            const tg_epilogue* ep, const void* ws, int64_t ws_bytes, tg_ep_plan* plan, EpArgs* g) {
+            const tg_epilogue* ep, const void* ws, int64_t ws_bytes, tg_ep_plan* plan, EpArgs* g, bool gated = false) {
   static const tg_epilogue kNone{};
   if (!ep) ep = &kNone;
-  int st = check_extents(M, N, K);
+  const int64_t W = gated && N <= kMaxDim ? 2 * N : N;   // columns of B
+  int st = check_extents(M, W, K);
   if (st) return st;
+  if (gated && ep->residual) return fail(TG_E_ARG, "a gated product takes no residual");
+  if (gated && transA) return fail(TG_E_LAYOUT, "a gated product's A is stored [M,K]");
   if (!((is16(a_dtype) || a_dtype == TG_I8) && a_dtype == b_dtype) && !(isf8(a_dtype) && isf8(b_dtype)))
     return fail(TG_E_DTYPE, fmt("operands must both be TG_F16, both TG_BF16, both TG_I8, or both fp8 (got %lld, %lld)",
                                 a_dtype, b_dtype));
@@ -203,9 +210,9 @@ int plan_ep(const void* A, const void* B, const void* D, int64_t M, int64_t N, i
     return fail(TG_E_LAYOUT, "8-bit operands are stored A [M,K], B [N,K] (transA 0, transB 1)");
   int64_t ldr = ep->ld_residual, ldz = ep->ld_z;
   if ((st = resolve_ld("lda", &lda, transA ? M : K, transA ? K : M)) ||
-      (st = resolve_ld("ldb", &ldb, transB ? K : N, transB ? N : K)) ||
+      (st = resolve_ld("ldb", &ldb, transB ? K : W, transB ? W : K)) ||
       (st = resolve_ld("ldd", &ldd, N, M)) || (ep->residual && (st = resolve_ld("ld_residual", &ldr, N, M))) ||
-      (ep->Z && (st = resolve_ld("ld_z", &ldz, N, M))))
+      (ep->Z && (st = resolve_ld("ld_z", &ldz, W, M))))
     return st;
   if ((st = check_workspace(ws, ws_bytes))) return st;
   *plan = tg_ep_plan{};
@@ -218,12 +225,12 @@ int plan_ep(const void* A, const void* B, const void* D, int64_t M, int64_t N, i
       (ep->bias && misaligned(ep->bias, bytes_of(ep->bias_dtype))) || misaligned(ep->row_scale, 4) ||
       misaligned(ep->col_scale, 4))
     return fail(TG_E_ALIGN, "a pointer is not aligned to its element");
-  const Mat md = mat(D, M, N, ldd, db), mz = mat(ep->Z, M, N, ldz, db), mr = mat(ep->residual, M, N, ldr, db);
+  const Mat md = mat(D, M, N, ldd, db), mz = mat(ep->Z, M, W, ldz, db), mr = mat(ep->residual, M, N, ldr, db);
   const Mat mw = vec(ws, ws_bytes, 1);
   const Mat ins[] = {K > 0 ? mat(A, transA ? K : M, transA ? M : K, lda, eb) : Mat{},
-                     K > 0 ? mat(B, transB ? N : K, transB ? K : N, ldb, eb) : Mat{},
-                     ep->bias ? vec(ep->bias, N, bytes_of(ep->bias_dtype)) : Mat{}, vec(ep->row_scale, M, 4),
-                     vec(ep->col_scale, N, 4)};
+                     K > 0 ? mat(B, transB ? W : K, transB ? K : W, ldb, eb) : Mat{},
+                     ep->bias ? vec(ep->bias, W, bytes_of(ep->bias_dtype)) : Mat{}, vec(ep->row_scale, M, 4),
+                     vec(ep->col_scale, W, 4)};
   for (const Mat& in : ins)
     if (overlaps(md, in) || overlaps(mz, in) || overlaps(mw, in))
       return fail(TG_E_ALIAS, "an output or the workspace overlaps an input");
@@ -232,8 +239,9 @@ int plan_ep(const void* A, const void* B, const void* D, int64_t M, int64_t N, i
   if (overlaps(md, mz) || overlaps(md, mw) || overlaps(mz, mw))
     return fail(TG_E_ALIAS, "D, Z and the workspace must not overlap");
 
+  // gated weights [K][2N]: chunks of either half stay inside it where N's do
   const bool direct = K > 0 && direct_operand(A, lda, transA, M, K, eb) && direct_operand(B, ldb, !transB, N, K, eb);
-  const EpChoice c = choose_ep(M, N, K, transB, eb, direct, ws_bytes);
+  const EpChoice c = choose_ep(M, W, K, transB, eb, direct, gated, ws_bytes);
   plan->kernel = c.kernel;
   plan->splits = c.splits;
   plan->k_per_split = (int32_t)c.kps;
@@ -241,7 +249,7 @@ int plan_ep(const void* A, const void* B, const void* D, int64_t M, int64_t N, i
   if (c.bs) {
     plan->block_m = plan->block_n = c.bs;
     plan->block_k = 128 / eb;
-    plan->grid = ((M + c.bs - 1) / c.bs) * ((N + c.bs - 1) / c.bs) * c.splits;
+    plan->grid = ((M + c.bs - 1) / c.bs) * ((W + c.bs - 1) / c.bs) * c.splits;
   } else if (c.kernel == TG_EP_TOKENS) {
     plan->block_m = M <= 16 ? 16 : 32;
     plan->block_n = c.cn;
@@ -266,7 +274,7 @@ int plan_ep(const void* A, const void* B, const void* D, int64_t M, int64_t N, i
   g->K = (int32_t)K;
   if (c.bs) {
     g->tiles_m = (int32_t)((M + c.bs - 1) / c.bs);
-    g->tiles_n = (int32_t)((N + c.bs - 1) / c.bs);
+    g->tiles_n = (int32_t)((W + c.bs - 1) / c.bs);   // gated: of bs / 2 results
   }
   g->waves = c.waves;
   g->cn = c.cn;
@@ -274,7 +282,7 @@ int plan_ep(const void* A, const void* B, const void* D, int64_t M, int64_t N, i
   g->splits = c.splits;
   g->k_per_split = (int32_t)c.kps;
   g->part = (float*)const_cast<void*>(ws);
-  g->part_ld = part_ld(N);
+  g->part_ld = part_ld(W, gated);
   g->bias = (const uint8_t*)ep->bias;
   g->res = (const uint8_t*)ep->residual;
   g->Z = (uint8_t*)ep->Z;
@@ -303,7 +311,18 @@ int run_ep(const EpArgs& g, const tg_ep_plan& p, int transA, int transB, int a_d
                                                                     {p.block_m, p.kernel == TG_EP_STAGED, g.ring != 0}, s));
     if (st || g.splits == 1) return st;
   }
-  return hip_status("tile_gemm_ep join", launch_ep_join(g, s));
+  return hip_status("tile_gemm_ep join", launch_ep_join(g, false, s));
+}
+int run_gated(const EpArgs& g, const tg_ep_plan& p, int transB, int a_dtype, int b_dtype, hipStream_t s) {
+  if (p.kernel == TG_EP_NONE) return TG_OK;
+  if (p.kernel != TG_EP_JOIN) {
+    const int st = hip_status("tile_gemm_gated", p.kernel == TG_EP_TOKENS
+                                                     ? launch_gated_tokens(g, a_dtype, b_dtype, g.waves, s)
+                                                     : launch_gated_block(g, transB, a_dtype, b_dtype,
+                                                                          {p.block_m, p.kernel == TG_EP_STAGED, g.ring != 0}, s));
+    if (st || g.splits == 1) return st;
+  }
+  return hip_status("tile_gemm_gated join", launch_ep_join(g, true, s));
 }
 
 // Row groups of the bias gradient, one workgroup each per 64 columns: one up to 256 rows (no second
@@ -482,7 +501,7 @@ int64_t tile_gemm_ep_workspace(int64_t M, int64_t N, int64_t K, int transA, int 
   (void)transA;
   // the direct and the staged kernel can differ in block size: the larger need
   const int eb = bytes_of(a_dtype);
-  return std::max(choose_ep(M, N, K, transB, eb, true, -1).ws, choose_ep(M, N, K, transB, eb, false, -1).ws);
+  return std::max(choose_ep(M, N, K, transB, eb, true, false, -1).ws, choose_ep(M, N, K, transB, eb, false, false, -1).ws);
 }
 
 int tile_gemm_ep_plan(const void* A, const void* B, const void* D, int64_t M, int64_t N, int64_t K,
@@ -626,6 +645,122 @@ int tile_gemm_ep_bwd_scaled(const void* dY, const void* Z, const void* A, const 
     return st;
   if (dB && (st = transB ? run_ep(gb, pb, 1, transA, dtype, dtype, s) : run_ep(gb, pb, !transA, 0, dtype, dtype, s)))
     return st;
+  return TG_OK;
+}
+
+int64_t tile_gemm_gated_workspace(int64_t M, int64_t N, int64_t K, int transB, int a_dtype) {
+  if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim / 2 || K > kMaxDim || (!is16(a_dtype) && !is8(a_dtype))) return 0;
+  const int eb = bytes_of(a_dtype);
+  return std::max(choose_ep(M, 2 * N, K, transB, eb, true, true, -1).ws, choose_ep(M, 2 * N, K, transB, eb, false, true, -1).ws);
+}
+
+int tile_gemm_gated_plan(const void* A, const void* B, const void* D, int64_t M, int64_t N, int64_t K, int64_t lda,
+                         int64_t ldb, int64_t ldd, int transB, int a_dtype, int b_dtype, int d_dtype,
+                         const tg_epilogue* ep, const void* workspace, int64_t workspace_bytes, tg_ep_plan* out) {
+  clear_error();
+  if (!out) return fail(TG_E_ARG, "out is NULL");
+  EpArgs g;
+  return plan_ep(A, B, D, M, N, K, lda, ldb, ldd, 0, transB, a_dtype, b_dtype, d_dtype, ep, workspace, workspace_bytes,
+                 out, &g, true);
+}
+
+int tile_gemm_gated(const void* A, const void* B, void* D, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb,
+                    int64_t ldd, int transB, int a_dtype, int b_dtype, int d_dtype, const tg_epilogue* ep,
+                    void* workspace, int64_t workspace_bytes, void* stream) {
+  clear_error();
+  tg_ep_plan p;
+  EpArgs g;
+  const int st = plan_ep(A, B, D, M, N, K, lda, ldb, ldd, 0, transB, a_dtype, b_dtype, d_dtype, ep, workspace,
+                         workspace_bytes, &p, &g, true);
+  if (st) return st;
+  return run_gated(g, p, transB, a_dtype, b_dtype, (hipStream_t)stream);
+}
+
+int64_t tile_gemm_gated_bwd_workspace(int64_t M, int64_t N, int64_t K, int transB, int dtype) {
+  if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim / 2 || K > kMaxDim || !is16(dtype)) return 0;
+  const int64_t groups = bias_groups(M, N), W = 2 * N;
+  int64_t ws = groups > 1 ? groups * W * 4 : 0;
+  ws = std::max(ws, tile_gemm_ep_workspace(M, K, W, 0, !transB, dtype));
+  ws = std::max(ws, transB ? tile_gemm_ep_workspace(W, K, M, 1, 0, dtype) : tile_gemm_ep_workspace(K, W, M, 1, 0, dtype));
+  return ws;
+}
+
+int tile_gemm_gated_bwd(const void* dY, const void* Z, const void* A, const void* B, const float* row_scale,
+                        const float* col_scale, void* dZ, void* dA, void* dB, float* dbias, int64_t M, int64_t N,
+                        int64_t K, int64_t ld_dy, int64_t ld_z, int64_t lda, int64_t ldb, int transB, int dtype, int act,
+                        void* workspace, int64_t workspace_bytes, void* stream) {
+  clear_error();
+  const int64_t W = N <= kMaxDim ? 2 * N : N;
+  int st = check_extents(M, W, K);
+  if (st) return st;
+  if (!is16(dtype)) return fail(TG_E_DTYPE, fmt("dtype must be TG_F16 or TG_BF16 (got %lld)", dtype));
+  if (transB != 0 && transB != 1) return fail(TG_E_ARG, "transB must be 0 or 1");
+  if (act < TG_ACT_NONE || act > TG_ACT_SILU) return fail(TG_E_ARG, fmt("unknown activation %lld", act));
+  if ((st = resolve_ld("ld_dy", &ld_dy, N, M)) || (st = resolve_ld("ld_z", &ld_z, W, M)) ||
+      (st = resolve_ld("lda", &lda, K, M)) || (st = resolve_ld("ldb", &ldb, transB ? K : W, transB ? W : K)))
+    return st;
+  if ((st = check_workspace(workspace, workspace_bytes))) return st;
+  const bool outs = M > 0 && N > 0;
+  if (outs && (!dY || !Z || !dZ)) return fail(TG_E_NULL, "dY, Z or dZ is NULL");
+  if ((dA && outs && K > 0 && !B) || (dB && outs && K > 0 && !A)) return fail(TG_E_NULL, "dA needs B, dB needs A");
+  const void* all2[] = {dY, Z, A, B, dZ, dA, dB};
+  for (const void* p : all2)
+    if (misaligned(p, 2)) return fail(TG_E_ALIGN, "a pointer is not aligned to its element");
+  if (misaligned(dbias, 4) || misaligned(row_scale, 4) || misaligned(col_scale, 4))
+    return fail(TG_E_ALIGN, "dbias, row_scale and col_scale must be 4-byte aligned");
+  const Mat mz = mat(Z, M, W, ld_z, 2), mdz = mat(dZ, M, W, W, 2);
+  const Mat ins[] = {mat(dY, M, N, ld_dy, 2), mz, mat(dB ? A : nullptr, M, K, lda, 2),
+                     mat(dA ? B : nullptr, transB ? W : K, transB ? K : W, ldb, 2), vec(row_scale, M, 4), vec(col_scale, W, 4)};
+  const Mat results[] = {mat(dA, 1, M * K, M * K, 2), mat(dB, 1, K * W, K * W, 2), vec(dbias, W, 4), vec(workspace, workspace_bytes, 1)};
+  for (const Mat& o : results) {
+    for (const Mat& in : ins)
+      if (overlaps(o, in)) return fail(TG_E_ALIAS, "an output or the workspace overlaps an input");
+    if (overlaps(o, mdz)) return fail(TG_E_ALIAS, "an output or the workspace overlaps dZ");
+  }
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 4; ++j)
+      if (overlaps(results[i], results[j])) return fail(TG_E_ALIAS, "outputs and the workspace must not overlap");
+  for (int i = 0; i < 6; ++i)
+    if (overlaps(mdz, ins[i]) && !(i == 1 && same(mdz, mz))) return fail(TG_E_ALIAS, "dZ overlaps an input without being exactly Z");
+
+  // both products are planned before anything is launched: dA[M,K] = dZ·B^T; dB[K,2N] = A^T·dZ, or stored
+  // [2N,K]: dZ^T·A
+  tg_ep_plan pa{}, pb{};
+  EpArgs ga, gb;
+  if (dA && (st = plan_ep(dZ, B, dA, M, K, W, W, ldb, 0, 0, !transB, dtype, dtype, dtype, nullptr, workspace, workspace_bytes,
+                          &pa, &ga)))
+    return st;
+  if (dB) {
+    st = transB ? plan_ep(dZ, A, dB, W, K, M, W, lda, 0, 1, 0, dtype, dtype, dtype, nullptr, workspace, workspace_bytes, &pb, &gb)
+                : plan_ep(A, dZ, dB, K, W, M, lda, W, 0, 1, 0, dtype, dtype, dtype, nullptr, workspace, workspace_bytes, &pb, &gb);
+    if (st) return st;
+  }
+  hipStream_t s = (hipStream_t)stream;
+  const char* what = "tile_gemm_gated_bwd";
+  if (dbias && N > 0 && M == 0 && (st = hip_status(what, launch_sum_rows(dbias, 0, W, dbias, s)))) return st;   // a sum of nothing
+  if (outs) {
+    int64_t groups = bias_groups(M, N);
+    if (dbias) groups = std::max<int64_t>(1, std::min(groups, workspace_bytes / (4 * W)));
+    ActGradArgs a{};
+    a.dY = (const uint8_t*)dY;
+    a.Z = (const uint8_t*)Z;
+    a.dZ = (uint8_t*)dZ;
+    a.rs = row_scale;
+    a.cs = col_scale;
+    a.ldy = ld_dy;
+    a.ldz = ld_z;
+    a.M = (int32_t)M;
+    a.N = (int32_t)N;
+    a.rows_per = (int32_t)((M + groups - 1) / groups);
+    groups = (M + a.rows_per - 1) / a.rows_per;
+    a.t = dtype;
+    a.act = act;
+    a.sums = !dbias ? nullptr : groups > 1 ? (float*)workspace : dbias;
+    if ((st = hip_status(what, launch_gated_grad(a, (int)groups, s)))) return st;
+    if (dbias && groups > 1 && (st = hip_status(what, launch_sum_rows((const float*)workspace, groups, W, dbias, s)))) return st;
+  }
+  if (dA && (st = run_ep(ga, pa, 0, !transB, dtype, dtype, s))) return st;
+  if (dB && (st = run_ep(gb, pb, 1, 0, dtype, dtype, s))) return st;
   return TG_OK;
 }
 

@@ -27,6 +27,15 @@ constexpr StagedPlace staged_place(int stage, int bk, int ve, int row, int chunk
 constexpr int64_t staged_offset(StagedPlace p, int64_t ld, int lines, int width, int ve) {
   return (int64_t)staged_min(p.line, lines - 1) * ld + staged_min(p.first, width - ve);
 }
+// Row (K-major) or column (M/N-major) of the operand, from the block's first gate one, behind row or column `i` of
+// a gated block: groups of r of the gate's and of those `n` further, the up projection's, by turns.  Where the
+// last block has gate rows or columns past the n-th, they are up ones: inside the operand, and feeding only
+// outputs that are not stored.
+constexpr int gated_index(int i, int r, int n) { return i / (2 * r) * r + i % r + (i / r % 2) * n; }
+template <bool MN>
+constexpr StagedPlace gated_place(StagedPlace p, int r, int n) {
+  return MN ? StagedPlace{p.line, gated_index(p.first, r, n)} : StagedPlace{gated_index(p.line, r, n), p.first};
+}
 // Elements to shift the loaded chunk down by, zeros from above: how far it was moved, all of it for K past
 // the end (a row or column past the end feeds only outputs that are not stored).
 template <bool MN>

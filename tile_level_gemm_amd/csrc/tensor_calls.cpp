@@ -235,6 +235,85 @@ PyObject* gemm_ep(PyObject* const* a) {
   return Py_BuildValue("(NN)", wrap(out), wrap(Z));
 }
 
+// Columns of a gated product: half of B's.
+int64_t gated_columns(int64_t n) {
+  if (n % 2) refuse(TG_E_SHAPE, "B has the columns of two projections, got ", n);
+  return n / 2;
+}
+
+// A, B, bias, act, row_scale, col_scale, trans_b, out_dtype, keep_z, out
+PyObject* gemm_gated(PyObject* const* a) {
+  const Tensor &A = *tensor("A", a[0]), &B = *tensor("B", a[1]), *bias = tensor("bias", a[2], true);
+  const Tensor *rs = tensor("row_scale", a[4], true), *cs = tensor("col_scale", a[5], true);
+  const Tensor* given = tensor("out", a[9], true);
+  const bool tb = truth(a[6]), keep_z = truth(a[8]);
+  const Extents e = extents(A, B, false, tb);
+  const int64_t N = gated_columns(e.N);
+  const int at = dtype_code("A", A.scalar_type()), bt = dtype_code("B", B.scalar_type());
+  const bool eight = at == TG_FP8_E4M3 || at == TG_FP8_E5M2 || at == TG_I8;
+  const at::ScalarType out_t = a[7] != Py_None ? scalar_type("out_dtype", a[7])
+                               : given         ? given->scalar_type()
+                               : eight         ? at::kBFloat16
+                                               : A.scalar_type();
+  const int dt = dtype_code("out_dtype", out_t);
+  tg_epilogue ep{};
+  ep.act = (int32_t)integer(a[3]);
+  if (bias) {
+    vector("bias", *bias, e.N);
+    if (!is_float(bias->scalar_type())) refuse(TG_E_DTYPE, "bias: unsupported dtype ", bias->scalar_type());
+    ep.bias = address(bias);
+    ep.bias_dtype = code_of(bias->scalar_type());
+  }
+  if (rs) f32_vector("row_scale", *rs, e.M);
+  if (cs) f32_vector("col_scale", *cs, e.N);
+  ep.row_scale = (const float*)address(rs);
+  ep.col_scale = (const float*)address(cs);
+  const int64_t ldd = given ? matrix("out", *given, e.M, N, out_t) : 0;
+  const at::Device dev = one_gpu({&A, &B, bias, rs, cs, given});
+  Tensor out = given ? *given : make({e.M, N}, out_t, dev), Z, ws;
+  if (keep_z) Z = make({e.M, e.N}, out_t, dev);
+  ep.Z = address(Z);
+  const int64_t nb = tile_gemm_gated_workspace(e.M, N, e.K, tb, at);
+  if (nb) ws = make({nb}, at::kByte, dev);
+  check(tile_gemm_gated(address(&A), address(&B), address(out), e.M, N, e.K, e.lda, e.ldb, ldd, tb, at, bt, dt, &ep,
+                        address(ws), nb, stream_of(dev)));
+  written(given);
+  no_history("gemm_gated", {&A, &B, bias, rs, cs});
+  if (given && !keep_z) {
+    Py_INCREF(a[9]);
+    return a[9];
+  }
+  if (!keep_z) return wrap(out);
+  return Py_BuildValue("(NN)", wrap(out), wrap(Z));
+}
+
+// dY, A, B, Z, act, trans_b, need_dA, need_dB, need_dbias, row_scale, col_scale
+PyObject* gemm_gated_backward(PyObject* const* a) {
+  const Tensor &dY = *tensor("dY", a[0]), &A = *tensor("A", a[1]), &B = *tensor("B", a[2]), &Z = *tensor("Z", a[3]);
+  const Tensor *rs = tensor("row_scale", a[9], true), *cs = tensor("col_scale", a[10], true);
+  const int act = (int)integer(a[4]);
+  const bool tb = truth(a[5]);
+  const Extents e = extents(A, B, false, tb);
+  const int64_t N = gated_columns(e.N);
+  const at::ScalarType st = A.scalar_type();
+  if (B.scalar_type() != st) refuse(TG_E_DTYPE, "B must be ", st, ", got ", B.scalar_type());
+  const int t = dtype_code("A", st);
+  const int64_t ldy = matrix("dY", dY, e.M, N, st), ldz = matrix("Z", Z, e.M, e.N, st);
+  if (rs) f32_vector("row_scale", *rs, e.M);
+  if (cs) f32_vector("col_scale", *cs, e.N);
+  const at::Device dev = one_gpu({&dY, &A, &B, &Z, rs, cs});
+  Tensor dZ = make({e.M, e.N}, st, dev), dA, dB, dbias, ws;
+  if (truth(a[6])) dA = make(A.sizes(), st, dev);
+  if (truth(a[7])) dB = make(B.sizes(), st, dev);
+  if (truth(a[8])) dbias = make({e.N}, at::kFloat, dev);
+  const int64_t nb = tile_gemm_gated_bwd_workspace(e.M, N, e.K, tb, t);
+  if (nb) ws = make({nb}, at::kByte, dev);
+  check(tile_gemm_gated_bwd(address(&dY), address(&Z), address(&A), address(&B), (const float*)address(rs),
+                            (const float*)address(cs), address(dZ), address(dA), address(dB), (float*)address(dbias), e.M,
+                            N, e.K, ldy, ldz, e.lda, e.ldb, tb, t, act, address(ws), nb, stream_of(dev)));
+  return Py_BuildValue("(NNNN)", wrap(dZ), wrap(dA), wrap(dB), wrap(dbias));
+}
+
 // dY, A, B, Z, act, trans_a, trans_b, need_dA, need_dB, need_dbias, row_scale, col_scale
 PyObject* gemm_ep_backward(PyObject* const* a) {
   const Tensor &dY = *tensor("dY", a[0]), &A = *tensor("A", a[1]), &B = *tensor("B", a[2]);
@@ -447,7 +526,8 @@ PyObject* set_error_class(PyObject*, PyObject* c) {
 }
 
 #define TG_METHOD(f, n) {#f, (PyCFunction)(void (*)(void))(entry<f, n>), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {TG_METHOD(gemm_ep, 12), TG_METHOD(gemm_ep_backward, 12), TG_METHOD(rms_norm, 7),
+PyMethodDef methods[] = {TG_METHOD(gemm_ep, 12), TG_METHOD(gemm_ep_backward, 12),
+                         TG_METHOD(gemm_gated, 10), TG_METHOD(gemm_gated_backward, 11), TG_METHOD(rms_norm, 7),
                          TG_METHOD(rms_norm_backward, 6), TG_METHOD(layer_norm, 8),
                          TG_METHOD(layer_norm_backward, 8), TG_METHOD(quantize_rows, 3),
                          {"set_error_class", set_error_class, METH_O, nullptr},
