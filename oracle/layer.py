@@ -204,8 +204,10 @@ def layer_norm_backward(dY, H, w, mean, rstd, dH, out):
 
 
 def quantised_rows(X, fmt):
-    """(codes before their rounding, scales): the scale is an fp32 quotient, and the codes are X by it."""
-    s = (np.maximum(np.abs(X).max(axis=1), AMAX_FLOOR).astype(np.float32) / np.float32(QMAX[fmt])).astype(np.float64)
+    """(codes before their rounding, scales): the scale is an fp32 quotient, for integers the fp32 product
+    with the fp32 value of 1/127, and the codes are X by it."""
+    top = np.maximum(np.abs(X).max(axis=1), AMAX_FLOOR).astype(np.float32)
+    s = (top * (np.float32(1) / np.float32(127)) if fmt == "i8" else top / np.float32(QMAX[fmt])).astype(np.float64)
     return X / s[:, None], s
 
 

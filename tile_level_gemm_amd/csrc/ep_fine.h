@@ -1,0 +1,238 @@
+// 256-wide blocks of the products with an epilogue on the 16-row matrix instructions (ep.h has the formulas).
+//
+// gemm_ep_direct's blocks, stages, loads and epilogue with v_mfma_*_16x16x* in place of 32x32x*.  The two do
+// the same operations in the same cycles from the same bytes of LDS, but the large products run at the clock
+// that the power limit leaves, and there the 16-row form is cheaper: nothing but matrix instructions on random
+// operands runs at 2000 TFLOP/s in bf16 and 4050 in int8, 32-row ones at 1450 and 2850 (on zeros both reach
+// 2450 and 4900).
+//
+// A lane carries 16 bytes of K of row l%16 (fp8: 32), K-group l/16, so an instruction takes 64 bytes of K
+// (fp8: 128), and a wave's 128 x 64 results are 8 x 4 tiles.  The wave's products of a K step run in phases of
+// PT row tiles against all four column tiles; while one phase runs, the row fragments of the next are read
+// into the other half of the registers (and with the last phase of a step the next step's column fragments),
+// so every read has a phase's 16 products, twice that with the SIMD's other wave, to arrive.  Gated blocks
+// have waves of 64 rows by 128 columns, 64 of each projection, so that a wave holds whole 128-byte lines of
+// its results; there the column fragments go by phases.
+//
+// LDS holds three stages of A and two of B, all of its 160 KB.  The barrier of a stage comes before its last
+// phase, all of whose fragments are in registers: that phase covers the first reads of the next stage and the
+// issue of B's loads of the one after it, and the next stage's first phase the issue of A's.  So the loads go
+// out in two bursts of half a stage, A's have two stages' time to arrive, and the wait at the barrier leaves
+// A's latest in flight.
+//
+// Measured, 8192 x 16384 x 4096 bf16, all back to back on one card: gemm_ep_direct 800 us (K loop 753), this with
+// two stages of both 748 (697), with three of A 735 (685), the vendor library's product 681.  The epilogue is
+// what is left: as a gated product with Z (402 MB of results) 770 us in waves of 64 x 128, 795 in waves of
+// 128 x 64, whose lines of D are halves.  Results straight from the registers, and a workgroup a CU that loads
+// the next block's first stages before it stores, both spilled and were slower.
+//
+// Internal header, on top of ep_gemm.h.
+#pragma once
+
+#include "ep_gemm.h"
+#include "mfma16.h"
+
+namespace tg {
+namespace {
+
+// Swizzles of 16-row fragments.  A K-major read of 16 bytes a lane takes four cycles of 16 lanes each: lanes 0-3,
+// 12-15 and 20-27 meet in the first, 4-11, 16-19 and 28-31 in the second, the others 32 lanes further.  Lanes
+// 16 apart read the same row one chunk further, so with the chunk XOR the row's low three bits either cycle's
+// 16 lanes hit every 16-byte slot of 256 bytes once (row parity, eight chunks); the fourth row bit that the
+// 32-row fragments need makes two lanes meet here (8 cycles a read; 8192 x 16384 x 4096 on zeros 634 us, without
+// 616).
+__device__ __forceinline__ uint32_t fine_sk(uint32_t r) { return r & 7u; }
+// M/N-major stages:  A transposing read's four 16-lane groups take two chunks
+// of four consecutive k-rows each, the groups' k-rows 8 apart: 2(k & 3) sends a group's rows to distinct chunk
+// pairs of 128 bytes, and 8 for every second group to the other 128 of 256 bytes.
+__device__ __forceinline__ uint32_t fine_sm(uint32_t k) { return ((k & 3u) << 1) ^ (k & 8u); }
+
+// Operand of one wave: fragments of 16 rows or columns; loads and LDS stages as Operand's, M/N-major stages
+// with the swizzle above.  R: of a gated block's [K][2N] weights, columns of a group (0: not gated), n: their N.
+template <bool MN, int PER, int DT, int BS, int R>
+struct FineOperand : Operand<MN, 1, PER, DT, BS> {
+  using EL = Elem<DT>;
+  using Frag = typename EL::Frag;
+  static constexpr int kSteps = EL::kFp8 ? 1 : 2;   // K steps of a stage
+  static constexpr int kRowB = BS * EL::kBytes;
+  static constexpr int kTileReads = MN || EL::kFp8 ? 2 : 1;
+  uint32_t at[2];   // K-major: byte offset of each 64 bytes of the row's stage; M/N-major: of tile 0
+
+  __device__ __forceinline__ void setup(int64_t ld, int base, int dma_wave, int lane, int n) {
+    const uint32_t g = (uint32_t)lane >> 4, j = (uint32_t)lane & 15u;
+    if constexpr (MN) {
+      static_assert(!EL::kFp8 && EL::kBytes == 2 && BS == 256, "16-bit M/N-major operands of 256-wide blocks");
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {   // two k-rows of 32 chunks an instruction
+        const uint32_t k = 2u * (uint32_t)(PER * dma_wave + p) + (uint32_t)lane / 32u;
+        const uint32_t c = ((uint32_t)lane % 32u) ^ fine_sm(k);
+        const uint32_t col = R ? (uint32_t)gated_index((int)c * 8, R ? R : 1, n) : c * 8u;
+        this->dma[p] = (k * (uint32_t)ld + col) * 2u;   // as mn_dma_offsets
+      }
+      // k-row 8g + j/4 (+ 4 and + 32 K as immediates: the swizzle's bits stay), columns base + 16t + 4(j % 4);
+      // the tile's bits of the chunk are apart from the base's and meet the swizzle's by XOR alone
+      const uint32_t k = 8u * g + (j >> 2), c = ((uint32_t)base + 4u * (j & 3u)) >> 3;
+      at[0] = k * (uint32_t)kRowB + ((c ^ fine_sm(k)) << 4) + ((4u * (j & 3u)) & 7u) * 2u;
+      at[1] = 0;
+    } else {
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {   // as km_dma_offsets
+        const uint32_t r = (uint32_t)(8 * PER * dma_wave + 8 * p + (lane >> 3)), kc = ((uint32_t)lane & 7u) ^ fine_sk(r);
+        this->kbyte[p] = kc * 16u;
+        this->dma[p] = r * (uint32_t)ld * (uint32_t)EL::kBytes + kc * 16u;
+      }
+      const uint32_t r = (uint32_t)base + j;   // the swizzle is the same for all tiles
+#pragma unroll
+      for (int s = 0; s < 2; ++s) at[s] = r * 128u + (((4u * (uint32_t)s + g) ^ fine_sk(r)) << 4);
+    }
+  }
+  // fragments of tiles first .. first + C-1, K step s
+  template <int C>
+  __device__ __forceinline__ void read(const uint8_t* stage, int s, int first, Frag (&f)[C]) const {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int t = first + c;
+      if constexpr (MN) {
+        u32x4 out;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t* p = stage + (at[0] ^ (uint32_t)(t << 5)) + (32 * s + 4 * h) * kRowB;
+          const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+          out[2 * h] = (uint32_t)(uint16_t)v[0] | ((uint32_t)(uint16_t)v[1] << 16);
+          out[2 * h + 1] = (uint32_t)(uint16_t)v[2] | ((uint32_t)(uint16_t)v[3] << 16);
+        }
+        f[c] = out;
+      } else if constexpr (EL::kFp8) {
+        const u32x4 lo = *(const u32x4*)(stage + at[0] + t * 2048), hi = *(const u32x4*)(stage + at[1] + t * 2048);
+        f[c] = u32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      } else {
+        f[c] = *(const u32x4*)(stage + at[s] + t * 2048);
+      }
+    }
+  }
+};
+
+template <bool A_MN, bool B_MN, int DT, bool GATED>
+__global__ __launch_bounds__(512, 2) void gemm_ep_fine(EpArgs g) {
+  constexpr int BS = 256, WGM = GATED ? 4 : 2, WGN = GATED ? 2 : 4, NW = WGM * WGN;
+  __shared__ __attribute__((aligned(1024))) uint8_t sa0[BS * kRowBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t sb0[BS * kRowBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t sa1[BS * kRowBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t sb1[BS * kRowBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t sa2[BS * kRowBytes];
+  using EL = Elem<DT>;
+  using Frag = typename EL::Frag;
+  constexpr int WM = BS / WGM, WN = BS / WGN, TM = WM / 16, TN = WN / 16, PER = BS / 8 / NW;
+  static_assert(DT == TG_F16 || DT == TG_BF16 || DT == TG_I8 || (DT >= kF8 && DT < kMX), "16-bit, int8 or fp8 operands");
+  static_assert(EL::kBytes == 2 || (!A_MN && !B_MN), "8-bit operands are K-contiguous");
+  static_assert(!GATED || !A_MN, "gated: A [M][K]");
+  const EpTile t = ep_tile<BS, GATED>(g);
+  const int tid = (int)threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int wm = (wave / WGN) * WM, wn = (wave % WGN) * WN;
+  using OA = FineOperand<A_MN, PER, DT, BS, 0>;
+  using OB = FineOperand<B_MN, PER, DT, BS, GATED && B_MN ? WN / 2 : 0>;
+  OA oa;
+  OB ob;
+  oa.setup(g.lda, wm, wave, lane, 0);
+  ob.setup(g.ldb, wn, GATED && !B_MN ? 0 : wave, lane, g.N);   // gated: the wave's rows are in its base address
+  f32x4 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{};
+  const DirectLoads<A_MN, B_MN, DT, BS, GATED, OA, OB, WN / 2> load_ab(oa, ob, g, t, wave);
+  const int KT = (t.kl + EL::kBK - 1) / EL::kBK;   // >= 1
+
+  // the operand that goes by phases of PT of its 8 tiles, and the one whose four tiles stay for a K step; fp8
+  // fragments are twice as large
+  constexpr int PT = EL::kFp8 ? 2 : 4, NPH = 8 / PT, NS = OA::kSteps, NP = NS * NPH;
+  static_assert(NP % 2 == 0 && (GATED ? TN : TM) == 8 && (GATED ? TM : TN) == 4, "fragments go by turns");
+  Frag f[2][PT], o[2][4];
+  auto read_f = [&](const uint8_t* a, const uint8_t* b, int s, int h, Frag (&x)[PT]) {
+    if constexpr (GATED) ob.template read<PT>(b, s, h * PT, x);
+    else oa.template read<PT>(a, s, h * PT, x);
+  };
+  auto read_o = [&](const uint8_t* a, const uint8_t* b, int s, Frag (&x)[4]) {
+    if constexpr (GATED) oa.template read<4>(a, s, 0, x);
+    else ob.template read<4>(b, s, 0, x);
+  };
+  constexpr int kF = PT * (GATED ? OB::kTileReads : OA::kTileReads), kO = 4 * (GATED ? OA::kTileReads : OB::kTileReads), kM = PT * 4;
+  using T_ = std::true_type;
+  using F_ = std::false_type;
+  // all but the latest n loads have landed, no LDS read is out, and every wave is here; __syncthreads would wait
+  // for every load
+  auto meet = [&](auto n) {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(wait_vm(decltype(n)::value) & ~(15 << 8));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Stage kt (odd: of two) from (ca, cb).  Its first phase issues A's stage kt+2 into fa, which the stage before
+  // freed, its last one B's into cb.  Stages past K read as zeros and touch no memory.
+  auto stage = [&](uint8_t* ca, uint8_t* cb, const uint8_t* na, const uint8_t* nb, uint8_t* fa, int kt, auto odd) {
+    constexpr int kOdd = decltype(odd)::value ? 1 : 0;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const int h = p % NPH, q = NS == 1 ? kOdd : p / NPH;
+      const bool last = p + 1 == NP;
+      if (last) meet(std::integral_constant<int, PER>{});
+      // fragments of the next phase
+      const int s1 = last ? 0 : (p + 1) / NPH, h1 = last ? 0 : (p + 1) % NPH;
+      read_f(last ? na : ca, last ? nb : cb, s1, h1, f[(p + 1) & 1]);
+      if (h1 == 0) read_o(last ? na : ca, last ? nb : cb, s1, o[1 - q]);
+      if (p == 0) load_ab.load_a(kt + 2, fa);
+      if (last) load_ab.load_b(kt + 2, cb);
+#pragma unroll
+      for (int i = 0; i < PT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (GATED) acc[j][h * PT + i] = mfma16t<DT>(f[p & 1][i], o[q][j], acc[j][h * PT + i]);
+          else acc[h * PT + i][j] = mfma16t<DT>(o[q][j], f[p & 1][i], acc[h * PT + i][j]);
+        }
+      if (p == 0) interleave<kM, kF, PER>();
+      else if (last) interleave<kM, kF + kO, PER>();
+      else if (h1 == 0) interleave<kM, kF + kO, 0>();
+      else interleave<kM, kF, 0>();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  load_ab(0, sa0, sb0);
+  load_ab(1, sa1, sb1);
+  meet(std::integral_constant<int, 2 * PER>{});
+  read_f(sa0, sb0, 0, 0, f[0]);
+  read_o(sa0, sb0, 0, o[0]);
+  // No way out of the middle of a round: the compiler would count the loads of every exit as possibly in flight
+  // at the loop's head, and wait for all of them there.
+  int kt = 0;
+  for (; kt + 6 <= KT; kt += 6) {
+    stage(sa0, sb0, sa1, sb1, sa2, kt, F_{});
+    stage(sa1, sb1, sa2, sb0, sa0, kt + 1, T_{});
+    stage(sa2, sb0, sa0, sb1, sa1, kt + 2, F_{});
+    stage(sa0, sb1, sa1, sb0, sa2, kt + 3, T_{});
+    stage(sa1, sb0, sa2, sb1, sa0, kt + 4, F_{});
+    stage(sa2, sb1, sa0, sb0, sa1, kt + 5, T_{});
+  }
+  if (kt < KT) {
+    stage(sa0, sb0, sa1, sb1, sa2, kt, F_{});
+    if (kt + 1 < KT) {
+      stage(sa1, sb1, sa2, sb0, sa0, kt + 1, T_{});
+      if (kt + 2 < KT) {
+        stage(sa2, sb0, sa0, sb1, sa1, kt + 2, F_{});
+        if (kt + 3 < KT) {
+          stage(sa0, sb1, sa1, sb0, sa2, kt + 3, T_{});
+          if (kt + 4 < KT) stage(sa1, sb0, sa2, sb1, sa0, kt + 4, F_{});
+        }
+      }
+    }
+  }
+  // the zero stages still on their way land in LDS: before the bands take the place, and before the wave ends
+  meet(std::integral_constant<int, 0>{});
+  if constexpr (GATED) gated_store<BS, WN, WM / 32, EL::kI8>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
+  else ep_store<BS, WN, WM / 32, EL::kI8>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
+}
+
+}  // namespace
+}  // namespace tg

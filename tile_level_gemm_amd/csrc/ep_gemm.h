@@ -32,6 +32,7 @@
 
 #include "direct_gemm.h"
 #include "ep.h"
+#include "mfma16.h"
 #include "staged.h"
 
 namespace tg {
@@ -162,13 +163,50 @@ __device__ __forceinline__ EpTile ep_tile(const EpArgs& g) {
 
 // Epilogue, one 32-row band of the wave's tile at a time.  No wave reads or fills a stage buffer any
 // more, so the bands live there: s0 .. s3 are four stage arrays.
-// Accumulator element r of tile (i, j): row 32i + lane%32, column 32j + 8(r/4) + 4(lane/32) + r%4.
-// INT: the accumulators hold integers; parts of a sum stay integers, so that ep_join adds them exactly.
-template <int BS, int WN, int TM, int TN, bool INT>
-__device__ __forceinline__ void ep_store(const EpArgs& g, const EpTile& t, f32x16 (&acc)[TM][TN], int wave,
+// Accumulator element r of a 32-row tile (i, j): row 32i + lane%32, column 32j + 8(r/4) + 4(lane/32) + r%4.
+// Where a band holds 4 columns from `col` on of a row.  Rows are 4 banks apart, or, where only packed bands fit
+// (128 columns), 4 columns change places by the row.
+template <int LDF>
+__device__ __forceinline__ int band_at(int row, int col) {
+  return row * LDF + (LDF % 32 == 0 ? col ^ ((row & 7) << 2) : col);
+}
+constexpr int band_ld(int wn) { return wn == 128 ? wn : wn + 4; }   // floats per band row
+// The first 32 rows of a wave's accumulators into its band, and the others moved up to their place.
+template <int LDF, int TM, int TN>
+__device__ __forceinline__ void put_band(float* band, int lane, f32x16 (&acc)[TM][TN]) {
+#pragma unroll
+  for (int j = 0; j < TN; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *(float4*)(band + band_at<LDF>(lane & 31, 32 * j + 8 * q + 4 * (lane >> 5))) =
+          float4{acc[0][j][4 * q], acc[0][j][4 * q + 1], acc[0][j][4 * q + 2], acc[0][j][4 * q + 3]};
+#pragma unroll
+  for (int k = 0; k + 1 < TM; ++k)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[k][j] = acc[k + 1][j];
+}
+// 16-row tiles: accumulator element r of tile (i, j): row 16i + lane%16, column 16j + 4(lane/16) + r
+template <int LDF, int TM, int TN>
+__device__ __forceinline__ void put_band(float* band, int lane, f32x4 (&acc)[TM][TN]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+      *(float4*)(band + band_at<LDF>(16 * i + (lane & 15), 16 * j + 4 * (lane >> 4))) =
+          float4{acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+#pragma unroll
+  for (int k = 0; k + 2 < TM; ++k)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[k][j] = acc[k + 2][j];
+}
+
+// BANDS: of 32 rows.  INT: the accumulators hold integers; parts of a sum stay integers, so that ep_join adds
+// them exactly.
+template <int BS, int WN, int BANDS, bool INT, class ACC>
+__device__ __forceinline__ void ep_store(const EpArgs& g, const EpTile& t, ACC& acc, int wave,
                                          int lane, int wm, int wn, uint8_t* s0, uint8_t* s1, uint8_t* s2,
                                          uint8_t* s3) {
-  constexpr int LDF = WN + 4;   // floats per band row: 16-byte rows, 4 banks apart
+  constexpr int LDF = band_ld(WN);
   static_assert((BS == 64 ? 1 : 2) * 32 * LDF * 4 <= BS * kRowBytes, "two bands (four waves: one) per stage array");
   float* band = (float*)((wave & 2) ? ((wave & 1) ? s3 : s2) : ((wave & 1) ? s1 : s0)) + (wave >> 2) * 32 * LDF;
   constexpr int LPR = WN / 8, RPP = 64 / LPR;   // lanes per row, rows per pass
@@ -179,8 +217,8 @@ __device__ __forceinline__ void ep_store(const EpArgs& g, const EpTile& t, f32x1
   // The bands run in a loop, the accumulators moving down a row of tiles each time: unrolled, the
   // epilogue was 250 KB of code, and fetching it took 16 us a 256-wide block.
   auto from_band = [&](int p, float (&v)[8]) {
-    const float* src = band + (p * RPP + brow) * LDF + bcol;
-    const float4 lo = *(const float4*)src, hi = *(const float4*)(src + 4);
+    const int row = p * RPP + brow;
+    const float4 lo = *(const float4*)(band + band_at<LDF>(row, bcol)), hi = *(const float4*)(band + band_at<LDF>(row, bcol + 4));
     v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
     v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
   };
@@ -207,23 +245,14 @@ __device__ __forceinline__ void ep_store(const EpArgs& g, const EpTile& t, f32x1
   constexpr bool kAhead = BS == 256;
   if (kAhead) look(0);
 #pragma unroll 1
-  for (int i = 0; i < TM; ++i) {
+  for (int i = 0; i < BANDS; ++i) {
     const int row0 = t.m0 + wm + 32 * i + brow;
     if (!kAhead) look(i);
     EpRow rows[NP];
 #pragma unroll
     for (int p = 0; p < NP; ++p) rows[p] = ahead[p];
-    if (kAhead && i + 1 < TM) look(i + 1);
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *(float4*)(band + (lane & 31) * LDF + 32 * j + 8 * q + 4 * (lane >> 5)) =
-            float4{acc[0][j][4 * q], acc[0][j][4 * q + 1], acc[0][j][4 * q + 2], acc[0][j][4 * q + 3]};
-#pragma unroll
-    for (int k = 0; k + 1 < TM; ++k)
-#pragma unroll
-      for (int j = 0; j < TN; ++j) acc[k][j] = acc[k + 1][j];
+    if (kAhead && i + 1 < BANDS) look(i + 1);
+    put_band<LDF>(band, lane, acc);
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
@@ -260,11 +289,11 @@ __device__ __forceinline__ void ep_store(const EpArgs& g, const EpTile& t, f32x1
 }
 
 // Epilogue of a gated block, as ep_store: the first half of a band's columns are the gate's.
-template <int BS, int WN, int TM, int TN, bool INT>
-__device__ __forceinline__ void gated_store(const EpArgs& g, const EpTile& t, f32x16 (&acc)[TM][TN], int wave,
+template <int BS, int WN, int BANDS, bool INT, class ACC>
+__device__ __forceinline__ void gated_store(const EpArgs& g, const EpTile& t, ACC& acc, int wave,
                                             int lane, int wm, int wn, uint8_t* s0, uint8_t* s1, uint8_t* s2,
                                             uint8_t* s3) {
-  constexpr int LDF = WN + 4, R = WN / 2;
+  constexpr int LDF = band_ld(WN), R = WN / 2;
   static_assert((BS == 64 ? 1 : 2) * 32 * LDF * 4 <= BS * kRowBytes, "two bands (four waves: one) per stage array");
   float* band = (float*)((wave & 2) ? ((wave & 1) ? s3 : s2) : ((wave & 1) ? s1 : s0)) + (wave >> 2) * 32 * LDF;
   constexpr int LPR = R / 8, RPP = 64 / LPR, NP = 32 / RPP;   // lanes per row, rows per pass
@@ -274,8 +303,8 @@ __device__ __forceinline__ void gated_store(const EpArgs& g, const EpTile& t, f3
   GatedCols cols;
   if (g.splits == 1) gated_cols(g, col, cols);
   auto from_band = [&](int p, int at, float (&v)[8]) {
-    const float* src = band + (p * RPP + brow) * LDF + bcol + at;
-    const float4 lo = *(const float4*)src, hi = *(const float4*)(src + 4);
+    const int row = p * RPP + brow, col = bcol + at;
+    const float4 lo = *(const float4*)(band + band_at<LDF>(row, col)), hi = *(const float4*)(band + band_at<LDF>(row, col + 4));
     v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
     v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
   };
@@ -287,18 +316,9 @@ __device__ __forceinline__ void gated_store(const EpArgs& g, const EpTile& t, f3
     }
   };
 #pragma unroll 1
-  for (int i = 0; i < TM; ++i) {
+  for (int i = 0; i < BANDS; ++i) {
     const int row0 = t.m0 + wm + 32 * i + brow;
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *(float4*)(band + (lane & 31) * LDF + 32 * j + 8 * q + 4 * (lane >> 5)) =
-            float4{acc[0][j][4 * q], acc[0][j][4 * q + 1], acc[0][j][4 * q + 2], acc[0][j][4 * q + 3]};
-#pragma unroll
-    for (int k = 0; k + 1 < TM; ++k)
-#pragma unroll
-      for (int j = 0; j < TN; ++j) acc[k][j] = acc[k + 1][j];
+    put_band<LDF>(band, lane, acc);
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
@@ -353,7 +373,8 @@ __device__ __forceinline__ void gated_mn_dma_offsets(int64_t ld, int n, int wave
 }
 
 // fills one stage's LDS images of both operands from memory
-template <bool A_MN, bool B_MN, int DT, int BS, bool GATED, class OA, class OB>
+// GR: gated: columns of a group
+template <bool A_MN, bool B_MN, int DT, int BS, bool GATED, class OA, class OB, int GR = BS / (ep_threads(BS) / 64)>
 struct DirectLoads {
   using EL = Elem<DT>;
   static constexpr int E = EL::kBytes, BK = EL::kBK, PER = BS / 8 / (ep_threads(BS) / 64);
@@ -371,10 +392,11 @@ struct DirectLoads {
     // records: from the panel's first element to the last one of this part of K
     oa.bind(pa, (A_MN ? (int64_t)(kl - 1) * g.lda + ra : (int64_t)(min(ra, BS) - 1) * g.lda + kl) * E);
     if constexpr (GATED && !B_MN) {
-      // the wave's rows: a group of one projection
+      // the wave's rows: of one projection, as a group holds a whole number of waves' rows
       constexpr int R = 8 * PER;
-      const int first = t.n0 + (wave >> 1) * R, left = g.N - first;
-      const int64_t row = (int64_t)(wave & 1) * g.N + min(first, g.N - 1);
+      static_assert(GR % R == 0, "a wave's rows are of one group");
+      const int at = wave * R, first = t.n0 + gated_index(at, GR, 0), left = g.N - first;
+      const int64_t row = (int64_t)(at / GR % 2) * g.N + min(first, g.N - 1);
       ob.bind(g.B + (row * g.ldb + t.k0) * E, left <= 0 ? 0 : ((int64_t)(min(left, R) - 1) * g.ldb + kl) * E);
     } else {
       ob.bind(pb, (B_MN ? (int64_t)(kl - 1) * g.ldb + rb : (int64_t)(min(rb, BS) - 1) * g.ldb + kl) * E);
@@ -383,10 +405,12 @@ struct DirectLoads {
     adv_b = B_MN ? (uint32_t)(BK * g.ldb * E) : (uint32_t)kRowBytes;
   }
   // valid bytes of each K row in stage s (K-major operands; 0 for a stage past the end)
+  __device__ __forceinline__ uint32_t valid(int s) const { return (uint32_t)max(0, min(kRowBytes, kl * E - s * kRowBytes)); }
+  __device__ __forceinline__ void load_a(int s, uint8_t* xa) const { oa.template load<true>((uint32_t)s * adv_a, g.lda, xa, wave, valid(s)); }
+  __device__ __forceinline__ void load_b(int s, uint8_t* xb) const { ob.template load<true>((uint32_t)s * adv_b, g.ldb, xb, wave, valid(s)); }
   __device__ __forceinline__ void operator()(int s, uint8_t* xa, uint8_t* xb) const {
-    const uint32_t lim = (uint32_t)max(0, min(kRowBytes, kl * E - s * kRowBytes));
-    oa.template load<true>((uint32_t)s * adv_a, g.lda, xa, wave, lim);
-    ob.template load<true>((uint32_t)s * adv_b, g.ldb, xb, wave, lim);
+    load_a(s, xa);
+    load_b(s, xb);
   }
 };
 
@@ -515,8 +539,8 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_dir
   }
   stage(sa0, sb0, sa1, sb1, kt, F_{}, T_{});
   stage(sa1, sb1, sa0, sb0, kt + 1, F_{}, F_{});
-  if constexpr (GATED) gated_store<BS, WN, TM, TN, EL::kI8>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
-  else ep_store<BS, WN, TM, TN, EL::kI8>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
+  if constexpr (GATED) gated_store<BS, WN, TM, EL::kI8>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
+  else ep_store<BS, WN, TM, EL::kI8>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
 }
 
 // s_waitcnt: at most n vector memory instructions outstanding (n < 64), no LDS read
@@ -627,8 +651,8 @@ __global__ __launch_bounds__(ep_threads(BS)) void gemm_ep_ring(EpArgs g) {
   }
   // the zero stages still on their way must land before the epilogue takes the buffers
   meet(std::integral_constant<int, 0>{});
-  if constexpr (GATED) gated_store<BS, WN, TM, TN, EL::kI8>(g, t, acc, wave, lane, wm, wn, s0, s1, s2, s3);
-  else ep_store<BS, WN, TM, TN, EL::kI8>(g, t, acc, wave, lane, wm, wn, s0, s1, s2, s3);
+  if constexpr (GATED) gated_store<BS, WN, TM, EL::kI8>(g, t, acc, wave, lane, wm, wn, s0, s1, s2, s3);
+  else ep_store<BS, WN, TM, EL::kI8>(g, t, acc, wave, lane, wm, wn, s0, s1, s2, s3);
 }
 
 // Operands through registers, two stages ahead of the one computed: one register set each for the even
@@ -739,30 +763,8 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_sta
     }
     if (kt < KT) stage(sa0, sb0, sa1, sb1, kt, S0, S1);
   }
-  if constexpr (GATED) gated_store<BS, WN, TM, TN, EL::kI8>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
-  else ep_store<BS, WN, TM, TN, EL::kI8>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
-}
-
-template <bool A_MN, bool B_MN, int DT, bool GATED = false>
-hipError_t launch_ep_one(const EpArgs& g, const EpKernel& k, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)g.tiles_m * g.tiles_n * g.splits)), block(ep_threads(k.bs));
-  if (k.staged) {
-    if (k.bs == 64) hipLaunchKernelGGL((gemm_ep_staged<A_MN, B_MN, DT, 64, GATED>), grid, block, 0, s, g);
-    else hipLaunchKernelGGL((gemm_ep_staged<A_MN, B_MN, DT, 128, GATED>), grid, block, 0, s, g);
-  } else if (k.ring) {
-    if (k.bs == 64) hipLaunchKernelGGL((gemm_ep_ring<A_MN, B_MN, DT, 64, GATED>), grid, block, 0, s, g);
-    else hipLaunchKernelGGL((gemm_ep_ring<A_MN, B_MN, DT, 128, GATED>), grid, block, 0, s, g);
-  } else {
-    if (k.bs == 256) hipLaunchKernelGGL((gemm_ep_direct<A_MN, B_MN, DT, 256, GATED>), grid, block, 0, s, g);
-    else hipLaunchKernelGGL((gemm_ep_direct<A_MN, B_MN, DT, 128, GATED>), grid, block, 0, s, g);
-  }
-  return hipGetLastError();
-}
-
-template <bool A_MN, bool B_MN>
-hipError_t launch_ep_layout(const EpArgs& g, int dtype, const EpKernel& k, hipStream_t s) {
-  return dtype == TG_F16 ? launch_ep_one<A_MN, B_MN, TG_F16>(g, k, s)
-                         : launch_ep_one<A_MN, B_MN, TG_BF16>(g, k, s);
+  if constexpr (GATED) gated_store<BS, WN, TM, EL::kI8>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
+  else ep_store<BS, WN, TM, EL::kI8>(g, t, acc, wave, lane, wm, wn, sa0, sb0, sa1, sb1);
 }
 
 }  // namespace

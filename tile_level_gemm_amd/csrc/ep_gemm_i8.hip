@@ -2,7 +2,7 @@
 //
 // v_mfma_i32_32x32x32_i8: 16 bytes of K a lane as in the 16-bit kernels, so their stages, fragment reads
 // and schedule serve with twice the K.  The sums are exact, and the epilogue turns them to fp32.
-#include "ep_gemm.h"
+#include "ep_launch.h"
 
 namespace tg {
 

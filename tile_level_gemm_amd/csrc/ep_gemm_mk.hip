@@ -1,5 +1,5 @@
 // Block kernels of the product with an epilogue, 16-bit operands, stored A [K,M], B [N,K].
-#include "ep_gemm.h"
+#include "ep_launch.h"
 
 namespace tg {
 

@@ -24,25 +24,10 @@
 // 8192 25.8 us (5.2 TB/s), 16 x 8192 x 4096 e4m3 9.8 us; about 4 us of each are launch and first bytes.
 #include "direct_gemm.h"
 #include "ep.h"
+#include "mfma16.h"
 
 namespace tg {
 namespace {
-
-typedef __attribute__((ext_vector_type(4))) float f32x4;
-
-template <int DT, class F>
-__device__ __forceinline__ f32x4 mfma16t(F b, F a, f32x4 c) {
-  if constexpr (DT == TG_F16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), c, 0, 0, 0);
-  else if constexpr (DT == TG_BF16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), c, 0, 0, 0);
-  else if constexpr (DT == TG_I8)   // integer sums, held as the bits of c's floats
-    return __builtin_bit_cast(f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, b), __builtin_bit_cast(i32x4, a),
-                                                                           __builtin_bit_cast(i32x4, c), 0, 0, 0));
-  else
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(i32x8, b), __builtin_bit_cast(i32x8, a),
-                                                            c, DT & 1, (DT & 3) >> 1, 0, 0, 0, 0);
-}
 
 // 16 bytes of a K-contiguous row, n valid elements of E bytes from p on (n <= 0: none, nothing is read)
 template <int E>

@@ -1,5 +1,5 @@
 // Gated block kernels, 16-bit operands, A [M,K], B [2N,K] or [K,2N].
-#include "ep_gemm.h"
+#include "ep_launch.h"
 
 namespace tg {
 

@@ -1,5 +1,5 @@
 // Gated block kernels, 8-bit operands, A [M,K], B [2N,K].
-#include "ep_gemm.h"
+#include "ep_launch.h"
 
 namespace tg {
 

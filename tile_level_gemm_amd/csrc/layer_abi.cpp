@@ -302,13 +302,14 @@ int hip_status(const char* what, hipError_t e) {
   return fail(TG_E_HIP, std::string(what) + " launch: " + hipGetErrorString(e));
 }
 
-int run_ep(const EpArgs& g, const tg_ep_plan& p, int transA, int transB, int a_dtype, int b_dtype, hipStream_t s) {
+int run_ep(const EpArgs& g, const tg_ep_plan& p, int transA, int transB, int a_dtype, int b_dtype, hipStream_t s,
+           bool fine = false) {
   if (p.kernel == TG_EP_NONE) return TG_OK;
   if (p.kernel != TG_EP_JOIN) {
     const int st = hip_status("tile_gemm_ep", p.kernel == TG_EP_TOKENS
                                                   ? launch_ep_tokens(g, transA, transB, a_dtype, b_dtype, g.waves, s)
                                                   : launch_ep_block(g, transA, transB, a_dtype, b_dtype,
-                                                                    {p.block_m, p.kernel == TG_EP_STAGED, g.ring != 0}, s));
+                                                                    {p.block_m, p.kernel == TG_EP_STAGED, g.ring != 0, fine}, s));
     if (st || g.splits == 1) return st;
   }
   return hip_status("tile_gemm_ep join", launch_ep_join(g, false, s));
@@ -319,7 +320,7 @@ int run_gated(const EpArgs& g, const tg_ep_plan& p, int transB, int a_dtype, int
     const int st = hip_status("tile_gemm_gated", p.kernel == TG_EP_TOKENS
                                                      ? launch_gated_tokens(g, a_dtype, b_dtype, g.waves, s)
                                                      : launch_gated_block(g, transB, a_dtype, b_dtype,
-                                                                          {p.block_m, p.kernel == TG_EP_STAGED, g.ring != 0}, s));
+                                                                          {p.block_m, p.kernel == TG_EP_STAGED, g.ring != 0, true}, s));
     if (st || g.splits == 1) return st;
   }
   return hip_status("tile_gemm_gated join", launch_ep_join(g, true, s));
@@ -759,8 +760,8 @@ int tile_gemm_gated_bwd(const void* dY, const void* Z, const void* A, const void
     if ((st = hip_status(what, launch_gated_grad(a, (int)groups, s)))) return st;
     if (dbias && groups > 1 && (st = hip_status(what, launch_sum_rows((const float*)workspace, groups, W, dbias, s)))) return st;
   }
-  if (dA && (st = run_ep(ga, pa, 0, !transB, dtype, dtype, s))) return st;
-  if (dB && (st = run_ep(gb, pb, 1, 0, dtype, dtype, s))) return st;
+  if (dA && (st = run_ep(ga, pa, 0, !transB, dtype, dtype, s, true))) return st;
+  if (dB && (st = run_ep(gb, pb, 1, 0, dtype, dtype, s, true))) return st;
   return TG_OK;
 }
 

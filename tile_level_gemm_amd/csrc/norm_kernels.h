@@ -151,10 +151,13 @@ __device__ __forceinline__ void row_sums(float& s, float& q, float (*red)[2]) {
 // Whether rstd·max|H·w| is max|Y|: the product with the weight has neither overflowed nor lost bits
 // below the floor of max|Y| (NaN: no).
 __device__ __forceinline__ bool top_fits(float top) { return top >= kAmaxFloor && top < __builtin_inff(); }
-// Row scale of max|Y| >= the floor; NaN for a row with a NaN or an infinity.
+// Row scale of max|Y| >= the floor; NaN for a row with a NaN or an infinity.  For integers the product with
+// 1/127 in fp32, up to two units from the quotient: their codes are rounded to whole numbers by whatever scale
+// is stored, and clamped to 127.
 __device__ __forceinline__ float row_scale(float amax, int t) {
   amax = nan_max(amax, kAmaxFloor);
-  return amax < __builtin_inff() ? amax / q_max(t) : __builtin_nanf("");
+  const float s = t == TG_I8 ? amax * (1.0f / 127.0f) : amax / q_max(t);
+  return amax < __builtin_inff() ? s : __builtin_nanf("");
 }
 // y/s rounded to nearest for inv = 1/s rounded to nearest: Markstein's correction (IBM J. Res. Dev. 34,
 // 1990) of the product.  The codes are then the quotient by the very scale that is stored; the product
