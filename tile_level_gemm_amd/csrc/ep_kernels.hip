@@ -126,7 +126,9 @@ __global__ __launch_bounds__(8 * RL) void act_grad(ActGradArgs a) {
 }
 
 // The same for D = act(G)·U: dY, G and U are read and dG = dY·U·act'(G), dU = dY·act(G) written by one
-// thread, with the column sums of both.
+// thread, with the column sums of both.  Bound by memory, 4096 x 4096 (168 MB) 36 us with one row a thread in
+// flight (two 38, four 43: registers, 107 of them with one, cost more waves than rows in flight give); small
+// problems by latency, 200 x 264 6.6 us with 1024 threads (512 with two rows 8.1).
 template <int RL, int K, bool SCALED>
 __global__ __launch_bounds__(8 * RL) void gated_grad(ActGradArgs a) {
   __shared__ float red[RL][128 + 1];
@@ -260,11 +262,11 @@ hipError_t launch_gated_grad(const ActGradArgs& a, int groups, hipStream_t s) {
   const dim3 cols = wide_grid(((int64_t)a.N + 63) / 64), grid(cols.x, (unsigned)groups, cols.y);
   const bool scaled = a.rs || a.cs;
   if (groups == 1) {
-    if (scaled) hipLaunchKernelGGL((gated_grad<64, 2, true>), grid, dim3(512), 0, s, a);
-    else hipLaunchKernelGGL((gated_grad<64, 2, false>), grid, dim3(512), 0, s, a);
+    if (scaled) hipLaunchKernelGGL((gated_grad<128, 1, true>), grid, dim3(1024), 0, s, a);
+    else hipLaunchKernelGGL((gated_grad<128, 1, false>), grid, dim3(1024), 0, s, a);
   } else {
-    if (scaled) hipLaunchKernelGGL((gated_grad<32, 4, true>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((gated_grad<32, 4, false>), grid, dim3(256), 0, s, a);
+    if (scaled) hipLaunchKernelGGL((gated_grad<32, 1, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((gated_grad<32, 1, false>), grid, dim3(256), 0, s, a);
   }
   return hipGetLastError();
 }

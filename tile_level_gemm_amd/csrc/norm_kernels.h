@@ -180,7 +180,7 @@ __global__ __launch_bounds__(MAXT) void norm_rows(NormArgs a) {
   const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
   if (WAVE && row >= a.rows) return;
   const int cols = (int)a.cols;
-  float h[NV][8], w[NV][8], b[NV][8];
+  float h[NV][8], w[NV][8];
 #pragma unroll
   for (int j = 0; j < NV; ++j) ep_get8(a.X, DT, row * a.ldx + min((j * TPR + t) * 8, cols - 8), 8, h[j]);
   if (KIND != kRows && a.R) {
@@ -197,27 +197,22 @@ __global__ __launch_bounds__(MAXT) void norm_rows(NormArgs a) {
         else h[j][e] = x;
       }
   }
-  if constexpr (KIND != kRows) {
+  if constexpr (KIND == kRms) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int col = min((j * TPR + t) * 8, cols - 8);
       if (a.w_t == TG_F32) ep_get8(a.W, TG_F32, col, 8, w[j]);
       else ep_get8(a.W, DT, col, 8, w[j]);
-      if constexpr (KIND == kLayer) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) b[j][e] = 0.0f;
-        if (a.B && a.w_t == TG_F32) ep_get8(a.B, TG_F32, col, 8, b[j]);
-        else if (a.B) ep_get8(a.B, DT, col, 8, b[j]);
-      }
     }
   }
+  constexpr bool EARLY = KIND == kLayer && NV == 1 && DT != TG_F32;
+  ep_u32x4 rw = {0, 0, 0, 0}, rb = {0, 0, 0, 0};
+  if (EARLY && a.w_t != TG_F32) {
+    const int64_t col = min(t * 8, cols - 8);
+    rw = load16(a.W + 2 * col);
+    if (a.B) rb = load16(a.B + 2 * col);
+  }
   float ss = 0.0f, top = 0.0f, mean = 0.0f, rstd = 1.0f, none = 0.0f;
-  // Y of a chunk's element
-  auto value = [&](int j, int e) {
-    if constexpr (KIND == kRms) return h[j][e] * rstd * w[j][e];
-    else if constexpr (KIND == kLayer) return fmaf((h[j][e] - mean) * rstd, w[j][e], b[j][e]);
-    else return h[j][e];
-  };
   if constexpr (KIND == kLayer) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -243,6 +238,30 @@ __global__ __launch_bounds__(MAXT) void norm_rows(NormArgs a) {
   if constexpr (KIND != kRows || SC == TG_SCALE_ROW)
     row_reduce<WAVE>(ss, top, SC == TG_SCALE_ROW && KIND != kLayer, red[0]);
   if constexpr (KIND != kRows) rstd = 1.0f / sqrtf(ss / (float)cols + a.eps);
+  // The layer norm stores H now (every wave has its loads behind it) and puts Y in its place.  Weight and bias
+  // of two chunks come from the caches: held from the start they left a SIMD 5 waves instead of 8, two
+  // workgroups a CU instead of four (16384 x 8192 bf16 with residual to bf16 208 us, now 190, to e4m3 rows
+  // 241, now 187).  One chunk's wait in registers as they are in memory.
+  if constexpr (KIND == kLayer) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int at = (j * TPR + t) * 8, col = min(at, cols - 8);
+      if (a.H && at < cols) ep_put8(a.H, DT, row * a.ldh + col, 8, h[j]);
+      float lb[8] = {};
+      if (a.w_t == TG_F32) {
+        ep_get8(a.W, TG_F32, col, 8, w[j]);
+        if (a.B) ep_get8(a.B, TG_F32, col, 8, lb);
+      } else if constexpr (EARLY) {
+        ep_unpack8(DT, rw, w[j]);
+        ep_unpack8(DT, rb, lb);
+      } else {
+        ep_get8(a.W, DT, col, 8, w[j]);
+        if (a.B) ep_get8(a.B, DT, col, 8, lb);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[j][e] = fmaf((h[j][e] - mean) * rstd, w[j][e], lb[e]);
+    }
+  }
   float scale = 1.0f, inv = 1.0f;   // S and 1/S
   if constexpr (SC == TG_SCALE_ROW) {
     float amax = KIND == kRms ? top * rstd : top;
@@ -251,7 +270,7 @@ __global__ __launch_bounds__(MAXT) void norm_rows(NormArgs a) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = nan_max(amax, fabsf(value(j, e)));
+        for (int e = 0; e < 8; ++e) amax = nan_max(amax, fabsf(KIND == kRms ? h[j][e] * rstd * w[j][e] : h[j][e]));
       if constexpr (!WAVE && KIND == kRms) __syncthreads();   // every wave has read the first reduction
       row_reduce<WAVE>(none, amax, true, red[KIND == kLayer ? 2 : 0]);
     }
@@ -265,7 +284,7 @@ __global__ __launch_bounds__(MAXT) void norm_rows(NormArgs a) {
     const int at = (j * TPR + t) * 8, col = min(at, cols - 8);
     float y[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = value(j, e);
+    for (int e = 0; e < 8; ++e) y[e] = KIND == kRms ? h[j][e] * rstd * w[j][e] : h[j][e];
     if constexpr (SC == TG_SCALE_BLOCK) {   // cols % 32 == 0: a block is 4 adjacent lanes' chunks
       float m = 0.0f;
 #pragma unroll
@@ -279,7 +298,7 @@ __global__ __launch_bounds__(MAXT) void norm_rows(NormArgs a) {
       if (at < cols && (t & 3) == 0) a.S[row * (a.cols / 32) + at / 32] = fine ? (uint8_t)(x + 127) : 255;
     }
     if (at >= cols) continue;
-    if (KIND != kRows && a.H) ep_put8(a.H, DT, row * a.ldh + col, 8, h[j]);
+    if (KIND == kRms && a.H) ep_put8(a.H, DT, row * a.ldh + col, 8, h[j]);
     if constexpr (SC == TG_SCALE_NONE) {
       ep_put8(a.Y, DT, row * a.ldy + col, 8, y);
     } else {
