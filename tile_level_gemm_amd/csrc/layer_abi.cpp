@@ -337,8 +337,10 @@ int64_t bias_groups(int64_t M, int64_t N) {
 // Workgroups of the norm's backward pass, each with a row (four short rows) at least.  More of them
 // keep more rows in flight but write and add more shares of dW: 16384 x 4096 bf16 103 us with 512
 // (256: 118, 1024: 107), 8192 x 8192 104 us with 256 (512: 109).
-int64_t norm_groups(int64_t rows, int64_t cols) {
-  const int64_t per = cols <= 1024 && norm_in_registers(cols) ? 4 : 1, most = cols <= 4096 ? 512 : 256;
+// The layer norm's shares are twice as long: 512 only from 2048 rows on (1003 x 2057 f16 256: 15.0, 512: 15.8).
+int64_t norm_groups(NormKind kind, int64_t rows, int64_t cols) {
+  const int64_t per = cols <= 1024 && norm_in_registers(cols) ? 4 : 1;
+  const int64_t most = cols <= 4096 && (kind == kRms || rows >= 2048) ? 512 : 256;
   return std::max<int64_t>(1, std::min<int64_t>((rows + per - 1) / per, most));
 }
 
@@ -422,7 +424,7 @@ int64_t norm_dots(NormKind kind, int64_t rows, int64_t cols) {
 
 int64_t norm_bwd_workspace(NormKind kind, int64_t rows, int64_t cols, int dtype) {
   if (rows < 0 || rows > kMaxDim || cols < 1 || cols > kMaxDim || !is_float(dtype)) return 0;
-  const int64_t g = norm_groups(rows, cols);
+  const int64_t g = norm_groups(kind, rows, cols);
   return (norm_dots(kind, rows, cols) + 15) / 16 * 16 + (g > 1 ? g * cols * (kind == kLayer ? 8 : 4) : 0);
 }
 
@@ -481,7 +483,7 @@ int run_norm_bwd(NormKind kind, const void* dY, const void* H, const void* W, co
   a.ldx = ld_dx;
   a.w_t = w_dtype;
   a.dot = dots ? (float*)workspace : nullptr;
-  int64_t groups = norm_groups(rows, cols);
+  int64_t groups = norm_groups(kind, rows, cols);
   float* part = (float*)((uint8_t*)workspace + dots);
   a.share_ld = cols * ((dW != nullptr) + (dB != nullptr));   // a workgroup's shares, dW's first
   if (a.share_ld) groups = std::max<int64_t>(1, std::min(groups, (workspace_bytes - dots) / (4 * a.share_ld)));
