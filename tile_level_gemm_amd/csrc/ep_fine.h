@@ -6,13 +6,14 @@
 // operands runs at 2000 TFLOP/s in bf16 and 4050 in int8, 32-row ones at 1450 and 2850 (on zeros both reach
 // 2450 and 4900).
 //
-// A lane carries 16 bytes of K of row l%16 (fp8: 32), K-group l/16, so an instruction takes 64 bytes of K
-// (fp8: 128), and a wave's 128 x 64 results are 8 x 4 tiles.  The wave's products of a K step run in phases of
-// PT row tiles against all four column tiles; while one phase runs, the row fragments of the next are read
-// into the other half of the registers (and with the last phase of a step the next step's column fragments),
-// so every read has a phase's 16 products, twice that with the SIMD's other wave, to arrive.  Gated blocks
-// have waves of 64 rows by 128 columns, 64 of each projection, so that a wave holds whole 128-byte lines of
-// its results; there the column fragments go by phases.
+// A lane carries 16 bytes of K of row l%16, K-group l/16, so an instruction takes 64 bytes of K, and a wave's
+// 128 x 64 results are 8 x 4 tiles.  The wave's products of a K step run in two phases of four row tiles
+// against all four column tiles; while one phase runs, the row fragments of the next are read into the other
+// half of the registers (and with the last phase of a step the next step's column fragments), so every read
+// has a phase's 16 products, twice that with the SIMD's other wave, to arrive.  Gated blocks have waves of 64
+// rows by 128 columns, 64 of each projection, so that a wave holds whole 128-byte lines of its results; there
+// the column fragments go by phases.  16-bit operands and integers: fp8 fragments are twice as large and do
+// not leave registers enough (gated 8192 x 2x8192 x 4096 e4m3 657 us, gemm_ep_direct 422).
 //
 // LDS holds three stages of A and two of B, all of its 160 KB.  The barrier of a stage comes before its last
 // phase, all of whose fragments are in registers: that phase covers the first reads of the next stage and the
@@ -42,9 +43,9 @@ namespace {
 // 32-row fragments need makes two lanes meet here (8 cycles a read; 8192 x 16384 x 4096 on zeros 634 us, without
 // 616).
 __device__ __forceinline__ uint32_t fine_sk(uint32_t r) { return r & 7u; }
-// M/N-major stages:  A transposing read's four 16-lane groups take two chunks
-// of four consecutive k-rows each, the groups' k-rows 8 apart: 2(k & 3) sends a group's rows to distinct chunk
-// pairs of 128 bytes, and 8 for every second group to the other 128 of 256 bytes.
+// M/N-major stages: a transposing read's four 16-lane groups take two chunks of four consecutive k-rows each, the
+// groups' k-rows 8 apart: 2(k & 3) sends a group's rows to distinct chunk pairs of 128 bytes, and 8 for every
+// second group to the other 128 of 256 bytes.
 __device__ __forceinline__ uint32_t fine_sm(uint32_t k) { return ((k & 3u) << 1) ^ (k & 8u); }
 
 // Operand of one wave: fragments of 16 rows or columns; loads and LDS stages as Operand's, M/N-major stages
@@ -53,15 +54,14 @@ template <bool MN, int PER, int DT, int BS, int R>
 struct FineOperand : Operand<MN, 1, PER, DT, BS> {
   using EL = Elem<DT>;
   using Frag = typename EL::Frag;
-  static constexpr int kSteps = EL::kFp8 ? 1 : 2;   // K steps of a stage
   static constexpr int kRowB = BS * EL::kBytes;
-  static constexpr int kTileReads = MN || EL::kFp8 ? 2 : 1;
+  static constexpr int kTileReads = MN ? 2 : 1;   // LDS reads of a fragment
   uint32_t at[2];   // K-major: byte offset of each 64 bytes of the row's stage; M/N-major: of tile 0
 
   __device__ __forceinline__ void setup(int64_t ld, int base, int dma_wave, int lane, int n) {
     const uint32_t g = (uint32_t)lane >> 4, j = (uint32_t)lane & 15u;
     if constexpr (MN) {
-      static_assert(!EL::kFp8 && EL::kBytes == 2 && BS == 256, "16-bit M/N-major operands of 256-wide blocks");
+      static_assert(EL::kBytes == 2 && BS == 256, "16-bit M/N-major operands of 256-wide blocks");
 #pragma unroll
       for (int p = 0; p < 2; ++p) {   // two k-rows of 32 chunks an instruction
         const uint32_t k = 2u * (uint32_t)(PER * dma_wave + p) + (uint32_t)lane / 32u;
@@ -102,9 +102,6 @@ struct FineOperand : Operand<MN, 1, PER, DT, BS> {
           out[2 * h + 1] = (uint32_t)(uint16_t)v[2] | ((uint32_t)(uint16_t)v[3] << 16);
         }
         f[c] = out;
-      } else if constexpr (EL::kFp8) {
-        const u32x4 lo = *(const u32x4*)(stage + at[0] + t * 2048), hi = *(const u32x4*)(stage + at[1] + t * 2048);
-        f[c] = u32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
       } else {
         f[c] = *(const u32x4*)(stage + at[s] + t * 2048);
       }
@@ -123,7 +120,7 @@ __global__ __launch_bounds__(512, 2) void gemm_ep_fine(EpArgs g) {
   using EL = Elem<DT>;
   using Frag = typename EL::Frag;
   constexpr int WM = BS / WGM, WN = BS / WGN, TM = WM / 16, TN = WN / 16, PER = BS / 8 / NW;
-  static_assert(DT == TG_F16 || DT == TG_BF16 || DT == TG_I8 || (DT >= kF8 && DT < kMX), "16-bit, int8 or fp8 operands");
+  static_assert(DT == TG_F16 || DT == TG_BF16 || DT == TG_I8, "16-bit or int8 operands");
   static_assert(EL::kBytes == 2 || (!A_MN && !B_MN), "8-bit operands are K-contiguous");
   static_assert(!GATED || !A_MN, "gated: A [M][K]");
   const EpTile t = ep_tile<BS, GATED>(g);
@@ -144,9 +141,8 @@ __global__ __launch_bounds__(512, 2) void gemm_ep_fine(EpArgs g) {
   const DirectLoads<A_MN, B_MN, DT, BS, GATED, OA, OB, WN / 2> load_ab(oa, ob, g, t, wave);
   const int KT = (t.kl + EL::kBK - 1) / EL::kBK;   // >= 1
 
-  // the operand that goes by phases of PT of its 8 tiles, and the one whose four tiles stay for a K step; fp8
-  // fragments are twice as large
-  constexpr int PT = EL::kFp8 ? 2 : 4, NPH = 8 / PT, NS = OA::kSteps, NP = NS * NPH;
+  // the operand that goes by phases of PT of its 8 tiles, and the one whose four tiles stay for a K step
+  constexpr int PT = 4, NPH = 8 / PT, NS = 2, NP = NS * NPH;
   static_assert(NP % 2 == 0 && (GATED ? TN : TM) == 8 && (GATED ? TM : TN) == 4, "fragments go by turns");
   Frag f[2][PT], o[2][4];
   auto read_f = [&](const uint8_t* a, const uint8_t* b, int s, int h, Frag (&x)[PT]) {
@@ -158,8 +154,6 @@ __global__ __launch_bounds__(512, 2) void gemm_ep_fine(EpArgs g) {
     else ob.template read<4>(b, s, 0, x);
   };
   constexpr int kF = PT * (GATED ? OB::kTileReads : OA::kTileReads), kO = 4 * (GATED ? OA::kTileReads : OB::kTileReads), kM = PT * 4;
-  using T_ = std::true_type;
-  using F_ = std::false_type;
   // all but the latest n loads have landed, no LDS read is out, and every wave is here; __syncthreads would wait
   // for every load
   auto meet = [&](auto n) {
@@ -170,13 +164,12 @@ __global__ __launch_bounds__(512, 2) void gemm_ep_fine(EpArgs g) {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
   };
-  // Stage kt (odd: of two) from (ca, cb).  Its first phase issues A's stage kt+2 into fa, which the stage before
+  // Stage kt from (ca, cb).  Its first phase issues A's stage kt+2 into fa, which the stage before
   // freed, its last one B's into cb.  Stages past K read as zeros and touch no memory.
-  auto stage = [&](uint8_t* ca, uint8_t* cb, const uint8_t* na, const uint8_t* nb, uint8_t* fa, int kt, auto odd) {
-    constexpr int kOdd = decltype(odd)::value ? 1 : 0;
+  auto stage = [&](uint8_t* ca, uint8_t* cb, const uint8_t* na, const uint8_t* nb, uint8_t* fa, int kt) {
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-      const int h = p % NPH, q = NS == 1 ? kOdd : p / NPH;
+      const int h = p % NPH, q = p / NPH;
       const bool last = p + 1 == NP;
       if (last) meet(std::integral_constant<int, PER>{});
       // fragments of the next phase
@@ -208,22 +201,22 @@ __global__ __launch_bounds__(512, 2) void gemm_ep_fine(EpArgs g) {
   // at the loop's head, and wait for all of them there.
   int kt = 0;
   for (; kt + 6 <= KT; kt += 6) {
-    stage(sa0, sb0, sa1, sb1, sa2, kt, F_{});
-    stage(sa1, sb1, sa2, sb0, sa0, kt + 1, T_{});
-    stage(sa2, sb0, sa0, sb1, sa1, kt + 2, F_{});
-    stage(sa0, sb1, sa1, sb0, sa2, kt + 3, T_{});
-    stage(sa1, sb0, sa2, sb1, sa0, kt + 4, F_{});
-    stage(sa2, sb1, sa0, sb0, sa1, kt + 5, T_{});
+    stage(sa0, sb0, sa1, sb1, sa2, kt);
+    stage(sa1, sb1, sa2, sb0, sa0, kt + 1);
+    stage(sa2, sb0, sa0, sb1, sa1, kt + 2);
+    stage(sa0, sb1, sa1, sb0, sa2, kt + 3);
+    stage(sa1, sb0, sa2, sb1, sa0, kt + 4);
+    stage(sa2, sb1, sa0, sb0, sa1, kt + 5);
   }
   if (kt < KT) {
-    stage(sa0, sb0, sa1, sb1, sa2, kt, F_{});
+    stage(sa0, sb0, sa1, sb1, sa2, kt);
     if (kt + 1 < KT) {
-      stage(sa1, sb1, sa2, sb0, sa0, kt + 1, T_{});
+      stage(sa1, sb1, sa2, sb0, sa0, kt + 1);
       if (kt + 2 < KT) {
-        stage(sa2, sb0, sa0, sb1, sa1, kt + 2, F_{});
+        stage(sa2, sb0, sa0, sb1, sa1, kt + 2);
         if (kt + 3 < KT) {
-          stage(sa0, sb1, sa1, sb0, sa2, kt + 3, T_{});
-          if (kt + 4 < KT) stage(sa1, sb0, sa2, sb1, sa0, kt + 4, F_{});
+          stage(sa0, sb1, sa1, sb0, sa2, kt + 3);
+          if (kt + 4 < KT) stage(sa1, sb0, sa2, sb1, sa0, kt + 4);
         }
       }
     }
