@@ -529,9 +529,9 @@ def tile_gemm_atom_select(M, N, K, dtype, transA, transB):
 # ------------------------------------------------- transformer-layer operators ----
 #
 # The tile_* functions take the C ABI's arguments (leading dimensions given, so operands may be
-# slices of wider tensors); gemm_ep, gemm_ep_backward, rms_norm and rms_norm_backward take
-# tensors, allocate the results and the workspace on the call's stream and are what a model calls:
-# their checks and allocations are native (csrc/tensor_calls.cpp).  Their results carry no autograd
+# slices of wider tensors); gemm_ep, gemm_gated, rms_norm, layer_norm, their _backward calls and
+# quantize_rows take tensors, allocate the results and the workspace on the call's stream and are what
+# a model calls: their checks and allocations are native (csrc/tensor_calls.cpp).  Their results carry no autograd
 # history: the backward calls give the gradients.  An input that requires one gets a warning while
 # gradients are recorded, and tensors they write (out, h_out) count as changed.
 # stream (a stream or its handle; the current one by default): the results and the workspace belong to it.
@@ -922,11 +922,8 @@ class Norm:
 _SCALES = {None: TG_SCALE_NONE, "row": TG_SCALE_ROW, "block": TG_SCALE_BLOCK}
 
 
-def _scale_kind(scales):
-    kind = _SCALES.get(scales)
-    if kind is None:
-        raise TileError(TG_E_ARG, f"scales must be None, 'row' or 'block', got {scales!r}")
-    return kind
+def _no_scales(scales):
+    raise TileError(TG_E_ARG, f"scales must be None, 'row' or 'block', got {scales!r}")
 
 
 def rms_norm(X, weight, eps=1e-5, residual=None, out_dtype=None, scales=None, h_out=None, stream=None):
@@ -938,7 +935,10 @@ def rms_norm(X, weight, eps=1e-5, residual=None, out_dtype=None, scales=None, h_
     if stream is not None:
         with _On(stream):
             return rms_norm(X, weight, eps, residual, out_dtype, scales, h_out)
-    return Norm(*(_calls or _native()).rms_norm(X, weight, eps, residual, out_dtype, _scale_kind(scales), h_out))
+    kind = _SCALES.get(scales)
+    if kind is None:
+        _no_scales(scales)
+    return Norm(*(_calls or _native()).rms_norm(X, weight, eps, residual, out_dtype, kind, h_out))
 
 
 def rms_norm_backward(dY, h, weight, rstd, dH=None, need_dw=True, stream=None):
@@ -955,8 +955,7 @@ class LayerNorm(Norm):
     __slots__ = ("mean",)
 
     def __init__(self, y, scale, mean, rstd, h):
-        super().__init__(y, scale, rstd, h)
-        self.mean = mean
+        self.y, self.scale, self.mean, self.rstd, self.h = y, scale, mean, rstd, h
 
 
 def layer_norm(X, weight, bias=None, eps=1e-5, residual=None, out_dtype=None, scales=None, h_out=None, stream=None):
@@ -966,7 +965,10 @@ def layer_norm(X, weight, bias=None, eps=1e-5, residual=None, out_dtype=None, sc
     if stream is not None:
         with _On(stream):
             return layer_norm(X, weight, bias, eps, residual, out_dtype, scales, h_out)
-    return LayerNorm(*(_calls or _native()).layer_norm(X, weight, bias, eps, residual, out_dtype, _scale_kind(scales), h_out))
+    kind = _SCALES.get(scales)
+    if kind is None:
+        _no_scales(scales)
+    return LayerNorm(*(_calls or _native()).layer_norm(X, weight, bias, eps, residual, out_dtype, kind, h_out))
 
 
 def layer_norm_backward(dY, h, weight, mean, rstd, dH=None, need_dw=True, need_dbias=True, stream=None):
@@ -988,6 +990,7 @@ def quantize_rows(X, out_dtype=torch.int8, scales="row", stream=None):
     if stream is not None:
         with _On(stream):
             return quantize_rows(X, out_dtype, scales)
-    if scales is None:
-        raise TileError(TG_E_ARG, "scales must be 'row' or 'block', got None")
-    return (_calls or _native()).quantize_rows(X, out_dtype, _scale_kind(scales))
+    kind = _SCALES.get(scales)
+    if not kind:
+        raise TileError(TG_E_ARG, f"scales must be 'row' or 'block', got {scales!r}")
+    return (_calls or _native()).quantize_rows(X, out_dtype, kind)
