@@ -3,8 +3,8 @@
 // that its place in the block stands for, or zero for K past the end; the direct loads' chunks that the buffer
 // check lets through lie inside the operand and hold the same.
 //
-// argv: kind (0 [2N][K], 1 [K][2N]), bytes of an element, block size, N, K, leading dimension beyond the packed
-// one, K of a part.
+// argv: kind (0 [2N][K], 1 [K][2N]), bytes of an element, block size, columns of a group, N, K, leading dimension
+// beyond the packed one, K of a part.
 #include <cstdio>
 #include <cstdlib>
 
@@ -18,8 +18,8 @@ static int bad(const char* what, long a, long b, long c, long d) {
 }
 
 template <bool MN>
-static int walk(int eb, int bs, int N, int K, int gap, int kps) {
-  const int ve = 16 / eb, bk = 128 / eb, r = bs == 256 ? 32 : 16, waves = bs == 64 ? 4 : 8, per = bs / 8 / waves;
+static int walk(int eb, int bs, int r, int N, int K, int gap, int kps) {
+  const int ve = 16 / eb, bk = 128 / eb, waves = bs == 64 ? 4 : 8, per = bs / 8 / waves;
   const int cols = MN ? 2 * N : K, rows = MN ? K : 2 * N;
   const int64_t ld = cols + gap;
   const bool direct = (ld * eb) % 16 == 0 && (MN ? (int64_t)N * eb : (int64_t)K * eb) % 16 == 0;
@@ -64,12 +64,12 @@ static int walk(int eb, int bs, int N, int K, int gap, int kps) {
               records = ((int64_t)(kl - 1) * ld + left) * eb;
             } else {
               const int wave = (int)(row / (8 * per));   // whose instruction loads this row
-              const int first = n0 + (wave >> 1) * r, have = N - first;
-              if (8 * per != r) return bad("rows of a wave", n0, k0, s, line);
-              start = ((int64_t)(wave & 1) * N + staged_min(first, N - 1)) * ld + k0;
+              const int own = 8 * per, place = wave * own, first = n0 + gated_index(place, r, 0), have = N - first;
+              if (r % own) return bad("rows of a wave", n0, k0, s, line);
+              start = ((int64_t)(place / r % 2) * N + staged_min(first, N - 1)) * ld + k0;
               const bool past = chunk * 16 >= staged_max(0, staged_min(128, kl * eb - s * 128));
-              off = past ? (int64_t)1 << 31 : (row % (8 * per)) * ld * eb + (int64_t)s * 128 + chunk * 16;
-              records = have <= 0 ? 0 : ((int64_t)(staged_min(have, r) - 1) * ld + kl) * eb;
+              off = past ? (int64_t)1 << 31 : (row % own) * ld * eb + (int64_t)s * 128 + chunk * 16;
+              records = have <= 0 ? 0 : ((int64_t)(staged_min(have, own) - 1) * ld + kl) * eb;
             }
             for (int e = 0; e < ve; ++e) {
               const int k = MN ? s * bk + line : s * bk + chunk * ve + e, i = MN ? chunk * ve + e : line;
@@ -87,12 +87,12 @@ static int walk(int eb, int bs, int N, int K, int gap, int kps) {
 }
 
 int main(int argc, char** argv) {
-  int v[7], n = 0;
-  if (argc < 8 || (argc - 1) % 7) return 2;
-  for (int a = 1; a < argc; a += 7) {
-    for (int i = 0; i < 7; ++i) v[i] = std::atoi(argv[a + i]);
-    if (v[0] ? walk<true>(v[1], v[2], v[3], v[4], v[5], v[6]) : walk<false>(v[1], v[2], v[3], v[4], v[5], v[6])) {
-      std::printf("kind %d bytes %d block %d N %d K %d gap %d part %d\n", v[0], v[1], v[2], v[3], v[4], v[5], v[6]);
+  int v[8], n = 0;
+  if (argc < 9 || (argc - 1) % 8) return 2;
+  for (int a = 1; a < argc; a += 8) {
+    for (int i = 0; i < 8; ++i) v[i] = std::atoi(argv[a + i]);
+    if (v[0] ? walk<true>(v[1], v[2], v[3], v[4], v[5], v[6], v[7]) : walk<false>(v[1], v[2], v[3], v[4], v[5], v[6], v[7])) {
+      std::printf("kind %d bytes %d block %d group %d N %d K %d gap %d part %d\n", v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
       return 1;
     }
     ++n;

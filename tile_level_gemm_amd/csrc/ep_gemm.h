@@ -20,7 +20,8 @@
 //  * gated: a block is BS x BS/2 results of both projections.  Half of each wave's columns are the
 //    gate's and half the up projection's of the same results, so both meet in the wave's band, and the
 //    K loop is the plain one: only B's loads go by another map (gated_index), which is a base address a
-//    wave for [2N][K] weights, since a wave loads half a wave's columns, and an offset a lane for [K][2N].
+//    wave for [2N][K] weights, since the rows that a wave loads are of one projection, and an offset a lane for
+//    [K][2N].
 //
 // Bounds, measured on MI355X.  256-wide, 8192^3 bf16: 785 us (1400 TFLOP/s), of which the K loop takes
 // 725; with bias, gelu_tanh and Z 806 us; 8192 x 8192 x 4096 e4m3 with everything 217 us (2530 TFLOP/s),
