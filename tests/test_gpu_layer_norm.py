@@ -181,6 +181,21 @@ def test_quantised_rows_at_ties_and_extremes():
     assert not q.any() and (s > 0).all()
 
 
+@pytest.mark.parametrize("cols", [7, 64, 2048, 20000])
+@pytest.mark.parametrize("out", [torch.float8_e4m3fn, torch.float8_e5m2])
+def test_signs_of_zeros(cols, out):
+    """An RMS norm's zeros have code 0 whatever their sign; quantize_rows' keep it."""
+    X = torch.zeros(3, cols, device=dev())
+    X[:, 0] = 1.0
+    X[:, 1::2] = -0.0
+    w = torch.ones(cols, device=dev())
+    w[2::4] = -1.0   # zeros of either sign from a zero and its weight
+    y = tg.rms_norm(X, w, scales="row", out_dtype=out).y.view(torch.uint8)
+    assert not y[:, 1:].any() and y[:, 0].all()
+    q, _ = tg.quantize_rows(X, out)
+    assert torch.equal(q.view(torch.uint8)[:, 1:] == 0x80, torch.signbit(X[:, 1:]))
+
+
 @pytest.mark.parametrize("rows,cols", [(1, 96), (9, 2057), (300, 1000), (5, 20001)])
 def test_quantised_slices(rows, cols):
     say(f"quantise slices {rows}x{cols}")

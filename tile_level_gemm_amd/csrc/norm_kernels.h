@@ -190,11 +190,13 @@ __device__ __forceinline__ float row_scale(float amax, int t) {
 // y/s rounded to nearest for inv = 1/s rounded to nearest: Markstein's correction (IBM J. Res. Dev. 34,
 // 1990) of the product.  The codes are then the quotient by the very scale that is stored; the product
 // alone lands on the other side of a border once in some million codes.  Two operations an element
-// (16384 x 8192 bf16 166 us; 164.7 without), where the quotient itself takes ten (172).  Signed as it is,
-// the correction of an exact quotient is -0, which leaves a zero its sign.
+// (16384 x 8192 bf16 166 us; 164.7 without), where the quotient itself takes ten (172).  The correction
+// of an exact quotient is -0 and leaves a zero its sign; the RMS norm's is +0, as its fp8 codes always were: both of
+// its zeros have code 0.
+template <int KIND>
 __device__ __forceinline__ float quotient(float y, float s, float inv) {
   const float q = y * inv;
-  return fmaf(-fmaf(q, s, -y), inv, q);
+  return fmaf(KIND == kRms ? fmaf(-q, s, y) : -fmaf(q, s, -y), inv, q);
 }
 
 // SC: tg_scale_kind of the result
@@ -333,7 +335,7 @@ __global__ __launch_bounds__(MAXT) void norm_rows(NormArgs a) {
       ep_put8(a.Y, DT, row * a.ldy + col, 8, y);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = SC == TG_SCALE_ROW ? quotient(y[e], scale, inv) : y[e] * inv;
+      for (int e = 0; e < 8; ++e) y[e] = SC == TG_SCALE_ROW ? quotient<KIND>(y[e], scale, inv) : y[e] * inv;
       put_q8(a.Y + row * a.ldy + col, 8, quant8(y, a.y_t));
     }
   }
@@ -460,7 +462,7 @@ __global__ __launch_bounds__(1024) void norm_long(NormArgs a) {
       ep_put8(a.Y, DT, row * a.ldy + col, n, y);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = SC == TG_SCALE_ROW ? quotient(y[e], scale, inv) : y[e] * inv;
+      for (int e = 0; e < 8; ++e) y[e] = SC == TG_SCALE_ROW ? quotient<KIND>(y[e], scale, inv) : y[e] * inv;
       put_q8(a.Y + row * a.ldy + col, n, quant8(y, a.y_t));
     }
   }
