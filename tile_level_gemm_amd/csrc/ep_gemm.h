@@ -63,21 +63,27 @@ __device__ __forceinline__ u32x4 shift_down(u32x4 v, uint32_t bits) {
   return bits < 128 ? v : u32x4{0, 0, 0, 0};
 }
 
+// Where a block's chunk lies in its operand: there, or for a gated block's weights by groups of R of either
+// projection (n: their N).  An argument of the loads, not a member beside their registers: with that the 128-wide fp8
+// blocks spilled 123 registers, reloaded in the K loop on the counter that the operands' loads wait on (4096 x 4096 x
+// 4104 e4m3 262 us, 98 so).
+struct PlainPlace {
+  __device__ __forceinline__ StagedPlace operator()(StagedPlace p) const { return p; }
+};
+template <bool MN, int R>
+struct GatedPlace {
+  int n;
+  __device__ __forceinline__ StagedPlace operator()(StagedPlace p) const { return gated_place<MN>(p, R, n); }
+};
+
 // Fills one operand's LDS stage through registers.  Slot mapping as Operand::load: instruction
 // i of wave w fills the 1 KiB block PER·w + i, lane l its bytes 16l .. 16l+15.
-// R: of a gated block's weights, columns of a group (0: not gated); half: their N.
-template <bool MN, int PER, int DT, int BS, int R = 0>
+template <bool MN, int PER, int DT, int BS>
 struct StagedFetch {
   using EL = Elem<DT>;
   static constexpr int E = EL::kBytes, VE = 16 / E;   // elements per chunk
   u32x4 r[PER];
-  int half = 0;
 
-  __device__ __forceinline__ StagedPlace where(int i, int stage, int wave, int lane) const {
-    const StagedPlace p = in_block(i, stage, wave, lane);
-    if constexpr (R) return gated_place<MN>(p, R, half);
-    else return p;
-  }
   // instruction i's chunk of a stage
   __device__ __forceinline__ static StagedPlace in_block(int i, int stage, int wave, int lane) {
     const uint32_t blk = (uint32_t)(PER * wave + i);
@@ -94,27 +100,31 @@ struct StagedFetch {
   // (M/N-major) from there to the operand's end; kl: k of this part.
   // Every load is 16 whole bytes inside the operand (staged.h), so the loads of all stages are alike, no
   // branch hides how many are in flight, and fix() puts the moved chunks right once they are here.
-  __device__ __forceinline__ void get(const uint8_t* base, int64_t ld, int rows, int kl, int stage, int wave,
+  // place: where a chunk of the block lies in the operand (PlainPlace, or GatedPlace of a gated block's weights).
+  template <class P>
+  __device__ __forceinline__ void get(const P& place, const uint8_t* base, int64_t ld, int rows, int kl, int stage, int wave,
                                       int lane) {
     const int lines = MN ? kl : rows, width = MN ? rows : kl;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      r[i] = load16(base + staged_offset(where(i, stage, wave, lane), ld, lines, width, VE) * E);
+      r[i] = load16(base + staged_offset(place(in_block(i, stage, wave, lane)), ld, lines, width, VE) * E);
   }
   // Moved chunks down to their place, zeros for k past the end.
-  __device__ __forceinline__ void fix(int rows, int kl, int stage, int wave, int lane) {
+  template <class P>
+  __device__ __forceinline__ void fix(const P& place, int rows, int kl, int stage, int wave, int lane) {
     const int width = MN ? rows : kl;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      r[i] = shift_down(r[i], 8u * E * (uint32_t)staged_back<MN>(where(i, stage, wave, lane), kl, width, VE));
+      r[i] = shift_down(r[i], 8u * E * (uint32_t)staged_back<MN>(place(in_block(i, stage, wave, lane)), kl, width, VE));
   }
   // Element by element: lines shorter than 16 bytes.
-  __device__ __forceinline__ void get_each(const uint8_t* base, int64_t ld, int rows, int kl, int stage, int wave,
-                                           int lane) {
+  template <class P>
+  __device__ __forceinline__ void get_each(const P& place, const uint8_t* base, int64_t ld, int rows, int kl, int stage,
+                                           int wave, int lane) {
     const int lines = MN ? kl : rows, width = MN ? rows : kl;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const StagedPlace at = where(i, stage, wave, lane);
+      const StagedPlace at = place(in_block(i, stage, wave, lane));
       const uint8_t* p = base + ((int64_t)at.line * ld + at.first) * E;
       const int n = at.line < lines ? width - at.first : 0;
       u32x4 v = {0, 0, 0, 0};
@@ -700,12 +710,14 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_sta
   constexpr int E = EL::kBytes;
   const uint8_t* pa = g.A + (A_MN ? (int64_t)t.k0 * g.lda + t.m0 : (int64_t)t.m0 * g.lda + t.k0) * E;
   const uint8_t* pb = g.B + (B_MN ? (int64_t)t.k0 * g.ldb + t.n0 : (int64_t)t.n0 * g.ldb + t.k0) * E;
-  const int bw = GATED ? 2 * g.N : g.N;   // rows or columns of B
-  const int ra = g.M - t.m0, rb = bw - t.n0;   // rows / columns from here to the end
+  // rows / columns from here to the end
+  const int ra = g.M - t.m0, rb = GATED ? 2 * g.N - t.n0 : g.N - t.n0;
   const int KT = (t.kl + EL::kBK - 1) / EL::kBK;   // >= 1
   StagedFetch<A_MN, PER, DT, BS> fa[2];
-  StagedFetch<B_MN, PER, DT, BS, GATED ? WN / 2 : 0> fb[2];
-  if constexpr (GATED) fb[0].half = fb[1].half = g.N;
+  StagedFetch<B_MN, PER, DT, BS> fb[2];
+  const PlainPlace in_a;
+  typename std::conditional<GATED, GatedPlace<B_MN, WN / 2>, PlainPlace>::type in_b;
+  if constexpr (GATED) in_b.n = g.N;
   auto compute = [&](const uint8_t* xa, const uint8_t* xb) {
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
@@ -715,11 +727,11 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_sta
     }
   };
   constexpr int VE = 16 / E;
-  if (g.K < VE || (A_MN && g.M < VE) || (B_MN && bw < VE)) {
+  if (g.K < VE || (A_MN && g.M < VE) || (B_MN && (GATED ? 2 * g.N : g.N) < VE)) {
     // one stage after the other
     for (int kt = 0; kt < KT; ++kt) {
-      fa[0].get_each(pa, g.lda, ra, t.kl, kt, wave, lane);
-      fb[0].get_each(pb, g.ldb, rb, t.kl, kt, wave, lane);
+      fa[0].get_each(in_a, pa, g.lda, ra, t.kl, kt, wave, lane);
+      fb[0].get_each(in_b, pb, g.ldb, rb, t.kl, kt, wave, lane);
       __syncthreads();
       fa[0].put(sa0, wave, lane);
       fb[0].put(sb0, wave, lane);
@@ -731,15 +743,15 @@ __global__ __launch_bounds__(ep_threads(BS), BS == 128 ? 4 : 2) void gemm_ep_sta
     // stages past the last load what is not used
     auto get = [&](auto q, int s) {
       constexpr int set = decltype(q)::value;
-      fa[set].get(pa, g.lda, ra, t.kl, s, wave, lane);
-      fb[set].get(pb, g.ldb, rb, t.kl, s, wave, lane);
+      fa[set].get(in_a, pa, g.lda, ra, t.kl, s, wave, lane);
+      fb[set].get(in_b, pb, g.ldb, rb, t.kl, s, wave, lane);
       __builtin_amdgcn_sched_barrier(0);   // on their way before the stage's products
     };
     const bool edge_a = A_MN && ra < BS, edge_b = B_MN && (GATED ? 2 * (g.N - t.n0) : rb) < BS;
     auto put = [&](auto q, int s, uint8_t* xa, uint8_t* xb) {
       constexpr int set = decltype(q)::value;
-      if (edge_a || s + 1 >= KT) fa[set].fix(ra, t.kl, s, wave, lane);
-      if (edge_b || s + 1 >= KT) fb[set].fix(rb, t.kl, s, wave, lane);
+      if (edge_a || s + 1 >= KT) fa[set].fix(in_a, ra, t.kl, s, wave, lane);
+      if (edge_b || s + 1 >= KT) fb[set].fix(in_b, rb, t.kl, s, wave, lane);
       fa[set].put(xa, wave, lane);
       fb[set].put(xb, wave, lane);
     };
