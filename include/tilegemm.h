@@ -767,8 +767,9 @@ int64_t tile_rmsnorm_bwd_workspace(int64_t rows, int64_t cols, int dtype);
  *
  *   bias    device [cols] of w_dtype, or NULL.
  *   mean    device fp32 [rows], or NULL: for the backward pass, as rstd.  The squares are taken about
- *           the mean, in fp32: a row far from zero keeps its variance, deviations above about 2^63
- *           overflow it (rstd 0).
+ *           the mean, in fp32, and mean and squares are corrected by the mean of the deviations: a row far
+ *           from zero, or of one value, keeps its result (Y and rstd are of the mean before it is rounded to
+ *           be stored).  Deviations above about 2^63 overflow the squares (rstd 0).
  * Everything else as for tile_rmsnorm.
  */
 int tile_layernorm(const void* X, const void* R, const void* W, const void* bias, void* H, void* Y, void* S,

@@ -16,8 +16,8 @@
 // barrier; longer ones a workgroup of as many waves as their chunks need (1003 x 2057: 5 waves of one
 // chunk 5.4 us, 4 waves of two 6.2).  The sum of squares and max|H·w| (a row scale needs it:
 // max|Y| = rstd·max|H·w|) travel in one reduction; a row whose max|H·w| is out of fp32's range
-// (top_fits) takes a second one for max|Y| itself.  The layer norm reduces the sum, then the squares about
-// the mean (from registers: rows far from zero keep their variance), then max|Y| if a row scale needs it.
+// (top_fits) takes a second one for max|Y| itself.  The layer norm reduces the sum, then the deviations from
+// the mean and their squares (from registers; centre() has why), then max|Y| if a row scale needs it.
 // Measured: 16384 x 8192 bf16 with residual to e4m3 blocks 163 us (5.8 TB/s of 944 MB); backward of
 // 8192 x 8192 bf16 with dH 100 us and 4 for the sum of dw's shares (5.2 TB/s of 537 MB); one row of
 // 4096 2.9 us, launch and latency.
@@ -176,6 +176,20 @@ __device__ __forceinline__ void row_join(float& s, float& q, float (*red)[2]) {
   }
 }
 
+// The layer norm's centre and variance.  `mean` is the rounded quotient of a rounded sum, off by a few units of itself:
+// in a row far from zero that is much beside its deviations, and in a row of one value it is all there is.  The
+// deviations from it are nearly exact, so their mean (ds/n) says how far it is off, and their mean square less that
+// one's is the variance about the true mean: 8192 fp32 values about 1e4 have Y within 1e-6, with the rounded mean alone
+// 3.5e-4 off.  The reduction of the squares takes both sums (16384 x 8192 bf16 with residual 184 us, 183 without; to
+// e4m3 rows 174, 170; 16384 x 4096 to e4m3 rows 103, 98).  Returns the variance; shift: what the mean lacks (0 where
+// the row is not finite, whose mean and squares say so).
+__device__ __forceinline__ float centre(float ss, float ds, float n, float& shift) {
+  shift = ds / n;
+  shift = fabsf(shift) < __builtin_inff() ? shift : 0.0f;
+  const float v = ss / n;
+  return v < __builtin_inff() ? fmaxf(fmaf(-shift, shift, v), 0.0f) : v;   // NaN and infinity stay
+}
+
 // Whether rstd·max|H·w| is max|Y|: the product with the weight has neither overflowed nor lost bits
 // below the floor of max|Y| (NaN: no).
 __device__ __forceinline__ bool top_fits(float top) { return top >= kAmaxFloor && top < __builtin_inff(); }
@@ -242,7 +256,7 @@ __global__ __launch_bounds__(MAXT) void norm_rows(NormArgs a) {
     rw = load16(a.W + 2 * col);
     if (a.B) rb = load16(a.B + 2 * col);
   }
-  float ss = 0.0f, top = 0.0f, mean = 0.0f, rstd = 1.0f, none = 0.0f;
+  float ss = 0.0f, ds = 0.0f, top = 0.0f, mean = 0.0f, back = 0.0f, rstd = 1.0f, none = 0.0f;
   if constexpr (KIND == kLayer) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -252,7 +266,6 @@ __global__ __launch_bounds__(MAXT) void norm_rows(NormArgs a) {
     }
     row_join<WAVE, Plus, void>(mean, none, red[1]);
     mean /= (float)cols;
-    if (a.mean && t == 0) a.mean[row] = mean;
   }
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -261,18 +274,25 @@ __global__ __launch_bounds__(MAXT) void norm_rows(NormArgs a) {
     for (int e = 0; e < 8; ++e) {
       const float d = KIND == kLayer ? h[j][e] - mean : h[j][e], x = e >= dup ? d : 0.0f;
       if constexpr (KIND != kRows) ss += x * x;
+      if constexpr (KIND == kLayer) ds += x;
       if constexpr (SC == TG_SCALE_ROW && KIND == kRms) top = nan_max(top, fabsf(h[j][e] * w[j][e]));
       if constexpr (SC == TG_SCALE_ROW && KIND == kRows) top = nan_max(top, fabsf(h[j][e]));
     }
   }
   if constexpr (KIND == kRms) row_reduce<WAVE>(ss, top, SC == TG_SCALE_ROW, red[0]);
-  else if constexpr (KIND == kLayer) row_join<WAVE, Plus, void>(ss, none, red[0]);
+  else if constexpr (KIND == kLayer) row_join<WAVE, Plus, Plus>(ss, ds, red[0]);
   else if constexpr (SC == TG_SCALE_ROW) row_join<WAVE, Most, void>(top, none, red[0]);
-  if constexpr (KIND != kRows) rstd = 1.0f / sqrtf(ss / (float)cols + a.eps);
+  if constexpr (KIND == kRms) rstd = 1.0f / sqrtf(ss / (float)cols + a.eps);
+  if constexpr (KIND == kLayer) {
+    float shift;
+    rstd = 1.0f / sqrtf(centre(ss, ds, (float)cols, shift) + a.eps);
+    back = -shift * rstd;
+    if (a.mean && t == 0) a.mean[row] = mean + shift;
+  }
   // The layer norm stores H now (every wave has its loads behind it) and puts Y in its place.  Weight and bias
   // of two chunks come from the caches: held from the start they left a SIMD 5 waves instead of 8, two
-  // workgroups a CU instead of four (16384 x 8192 bf16 with residual to bf16 208 us, now 190, to e4m3 rows
-  // 241, now 187).  One chunk's wait in registers as they are in memory.
+  // workgroups a CU instead of four (16384 x 8192 bf16 with residual to bf16 208 us, late 190, to e4m3 rows
+  // 241, late 187; 184 and 174 with over_wave's reductions).  One chunk's wait in registers as they are in memory.
   if constexpr (KIND == kLayer) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -290,7 +310,7 @@ __global__ __launch_bounds__(MAXT) void norm_rows(NormArgs a) {
         if (a.B) ep_get8(a.B, DT, col, 8, lb);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[j][e] = fmaf((h[j][e] - mean) * rstd, w[j][e], lb[e]);
+      for (int e = 0; e < 8; ++e) h[j][e] = fmaf(fmaf(h[j][e] - mean, rstd, back), w[j][e], lb[e]);
     }
   }
   float scale = 1.0f, inv = 1.0f;   // S and 1/S
@@ -347,7 +367,7 @@ template <int KIND, int DT, int SC>
 __global__ __launch_bounds__(1024) void norm_long(NormArgs a) {
   __shared__ float red[KIND == kLayer ? 3 : 1][16][2];
   const int64_t row = blockIdx.x;
-  float mean = 0.0f, rstd = 1.0f;
+  float mean = 0.0f, back = 0.0f, rstd = 1.0f;
   auto get = [&](int64_t col, int n, float (&h)[8]) {
     ep_get8(a.X, DT, row * a.ldx + col, n, h);
     if (KIND != kRows && a.R) {
@@ -366,7 +386,7 @@ __global__ __launch_bounds__(1024) void norm_long(NormArgs a) {
     if (a.w_t == TG_F32) ep_get8(a.W, TG_F32, col, n, w);
     else ep_get8(a.W, DT, col, n, w);
   };
-  float ss = 0.0f, top = 0.0f, none = 0.0f, h[8];
+  float ss = 0.0f, ds = 0.0f, top = 0.0f, none = 0.0f, h[8];
   // Y of a chunk whose H is in h; elements past the row are 0
   auto values = [&](int64_t col, int n, float (&y)[8]) {
     float w[8], b[8] = {};
@@ -378,7 +398,7 @@ __global__ __launch_bounds__(1024) void norm_long(NormArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if constexpr (KIND == kRms) y[e] = h[e] * rstd * w[e];
-      else if constexpr (KIND == kLayer) y[e] = fmaf((h[e] - mean) * rstd, w[e], b[e]);
+      else if constexpr (KIND == kLayer) y[e] = fmaf(fmaf(h[e] - mean, rstd, back), w[e], b[e]);
       else y[e] = h[e];
   };
   if constexpr (KIND == kLayer) {
@@ -389,7 +409,6 @@ __global__ __launch_bounds__(1024) void norm_long(NormArgs a) {
     }
     row_join<false, Plus, void>(mean, none, red[1]);
     mean /= (float)a.cols;
-    if (a.mean && threadIdx.x == 0) a.mean[row] = mean;
   }
   if constexpr (KIND != kRows || SC == TG_SCALE_ROW) {
     for (int64_t col = (int64_t)threadIdx.x * 8; col < a.cols; col += 8192) {
@@ -401,15 +420,22 @@ __global__ __launch_bounds__(1024) void norm_long(NormArgs a) {
       for (int e = 0; e < 8; ++e) {   // elements past the row are 0
         const float x = KIND == kLayer ? (e < n ? h[e] - mean : 0.0f) : h[e];
         if constexpr (KIND != kRows) ss += x * x;
+        if constexpr (KIND == kLayer) ds += x;
         if constexpr (SC == TG_SCALE_ROW && KIND == kRms) top = nan_max(top, fabsf(h[e] * w[e]));
         if constexpr (SC == TG_SCALE_ROW && KIND == kRows) top = nan_max(top, fabsf(h[e]));
       }
     }
     if constexpr (KIND == kRms) row_reduce<false>(ss, top, SC == TG_SCALE_ROW, red[0]);
-    else if constexpr (KIND == kLayer) row_join<false, Plus, void>(ss, none, red[0]);
+    else if constexpr (KIND == kLayer) row_join<false, Plus, Plus>(ss, ds, red[0]);
     else row_join<false, Most, void>(top, none, red[0]);
   }
-  if constexpr (KIND != kRows) rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
+  if constexpr (KIND == kRms) rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
+  if constexpr (KIND == kLayer) {
+    float shift;
+    rstd = 1.0f / sqrtf(centre(ss, ds, (float)a.cols, shift) + a.eps);
+    back = -shift * rstd;
+    if (a.mean && threadIdx.x == 0) a.mean[row] = mean + shift;
+  }
   float scale = 1.0f, inv = 1.0f;   // S and 1/S
   if constexpr (SC == TG_SCALE_ROW) {
     float amax = KIND == kRms ? top * rstd : top;
