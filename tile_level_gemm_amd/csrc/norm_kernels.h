@@ -52,12 +52,19 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
-__device__ __forceinline__ float q_max(int t) { return t == TG_FP8_E4M3 ? 448.0f : t == TG_I8 ? 127.0f : 57344.0f; }
+// Scale kind of a kernel's result: a tg_scale_kind, and with TG_SCALE_ROW integers apart from fp8.  Told apart by a
+// branch on the type, the integers cost the RMS norm's fp8 rows 1 to 3 % (65536 x 136 bf16 33.1 -> 34.0 us).
+constexpr int kRowInt = TG_SCALE_BLOCK + 1;
+constexpr bool row_scaled(int sc) { return sc == TG_SCALE_ROW || sc == kRowInt; }
 
-// 8 values to 8 bits; |v| <= qmax up to rounding, clamped there; NaN stays NaN, as an integer it is 0
+__device__ __forceinline__ float q_max(int t) { return t == TG_FP8_E4M3 ? 448.0f : 57344.0f; }
+
+// 8 values to 8 bits (SC kRowInt: integers, else fp8 of type t); |v| <= qmax up to rounding, clamped there; NaN stays
+// NaN, as an integer it is 0
+template <int SC>
 __device__ __forceinline__ uint2 quant8(const float (&v)[8], int t) {
-  const float q = q_max(t);
-  if (t == TG_I8) {
+  if constexpr (SC == kRowInt) {
+    const float q = 127.0f;
     // v + 1.5·2^23 rounds v to the nearest integer, ties to even, and holds it in its low byte
     uint32_t b[8];
 #pragma unroll
@@ -68,6 +75,7 @@ __device__ __forceinline__ uint2 quant8(const float (&v)[8], int t) {
     o.y = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[7], b[6], 0x0c0c0400u), __builtin_amdgcn_perm(b[5], b[4], 0x0c0c0400u), 0x05040100u);
     return o;
   }
+  const float q = q_max(t);
   float c[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) c[e] = v[e] != v[e] ? v[e] : fminf(fmaxf(v[e], -q), q);
@@ -196,9 +204,10 @@ __device__ __forceinline__ bool top_fits(float top) { return top >= kAmaxFloor &
 // Row scale of max|Y| >= the floor; NaN for a row with a NaN or an infinity.  For integers the product with
 // 1/127 in fp32, up to two units from the quotient: their codes are rounded to whole numbers by whatever scale
 // is stored, and clamped to 127.
+template <int SC>
 __device__ __forceinline__ float row_scale(float amax, int t) {
   amax = nan_max(amax, kAmaxFloor);
-  const float s = t == TG_I8 ? amax * (1.0f / 127.0f) : amax / q_max(t);
+  const float s = SC == kRowInt ? amax * (1.0f / 127.0f) : amax / q_max(t);
   return amax < __builtin_inff() ? s : __builtin_nanf("");
 }
 // y/s rounded to nearest for inv = 1/s rounded to nearest: Markstein's correction (IBM J. Res. Dev. 34,
@@ -213,7 +222,7 @@ __device__ __forceinline__ float quotient(float y, float s, float inv) {
   return fmaf(KIND == kRms ? fmaf(-q, s, y) : -fmaf(q, s, -y), inv, q);
 }
 
-// SC: tg_scale_kind of the result
+// SC: scale kind of the result
 // WAVE: a wave per row, four rows a workgroup; else a workgroup per row.
 template <int KIND, int DT, int NV, int SC, bool WAVE, int MAXT>
 __global__ __launch_bounds__(MAXT) void norm_rows(NormArgs a) {
@@ -275,13 +284,13 @@ __global__ __launch_bounds__(MAXT) void norm_rows(NormArgs a) {
       const float d = KIND == kLayer ? h[j][e] - mean : h[j][e], x = e >= dup ? d : 0.0f;
       if constexpr (KIND != kRows) ss += x * x;
       if constexpr (KIND == kLayer) ds += x;
-      if constexpr (SC == TG_SCALE_ROW && KIND == kRms) top = nan_max(top, fabsf(h[j][e] * w[j][e]));
-      if constexpr (SC == TG_SCALE_ROW && KIND == kRows) top = nan_max(top, fabsf(h[j][e]));
+      if constexpr (row_scaled(SC) && KIND == kRms) top = nan_max(top, fabsf(h[j][e] * w[j][e]));
+      if constexpr (row_scaled(SC) && KIND == kRows) top = nan_max(top, fabsf(h[j][e]));
     }
   }
-  if constexpr (KIND == kRms) row_reduce<WAVE>(ss, top, SC == TG_SCALE_ROW, red[0]);
+  if constexpr (KIND == kRms) row_reduce<WAVE>(ss, top, row_scaled(SC), red[0]);
   else if constexpr (KIND == kLayer) row_join<WAVE, Plus, Plus>(ss, ds, red[0]);
-  else if constexpr (SC == TG_SCALE_ROW) row_join<WAVE, Most, void>(top, none, red[0]);
+  else if constexpr (row_scaled(SC)) row_join<WAVE, Most, void>(top, none, red[0]);
   if constexpr (KIND == kRms) rstd = 1.0f / sqrtf(ss / (float)cols + a.eps);
   if constexpr (KIND == kLayer) {
     float shift;
@@ -314,7 +323,7 @@ __global__ __launch_bounds__(MAXT) void norm_rows(NormArgs a) {
     }
   }
   float scale = 1.0f, inv = 1.0f;   // S and 1/S
-  if constexpr (SC == TG_SCALE_ROW) {
+  if constexpr (row_scaled(SC)) {
     float amax = KIND == kRms ? top * rstd : top;
     if (KIND == kLayer || (KIND == kRms && !top_fits(top))) {   // the same for all of the row's threads
       amax = 0.0f;
@@ -326,7 +335,7 @@ __global__ __launch_bounds__(MAXT) void norm_rows(NormArgs a) {
       if constexpr (KIND == kLayer) row_join<WAVE, Most, void>(amax, none, red[2]);
       else row_reduce<WAVE>(none, amax, true, red[0]);
     }
-    scale = row_scale(amax, a.y_t);
+    scale = row_scale<SC>(amax, a.y_t);
     inv = 1.0f / scale;
     if (t == 0) ((float*)a.S)[row] = scale;
   }
@@ -355,8 +364,8 @@ __global__ __launch_bounds__(MAXT) void norm_rows(NormArgs a) {
       ep_put8(a.Y, DT, row * a.ldy + col, 8, y);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = SC == TG_SCALE_ROW ? quotient<KIND>(y[e], scale, inv) : y[e] * inv;
-      put_q8(a.Y + row * a.ldy + col, 8, quant8(y, a.y_t));
+      for (int e = 0; e < 8; ++e) y[e] = row_scaled(SC) ? quotient<KIND>(y[e], scale, inv) : y[e] * inv;
+      put_q8(a.Y + row * a.ldy + col, 8, quant8<SC>(y, a.y_t));
     }
   }
 }
@@ -410,22 +419,22 @@ __global__ __launch_bounds__(1024) void norm_long(NormArgs a) {
     row_join<false, Plus, void>(mean, none, red[1]);
     mean /= (float)a.cols;
   }
-  if constexpr (KIND != kRows || SC == TG_SCALE_ROW) {
+  if constexpr (KIND != kRows || row_scaled(SC)) {
     for (int64_t col = (int64_t)threadIdx.x * 8; col < a.cols; col += 8192) {
       const int n = (int)min((int64_t)8, a.cols - col);
       float w[8];
       get(col, n, h);
-      if constexpr (SC == TG_SCALE_ROW && KIND == kRms) weight(col, n, w);
+      if constexpr (row_scaled(SC) && KIND == kRms) weight(col, n, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {   // elements past the row are 0
         const float x = KIND == kLayer ? (e < n ? h[e] - mean : 0.0f) : h[e];
         if constexpr (KIND != kRows) ss += x * x;
         if constexpr (KIND == kLayer) ds += x;
-        if constexpr (SC == TG_SCALE_ROW && KIND == kRms) top = nan_max(top, fabsf(h[e] * w[e]));
-        if constexpr (SC == TG_SCALE_ROW && KIND == kRows) top = nan_max(top, fabsf(h[e]));
+        if constexpr (row_scaled(SC) && KIND == kRms) top = nan_max(top, fabsf(h[e] * w[e]));
+        if constexpr (row_scaled(SC) && KIND == kRows) top = nan_max(top, fabsf(h[e]));
       }
     }
-    if constexpr (KIND == kRms) row_reduce<false>(ss, top, SC == TG_SCALE_ROW, red[0]);
+    if constexpr (KIND == kRms) row_reduce<false>(ss, top, row_scaled(SC), red[0]);
     else if constexpr (KIND == kLayer) row_join<false, Plus, Plus>(ss, ds, red[0]);
     else row_join<false, Most, void>(top, none, red[0]);
   }
@@ -437,7 +446,7 @@ __global__ __launch_bounds__(1024) void norm_long(NormArgs a) {
     if (a.mean && threadIdx.x == 0) a.mean[row] = mean + shift;
   }
   float scale = 1.0f, inv = 1.0f;   // S and 1/S
-  if constexpr (SC == TG_SCALE_ROW) {
+  if constexpr (row_scaled(SC)) {
     float amax = KIND == kRms ? top * rstd : top;
     if (KIND == kLayer || (KIND == kRms && !top_fits(top))) {
       amax = 0.0f;
@@ -456,7 +465,7 @@ __global__ __launch_bounds__(1024) void norm_long(NormArgs a) {
         row_reduce<false>(none, amax, true, red[0]);
       }
     }
-    scale = row_scale(amax, a.y_t);
+    scale = row_scale<SC>(amax, a.y_t);
     inv = 1.0f / scale;
     if (threadIdx.x == 0) ((float*)a.S)[row] = scale;
   }
@@ -488,8 +497,8 @@ __global__ __launch_bounds__(1024) void norm_long(NormArgs a) {
       ep_put8(a.Y, DT, row * a.ldy + col, n, y);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = SC == TG_SCALE_ROW ? quotient<KIND>(y[e], scale, inv) : y[e] * inv;
-      put_q8(a.Y + row * a.ldy + col, n, quant8(y, a.y_t));
+      for (int e = 0; e < 8; ++e) y[e] = row_scaled(SC) ? quotient<KIND>(y[e], scale, inv) : y[e] * inv;
+      put_q8(a.Y + row * a.ldy + col, n, quant8<SC>(y, a.y_t));
     }
   }
 }
@@ -745,7 +754,7 @@ hipError_t go_fwd(const NormArgs& a, hipStream_t s) {
 }
 template <int KIND, int DT>
 hipError_t go_fwd(const NormArgs& a, int sc, hipStream_t s) {
-  if (sc == TG_SCALE_ROW) return go_fwd<KIND, DT, TG_SCALE_ROW>(a, s);
+  if (sc == TG_SCALE_ROW) return a.y_t == TG_I8 ? go_fwd<KIND, DT, kRowInt>(a, s) : go_fwd<KIND, DT, TG_SCALE_ROW>(a, s);
   if (sc == TG_SCALE_BLOCK) return go_fwd<KIND, DT, TG_SCALE_BLOCK>(a, s);
   if constexpr (KIND != kRows) return go_fwd<KIND, DT, TG_SCALE_NONE>(a, s);
   return hipErrorInvalidValue;
