@@ -44,7 +44,7 @@ struct EpArgs {
 struct EpKernel {   // block kernels: block size 64 or 128 (staged, ring), 128 or 256 (direct)
   int bs;
   bool staged, ring;
-  bool fine;   // 256-wide blocks of 16-bit products: the 16-row matrix instructions
+  bool fine = false;   // 256-wide blocks of 16-bit products that are not gated: the 16-row matrix instructions
 };
 hipError_t launch_ep_block(const EpArgs& g, int trans_a, int trans_b, int a_dtype, int b_dtype,
                            const EpKernel& k, hipStream_t s);

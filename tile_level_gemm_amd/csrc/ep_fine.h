@@ -159,7 +159,7 @@ __global__ __launch_bounds__(512, 2) void gemm_ep_fine(EpArgs g) {
   auto meet = [&](auto n) {
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(wait_vm(decltype(n)::value) & ~(15 << 8));
+    __builtin_amdgcn_s_waitcnt(wait_vm(decltype(n)::value));
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);

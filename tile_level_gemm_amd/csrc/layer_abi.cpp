@@ -320,7 +320,7 @@ int run_gated(const EpArgs& g, const tg_ep_plan& p, int transB, int a_dtype, int
     const int st = hip_status("tile_gemm_gated", p.kernel == TG_EP_TOKENS
                                                      ? launch_gated_tokens(g, a_dtype, b_dtype, g.waves, s)
                                                      : launch_gated_block(g, transB, a_dtype, b_dtype,
-                                                                          {p.block_m, p.kernel == TG_EP_STAGED, g.ring != 0, true}, s));
+                                                                          {p.block_m, p.kernel == TG_EP_STAGED, g.ring != 0}, s));
     if (st || g.splits == 1) return st;
   }
   return hip_status("tile_gemm_gated join", launch_ep_join(g, true, s));
