@@ -202,8 +202,11 @@ __device__ __forceinline__ float centre(float ss, float ds, float n, float& shif
 // below the floor of max|Y| (NaN: no).
 __device__ __forceinline__ bool top_fits(float top) { return top >= kAmaxFloor && top < __builtin_inff(); }
 // Row scale of max|Y| >= the floor; NaN for a row with a NaN or an infinity.  For integers the product with
-// 1/127 in fp32, up to two units from the quotient: their codes are rounded to whole numbers by whatever scale
-// is stored, and clamped to 127.
+// 1/127 in fp32, which is what torch computes on the GPU for max / 127: a weight quantised there and one quantised here
+// have the same codes.  By the quotient 4.4 % of 4096 rows of 8192 bf16 values had a scale one unit off, and 30 of the
+// 33.5 million codes differed (half of a row's maximum is 63.5 steps, so the scale's last bit decides it).  The values
+// that the codes stand for are as exact either way, 0.28863 steps off in the mean square: codes are rounded by the
+// scale that is stored.
 template <int SC>
 __device__ __forceinline__ float row_scale(float amax, int t) {
   amax = nan_max(amax, kAmaxFloor);
@@ -528,7 +531,9 @@ template <int KIND, int DT, int NV, bool WAVE, int MAXT>
 __global__ __launch_bounds__(MAXT) void norm_bwd(NormBwdArgs a) {
   constexpr bool LAYER = KIND == kLayer;
   constexpr int RPB = WAVE ? 4 : 1;
-  // 1024 threads leave 128 registers: two fp32 rows, or two rows and both sums, do not fit
+  // 1024 threads leave 128 registers: two fp32 rows, or two rows and both sums, do not fit.  Nor does all of one row of
+  // the layer norm beside its weights and both sums: 22 registers are spilled there (fp32 29; RMS norm in 16 bits, two
+  // rows, 11).  Rows of 8193 to 16384 columns alone: 4096 x 16384 bf16 120 us (3.4 TB/s), 8192 x 8192 97 (4.2).
   constexpr bool AHEAD = !((DT == TG_F32 || LAYER) && MAXT == 1024);
   __shared__ float red[2][WAVE ? 1 : kMaxWaves][2];
   const int TPR = WAVE ? 64 : (int)blockDim.x;
