@@ -710,7 +710,8 @@ int64_t tile_gemm_gated_bwd_workspace(int64_t M, int64_t N, int64_t K, int trans
 
 typedef enum tg_scale_kind {
   TG_SCALE_NONE = 0,   /* Y in X's dtype */
-  TG_SCALE_ROW = 1,    /* Y in 8 bits, fp32 S[row] = max|Y[row]|/qmax (integers: max|Y|·(1/127)):
+  TG_SCALE_ROW = 1,    /* Y in 8 bits, fp32 S[row] = max|Y[row]|/qmax (integers: max|Y|·(1/127),
+                          as torch computes max / 127 on the GPU):
                           tile_gemm_ep's row_scale (of weight rows: its col_scale) */
   TG_SCALE_BLOCK = 2   /* Y in 8 bits, E8M0 bytes S[row][col/32]: the smallest power of two with
                           max|Y of the 32 columns|/S <= qmax: tile_gemm_mx's SA */

@@ -21,10 +21,13 @@
 // out in two bursts of half a stage, A's have two stages' time to arrive, and the wait at the barrier leaves
 // A's latest in flight.
 //
-// Measured, 8192 x 16384 x 4096 bf16, all back to back on one card: gemm_ep_direct 800 us (K loop 753), this with
-// two stages of both 748 (697), with three of A 735 (685), the vendor library's product 681.  The epilogue is
-// what is left: as a gated product with Z (402 MB of results) 770 us in waves of 64 x 128, 795 in waves of
-// 128 x 64, whose lines of D are halves.  Results straight from the registers, and a workgroup a CU that loads
+// Measured on random operands, each line in one run on one card (cards differ by 6 %), us: all of it, the K loop
+// alone, the K loop that multiplies its first stages again and again without loading others:
+//   8192 x 16384 x 4096 bf16: this 781, 717, 613; gemm_ep_direct 823, 766, 672; the vendor library's product 726
+//   8192 x 8192 x 4096 int8:  this 225, 185, 158; gemm_ep_direct 245, 205, 180; the library's 250
+// Two stages of A instead of three, on another card: 748 for 735.  The epilogue is what is left: as a gated product
+// with Z (402 MB of results), on that card too, 770 us in waves of 64 x 128, 795 in waves of 128 x 64, whose lines of
+// D are halves.  Results straight from the registers, and a workgroup a CU that loads
 // the next block's first stages before it stores, both spilled and were slower.
 //
 // Internal header, on top of ep_gemm.h.

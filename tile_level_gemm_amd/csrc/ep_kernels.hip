@@ -126,9 +126,12 @@ __global__ __launch_bounds__(8 * RL) void act_grad(ActGradArgs a) {
 }
 
 // The same for D = act(G)·U: dY, G and U are read and dG = dY·U·act'(G), dU = dY·act(G) written by one
-// thread, with the column sums of both.  Bound by memory, 4096 x 4096 (168 MB) 36 us with one row a thread in
+// thread, with the column sums of both.  dZ is rounded to 16 bits here, once, as act_grad's is: the matrix
+// instructions of both products take 16 bits, and an fp32 dZ would be two operands and twice the products.  Beside
+// products of an fp32 dZ that moves dA and dB by 2.6e-3 in the 2-norm in bf16 (3.3e-4 in fp16), 1.4 times the error
+// that their own rounding leaves; the sums for dbias are of the fp32 values.  Bound by memory, 4096 x 4096 (168 MB) 36 us with one row a thread in
 // flight (two 38, four 43: registers, 107 of them with one, cost more waves than rows in flight give); small
-// problems by latency, 200 x 264 6.6 us with 1024 threads (512 with two rows 8.1).
+// problems by latency, 200 x 264 7.0 us a call with 1024 threads (512 with two rows 8.1 where this was 6.6).
 template <int RL, int K, bool SCALED>
 __global__ __launch_bounds__(8 * RL) void gated_grad(ActGradArgs a) {
   __shared__ float red[RL][128 + 1];

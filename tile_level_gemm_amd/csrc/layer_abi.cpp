@@ -107,7 +107,7 @@ EpChoice choose_ep(int64_t M, int64_t N, int64_t K, int transB, int eb, bool dir
   // blocks 9.3); 17 to 32 rows of 16 bits read A twice over (24 x 4096 x 4096 13.2 us, blocks 11.1;
   // 32 x 1024 x 1024 5.4, blocks 6.0; fp8 32 x 8192 x 4096 11.6, blocks 12.9).
   const bool blocks_win = direct && (!transB ? N * K > (int64_t)1 << 23 : M > 16 && eb == 2 && N * K > (int64_t)1 << 22);
-  // gated weights [K][2N]: blocks alone
+  // gated weights [K][2N]: blocks alone (1 x 2·8192 x 4096 bf16 36 us, [2N][K] here 30; 32 rows 39, 31)
   if (M <= kTokenRows && !blocks_win && (transB || !gated)) {
     c.kernel = TG_EP_TOKENS;
     if (transB) {
@@ -131,7 +131,9 @@ EpChoice choose_ep(int64_t M, int64_t N, int64_t K, int transB, int eb, bool dir
     return c;
   }
   auto blocks = [&](int64_t b) { return ((M + b - 1) / b) * ((N + b - 1) / b); };
-  // Times below: bf16, MI355X, M x N x K.
+  // Times below: bf16, MI355X, M x N x K.  Gated products and products of integers go by the same bounds, by the columns
+  // of B and the bytes of K; theirs were not swept (gated bf16 of 2·8192 x 4096 weights, us: 128 rows 45, 512 rows 80,
+  // 2048 rows 203).
   const int64_t bk = 128 / eb, steps = (K + bk - 1) / bk;
   c.kernel = direct ? TG_EP_DIRECT : TG_EP_STAGED;
   int64_t s = 1;   // parts of K
@@ -337,7 +339,9 @@ int64_t bias_groups(int64_t M, int64_t N) {
 // Workgroups of the norm's backward pass, each with a row (four short rows) at least.  More of them
 // keep more rows in flight but write and add more shares of dW: 16384 x 4096 bf16 103 us with 512
 // (256: 118, 1024: 107), 8192 x 8192 104 us with 256 (512: 109).
-// The layer norm's shares are twice as long: 512 only from 2048 rows on (1003 x 2057 f16 256: 15.0, 512: 15.8).
+// The layer norm's shares are twice as long: 512 only from 2048 rows on (bf16, us a call with 256 and with 512: 1003 x
+// 4096 14.9, 17.4; 1500 x 2048 13.6, 13.7; 2000 x 4096 18.8, 19.2; 2048 x 2048 15.9, 14.1; 4096 x 2048 24.0, 18.9;
+// 16384 x 4096 103, 82).
 int64_t norm_groups(NormKind kind, int64_t rows, int64_t cols) {
   const int64_t per = cols <= 1024 && norm_in_registers(cols) ? 4 : 1;
   const int64_t most = cols <= 4096 && (kind == kRms || rows >= 2048) ? 512 : 256;
